@@ -12,6 +12,12 @@ dropless MoE layer (route -> permute+pad -> topology -> SDD(+act) -> DSD ->
 combine, and the reverse), following section 1 of George Lin's blog post on
 MoE training (MegaBlocks).  PyTorch only allocates device memory and
 provides the stream.
+
+Beside the layer stand the other operators of a training step:
+``add_rms_norm`` (residual addition and root-mean-square norm, with its
+backward and rows in 8 bits), ``linear_cross_entropy`` (vocabulary head,
+softmax cross entropy and both gradients without the logits in memory) and
+``clip_grad_norm`` (global norm of a ``GradList`` and its clipping).
 """
 
 from __future__ import annotations
@@ -27,6 +33,8 @@ __all__ = [
     "Topology",
     "route_topk", "route_topk_backward", "permute_pad", "permute_pad_workspace_size", "build_topology", "dispatch", "sdd", "dsd", "dsd_t",
     "dstd", "unpermute_combine", "combine_backward", "DMoELayer", "StepRunner",
+    "add_rms_norm", "add_rms_norm_backward", "add_rms_norm_backward_workspace_size", "linear_cross_entropy",
+    "linear_cross_entropy_workspace_size", "GradList", "clip_grad_norm",
     "EPI_STORE", "EPI_GELU_FWD", "EPI_SWIGLU_FWD", "EPI_GELU_BWD", "EPI_SWIGLU_BWD", "BLOCK",
 ]
 
@@ -56,6 +64,7 @@ _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIGS = {
     "dmoe_version": (ctypes.c_char_p, []),
     "dmoe_status_string": (ctypes.c_char_p, [_I]),
@@ -83,6 +92,15 @@ _SIGS = {
     "dmoe_dstd": (_I, [ctypes.POINTER(_Topo), _P, _P, _I, _I, _P, _P]),
     "dmoe_unpermute_combine": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P]),
     "dmoe_combine_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "dmoe_add_rms_norm": (_I, [_P, _L, _P, _L, _P, _I, ctypes.c_float, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "dmoe_add_rms_norm_backward_workspace_size": (ctypes.c_size_t, [_I, _I]),
+    "dmoe_add_rms_norm_backward": (_I, [_P, _L, _P, _P, _I, _P, _P, _L, _I, _I, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dmoe_linear_cross_entropy_workspace_size": (ctypes.c_size_t, [_I] * 6),
+    "dmoe_linear_cross_entropy": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P,
+                                       ctypes.c_size_t, _P]),
+    "dmoe_grad_chunks": (_L, [_P, _L, _I]),
+    "dmoe_clip_grad_norm_workspace_size": (ctypes.c_size_t, []),
+    "dmoe_clip_grad_norm": (_I, [_P, _I, _L, ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
 }
 
 
@@ -395,6 +413,157 @@ def combine_backward(dy, y_perm, src_of_row, gate_w, P_dev, k: int, P_max: int, 
     _check("dmoe_combine_backward", lib().dmoe_combine_backward(
         _ptr(dy), _ptr(y_perm), _ptr(src_of_row), _ptr(gate_w), _ptr(P_dev), T, d, k, P_max, _ptr(dy_perm),
         _ptr(d_gate), _stream(stream)))
+
+
+# --------------------------------------- beside the layer in a training step
+
+def _rows(t, dtype, name, T, d):
+    """Row pitch of a [T, d] tensor whose rows may lie apart."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != d:
+        raise ValueError(f"{name} must have shape {(T, d)}, got {tuple(t.shape)}")
+    if T <= 1 and d > 0 and (d == 1 or t.stride(1) == 1):
+        return d
+    if t.stride(1) != 1 or t.stride(0) < d or t.stride(0) % 8:
+        raise ValueError(f"{name} must have contiguous rows a multiple of 8 elements apart")
+    return t.stride(0)
+
+
+def _norm_weight(weight, d):
+    if weight is None or weight.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("weight must be torch.bfloat16 or torch.float32")
+    _need(weight, weight.dtype, "weight", shape=(d,))
+    return int(weight.dtype == torch.float32)
+
+
+def add_rms_norm(x, residual, weight, eps: float, h, y, rstd=None, q=None, q_scale=None, stream=None):
+    """h = x + residual (kept in bf16), y = h / rms(h) * weight; with ``q``
+    (float8_e4m3fn [T, d]) and ``q_scale`` (fp32 [T, ceil(d / 128)]) also, or
+    with ``y=None`` only, y in 8 bits with one scale per row and 128 columns.
+    ``residual=None`` norms x itself (``h`` may then be None).  ``x`` and
+    ``residual`` may be row slices of wider tensors; ``h`` may be ``x`` or
+    ``residual`` and ``y`` may be ``x``.  ``rstd`` (fp32 [T]) is what the
+    backward reads."""
+    T, d = x.shape
+    ldx = _rows(x, torch.bfloat16, "x", T, d)
+    ldr = 0 if residual is None else _rows(residual, torch.bfloat16, "residual", T, d)
+    wf = _norm_weight(weight, d)
+    if residual is not None or h is not None:
+        _need(h, torch.bfloat16, "h", shape=(T, d))
+    if y is not None:
+        _need(y, torch.bfloat16, "y", shape=(T, d))
+    if rstd is not None:
+        _need(rstd, torch.float32, "rstd", shape=(T,))
+    if q is not None:
+        _need(q, torch.float8_e4m3fn, "q", shape=(T, d))
+        _need(q_scale, torch.float32, "q_scale", shape=(T, (d + 127) // 128))
+    _check("dmoe_add_rms_norm", lib().dmoe_add_rms_norm(
+        _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), wf, eps, T, d, _ptr(h), _ptr(y), _ptr(rstd), _ptr(q),
+        _ptr(q_scale), _stream(stream)))
+
+
+def add_rms_norm_backward_workspace_size(T: int, d: int) -> int:
+    return int(lib().dmoe_add_rms_norm_backward_workspace_size(T, d))
+
+
+def add_rms_norm_backward(dy, h, weight, rstd, dx, dweight, ws, dh=None, stream=None):
+    """Gradient of ``add_rms_norm``: dx (of x and residual alike, with the
+    residual stream's own gradient ``dh`` added) and dweight (fp32 [d],
+    written; None: not computed, ``ws`` may be None too)."""
+    T, d = dy.shape
+    lddy = _rows(dy, torch.bfloat16, "dy", T, d)
+    _need(h, torch.bfloat16, "h", shape=(T, d))
+    wf = _norm_weight(weight, d)
+    _need(rstd, torch.float32, "rstd", shape=(T,))
+    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", T, d)
+    _need(dx, torch.bfloat16, "dx", shape=(T, d))
+    nws = 0
+    if dweight is not None:
+        _need(dweight, torch.float32, "dweight", shape=(d,))
+        nws = _need(ws, torch.uint8, "ws").numel()
+    _check("dmoe_add_rms_norm_backward", lib().dmoe_add_rms_norm_backward(
+        _ptr(dy), lddy, _ptr(h), _ptr(weight), wf, _ptr(rstd), _ptr(dh), lddh, T, d, _ptr(dx), _ptr(dweight),
+        _ptr(ws), nws, _stream(stream)))
+
+
+def linear_cross_entropy_workspace_size(T: int, d: int, V: int, grad: bool = True, dw_dtype=torch.bfloat16,
+                                        piece: int = 0) -> int:
+    return int(lib().dmoe_linear_cross_entropy_workspace_size(T, d, V, int(bool(grad)),
+                                                              int(dw_dtype == torch.float32), piece))
+
+
+def linear_cross_entropy(x, w, targets, loss, lse, ws, dx=None, dw=None, d_loss=None, ignore_index: int = -100,
+                         accumulate: bool = False, piece: int = 0, stream=None):
+    """Per-token softmax cross entropy of the head's logits x . w^T (w [V, d])
+    without the logits in memory, and with ``dx`` and / or ``dw`` the
+    gradients: of the mean loss over the targets that count, or of
+    sum(d_loss * loss) when ``d_loss`` [T] is given.  ``dw`` is bf16 or fp32
+    (``accumulate`` adds to an fp32 one).  ``piece`` bounds the workspace: the
+    tokens whose [piece, V] array exists at one time (0: 8192)."""
+    T, d = x.shape
+    V = w.shape[0]
+    _need(x, torch.bfloat16, "x")
+    _need(w, torch.bfloat16, "w", shape=(V, d))
+    _need(targets, torch.int32, "targets", shape=(T,))
+    _need(loss, torch.float32, "loss", shape=(T,))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", shape=(T,))
+    _need(ws, torch.uint8, "ws")
+    if d_loss is not None:
+        _need(d_loss, torch.float32, "d_loss", shape=(T,))
+    if dx is not None:
+        _need(dx, torch.bfloat16, "dx", shape=(T, d))
+    f32 = 0
+    if dw is not None:
+        if dw.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"dw must be torch.bfloat16 or torch.float32, got {dw.dtype}")
+        f32 = int(dw.dtype == torch.float32)
+        _need(dw, dw.dtype, "dw", shape=(V, d))
+    _check("dmoe_linear_cross_entropy", lib().dmoe_linear_cross_entropy(
+        _ptr(x), _ptr(w), _ptr(targets), T, d, V, ignore_index, _ptr(d_loss), _ptr(loss), _ptr(lse), _ptr(dx),
+        _ptr(dw), f32, int(bool(accumulate)), piece, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+class GradList:
+    """A list of gradients (bf16 or fp32, contiguous, any sizes and places) as
+    the device table that ``clip_grad_norm`` walks, with its scratch.  ``outs``
+    (same types and sizes) receive the clipped gradients; without them the
+    gradients are clipped in place.  The list keeps its tensors."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outputs")
+        rows, self.chunks = [], 0
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"gradient {i} must be torch.bfloat16 or torch.float32, got {g.dtype}")
+            _need(g, g.dtype, f"gradient {i}")
+            _need(o, g.dtype, f"output {i}", shape=g.shape)
+            f32 = int(g.dtype == torch.float32)
+            rows.append([g.data_ptr(), o.data_ptr(), g.numel(), self.chunks, f32])
+            self.chunks += int(lib().dmoe_grad_chunks(g.data_ptr(), g.numel(), f32))
+        device = self.grads[0].device if self.grads else "cuda"
+        self.table = torch.tensor(rows or [[0] * 5], dtype=torch.int64).to(device)
+        self.ws = torch.empty(int(lib().dmoe_clip_grad_norm_workspace_size()), dtype=torch.uint8, device=device)
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def clip_grad_norm(grads: GradList, max_norm: float, norm, eps: float = 1e-6, stream=None):
+    """norm (fp32 [1], written) = the global 2-norm of all gradients; every one
+    is scaled by min(1, max_norm / (norm + eps)) into its output."""
+    _need(norm, torch.float32, "norm", numel=1)
+    _check("dmoe_clip_grad_norm", lib().dmoe_clip_grad_norm(
+        _ptr(grads.table), len(grads), grads.chunks, max_norm, eps, _ptr(norm), _ptr(grads.ws), grads.ws.numel(),
+        _stream(stream)))
 
 
 # ----------------------------------------------------------------- whole layer

@@ -73,6 +73,7 @@ typedef enum dmoe_status {
 #define DMOE_SITE_COMBINE_INDEX (4 << 8)
 #define DMOE_SITE_ROUTE_INDEX (5 << 8)
 #define DMOE_SITE_SELFTEST (6 << 8)
+#define DMOE_SITE_LOSS_TARGET (7 << 8)
 
 /* Block-sparse topology (section 1.3, hybrid BCSR-COO + transpose index).
  * Plain device arrays, all int32, owned by the caller; filled by
@@ -472,6 +473,117 @@ dmoe_status dmoe_combine_backward(const uint16_t* dy, const uint16_t* y_perm,
                                   const int32_t* src_of_row, const float* gate_w,
                                   const int32_t* P_dev, int T, int d, int k, int P_max,
                                   uint16_t* dy_perm, float* d_gate, dmoe_stream_t stream);
+
+/* ============================================================================
+ * Operators that stand beside the layer in a training step: the norm that
+ * feeds it, the vocabulary head with its loss, and the clipping of the
+ * gradients.  The page has no counterpart to them. */
+
+/* ------------------------------------------ residual addition + RMS norm */
+
+/* For every row t of T:
+ *   h[t]    = bf16(x[t] + residual[t])        (h = x when residual is NULL)
+ *   r       = 1 / sqrt(mean_c h[t, c]^2 + eps)
+ *   n[t, c] = h[t, c] * r * weight[c]          (fp32)
+ * The stream is kept in bf16 and the norm reads the kept value, which is all
+ * the backward has.  Outputs (each may be NULL unless stated):
+ *   h       [T, d] bf16; required with a residual; may be x or residual
+ *   y       [T, d] bf16: n rounded; may be x
+ *   rstd    [T] fp32: r, what the backward reads
+ *   q       [T, d] e4m3 and q_scale [T, ceil(d / 128)] fp32 (both or
+ *           neither): n in 8 bits; 128 columns g share the scale
+ *           s = max |n[t, g]| / 448 (at least the smallest normal number; 1
+ *           for a group of zeros), q = e4m3(n / s), so n ~ q * s
+ * One of y and q is required.  x and residual may have rows ldx, ldr
+ * elements apart (at least d, multiples of 8); weight is bf16, or fp32 when
+ * weight_f32 != 0.  d a multiple of 8, 8 <= d <= 32768; eps >= 0. */
+dmoe_status dmoe_add_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
+                              const void* weight, int weight_f32, float eps, int T, int d, uint16_t* h,
+                              uint16_t* y, float* rstd, uint8_t* q, float* q_scale, dmoe_stream_t stream);
+
+/* Bytes of scratch dmoe_add_rms_norm_backward needs on the current device
+ * for its dw. */
+size_t dmoe_add_rms_norm_backward_workspace_size(int T, int d);
+
+/* Backward of dmoe_add_rms_norm: with u = dy * weight,
+ *   dx[t, c] = dh[t, c] + rstd[t] * (u - h[t, c] * rstd[t]^2 * mean_c(u h))
+ *   dw[c]    = sum_t dy[t, c] * h[t, c] * rstd[t]
+ * dx is the gradient of x and of residual alike.  dh [T, d] (may be NULL) is
+ * the gradient that arrives at h from the residual stream.  dy and dh may
+ * have rows lddy, lddh elements apart (at least d, multiples of 8); dx
+ * [T, d] bf16 may be dy or dh.  dw [d] fp32 may be NULL (then ws too); it is
+ * written, not added to, and summed in a fixed order.  T == 0 writes dw = 0.
+ * Calls sharing a ws must not overlap. */
+dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, const void* weight,
+                                       int weight_f32, const float* rstd, const uint16_t* dh, int64_t lddh, int T,
+                                       int d, uint16_t* dx, float* dw, void* ws, size_t ws_bytes,
+                                       dmoe_stream_t stream);
+
+/* ------------------------------------ vocabulary head + softmax cross entropy */
+
+/* Bytes of scratch dmoe_linear_cross_entropy needs: with gradients (grad != 0)
+ * about 2 * piece * V, and 4 * V * d more when T > piece and dw is bf16
+ * (dw_f32 == 0).  piece: tokens per piece (0: 8192), rounded up to a multiple
+ * of 256; at most 262144. */
+size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, int dw_f32, int piece);
+
+/* Logits l[t, v] = <x[t], w[v]> (bf16 products, fp32 sums on the tensor
+ * cores), never stored; for every token t:
+ *   lse[t]  = log sum_v exp(l[t, v])
+ *   loss[t] = lse[t] - l[t, targets[t]], or 0 where targets[t] == ignore_index
+ * and, with G[t, v] = g[t] * (exp(l[t, v] - lse[t]) - [v == targets[t]])
+ * rounded to bf16,
+ *   dx = G w,  dw = G^T x                       (each may be NULL)
+ * where g[t] = d_loss[t], or 1 / (number of targets that count) when d_loss
+ * is NULL (the mean loss), and 0 where targets[t] == ignore_index.
+ *   x [T, d] bf16, w [V, d] bf16, targets [T] int32 (read)
+ *   loss [T] fp32, lse [T] fp32 (may be NULL), dx [T, d] bf16,
+ *   dw [V, d] bf16, or fp32 when dw_f32 != 0 (written; with accumulate != 0,
+ *   fp32 only, added to what dw holds)
+ *   ws: scratch of dmoe_linear_cross_entropy_workspace_size() bytes, 256-byte
+ *   aligned; calls sharing one must not overlap.
+ * A target outside [0, V) other than ignore_index counts as ignored and sets
+ * DMOE_SITE_LOSS_TARGET | DMOE_ERR_DEVICE.  When no target counts, the losses
+ * and gradients are zero.  d a multiple of 8; 1 <= V <= 2^24; T == 0 writes
+ * only dw = 0 (unless accumulating). */
+dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, const int32_t* targets, int T, int d,
+                                      int V, int ignore_index, const float* d_loss, float* loss, float* lse,
+                                      uint16_t* dx, void* dw, int dw_f32, int accumulate, int piece, void* ws,
+                                      size_t ws_bytes, dmoe_stream_t stream);
+
+/* ------------------------------------------- global gradient norm + clipping */
+
+/* Elements per chunk of the gradients' walk. */
+#define DMOE_GRAD_CHUNK 8192
+
+/* One tensor of a list of gradients: n contiguous elements, bf16, or fp32
+ * when f32 != 0; out may be in.  first_chunk: the sum of dmoe_grad_chunks()
+ * over the tensors before this one. */
+typedef struct dmoe_grad {
+  const void* in;
+  void* out;
+  int64_t n;
+  int64_t first_chunk;
+  int64_t f32;
+} dmoe_grad;
+
+/* Chunks of a tensor (they are counted from its address rounded down to 16
+ * bytes).  Host-only, no CUDA call. */
+int64_t dmoe_grad_chunks(const void* in, int64_t n, int f32);
+
+/* Bytes of scratch of dmoe_clip_grad_norm. */
+size_t dmoe_clip_grad_norm_workspace_size(void);
+
+/* norm = sqrt(sum over all tensors of the squares of their elements);
+ * c = min(1, max_norm / (norm + eps)); out = c * in for every tensor (a
+ * tensor with out == in is left alone when c is 1).  A norm that is not
+ * finite is not replaced: an infinite one gives c = 0, NaN reaches every
+ * output.  grads [n] is a DEVICE array, chunks the total of its tensors'
+ * chunks; elements must be aligned to their size; norm [1] fp32 (device,
+ * written).  The sums run in a fixed order (squares in fp32, their sums of
+ * chunks and blocks in fp64).  Calls sharing a ws must not overlap. */
+dmoe_status dmoe_clip_grad_norm(const dmoe_grad* grads, int n, int64_t chunks, float max_norm, float eps, float* norm,
+                                void* ws, size_t ws_bytes, dmoe_stream_t stream);
 
 #ifdef __cplusplus
 }
