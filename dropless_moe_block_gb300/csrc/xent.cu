@@ -5,29 +5,49 @@
 //   loss_t = lse_t - l_t,target
 //   G_tv = g_t (exp(l_tv - lse_t) - [v = target_t]),  dx = G W,  dW = G^T x
 //
-// Tokens go in pieces.  A piece's launches:
-//   1 logits   P = x W^T on the tensor cores; the epilogue turns a tile's
-//              accumulators into exp(l - ref) and, for each row and 128
-//              columns, leaves the pair (ref, sum of exp(l - ref)).  With
-//              gradients the exponentials go to a [piece, V] bf16 array, the
-//              only thing of that size that ever exists; without, nothing is
-//              written.
-//   2 rows     the pairs of a row meet in lse_t; loss_t; the factor g_t
-//   3 scale    the piece's array becomes G in place
-//   4 dx, dW   two products with G
+// With a reference r_t of each row, E_tv = exp(l_tv - r_t) for v other than
+// the target and 0 at the target, s_t = g_t exp(r_t - lse_t) and
+// c_t = g_t (exp(-loss_t) - 1):
 //
-// ref is 0 while a row's 128 logits stay within +-kRefLimit, else their
-// maximum: exp(l) of a moderate logit needs no maximum subtracted in fp32
-// or bf16 (both reach 3e38), so in the usual case every pair of a row has
-// the same reference.  What bf16 costs here is one rounding of G (2^-9 of
-// an element), the rounding a bf16 gradient of the logits has anyway.
+//   dx_t = s_t (E W)_t + c_t W_target        dW_v = (E^T (s x))_v + sum c_t x_t
+//                                                   over the tokens whose target is v
+//
+// so the products need only the unnormalised exponentials, which the logits'
+// product can leave behind before lse is known, and the target's element,
+// the large one, never passes through 16 bits: it is added in fp32.
+//
+// Tokens go in pieces.  A piece's launches:
+//   1 sort     tokens ordered by target (with gradients)
+//   2 logits   x W^T on the tensor cores; the epilogue turns a tile's
+//              accumulators into E and, for each row and 128 columns, leaves
+//              the pair (ref, sum of exp(l - ref)).  With gradients E goes to a
+//              [piece, V] bf16 array, the only thing of that size that ever
+//              exists; without, nothing is written.
+//   3 rows     the pairs of a row meet in lse_t; loss_t, s_t, c_t, s_t x_t
+//   4 targets  sums of c_t x_t, 32 tokens each, for words with many tokens
+//   5 grads    the tiles of both products in one launch
+//
+// ref is 0 while the largest of a row's 128 logits lies in [kRefLow,
+// kRefHigh], else that maximum: exp of a moderate logit needs no maximum
+// subtracted, fp32 and bf16 reach from 1e-38 to 3e38, so in the usual case
+// every pair of a row has the reference 0 and E needs no second pass.  A row
+// whose groups disagree is brought to its largest reference by launch 3.
+// What bf16 costs is one rounding of E and one of s x (2^-8 of an element
+// at most, independent from element to element).
+//
+// The tensor cores truncate where they add a product to an accumulator: a
+// logit over d columns comes out about (d / 16) 2^-26 of itself too small
+// (measured, d = 512 to 8192: 1.3e-8 to 1.6e-8 per 16 columns).  The
+// epilogue gives that mean back; without it the loss is 1.3e-6 off at d =
+// 4096.
 //
 // The products are bound by the tensor cores (2 T V d flops each).  They run
-// as persistent CTA pairs (tcgen05 cta_group::2): M = 256 x N = 256 NS tiles,
-// a ring of TMA-filled K slices of 64, accumulators in TMEM.  Roles per CTA:
-// warp 0 TMA producer, warp 1 TMEM allocator and (rank 0) MMA issuer, warps
-// 2-9 epilogue.  Every ragged edge is the tensor maps': what lies past a
-// matrix reads as zero, and the epilogue stores nothing there.
+// as persistent CTA pairs (tcgen05 cta_group::2): M = 256 x N = 512 tiles (two
+// sub-tiles of N = 256 that share each K slice's A), a ring of TMA-filled K
+// slices of 64, accumulators in TMEM.  Roles per CTA: warp 0 TMA producer,
+// warp 1 TMEM allocator and (rank 0) MMA issuer, warps 2-9 epilogue.  Every
+// ragged edge is the tensor maps': what lies past a matrix reads as zero,
+// and the epilogue stores nothing there.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -55,12 +75,19 @@ constexpr uint32_t SLAB = 32 * 32 * 2;
 constexpr uint32_t SLAB_BYTES = kEpiWarps * 2 * SLAB;
 constexpr size_t kSmemMax = 232448;
 constexpr int kGroup = 128;          // columns that share a (ref, sum) pair
-constexpr float kRefLimit = 60.f;
+// Above: 2^24 exponentials of kRefHigh, times any sensible weights, stay far
+// below 3e38.  Below: what is 27 under kRefLow, 2e-12 of its group's largest
+// exponential, reaches the denormals.
+constexpr float kRefHigh = 40.f, kRefLow = -60.f;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kTruncation = 1.f / 67108864.f;  // 2^-26 of the sum per 16 products
 constexpr int kPieceDefault = 8192;  // tokens per piece when the caller names none
 constexpr int kPieceMax = 1 << 18;
 
-enum Job : int { JOB_LOGITS = 0, JOB_DX = 1, JOB_DW = 2 };
+constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
+constexpr int kMaxSplit = 16;
+constexpr int kRun = 32;             // tokens of one word per partial sum of launch 4
+constexpr int kDirect = 4;           // words with up to so many tokens are summed by dW's epilogue itself
 
 template <int NS>
 struct PlanX {
@@ -71,22 +98,45 @@ struct PlanX {
   static_assert(STAGES >= 4 && SMEM <= kSmemMax, "shared-memory plan");
 };
 
+// A grid of M x N tiles over K, cut into `parts` ranges of K slices.
+struct Grid {
+  int mt, nt;   // pair-tile rows, tile columns
+  int raster;   // pair-tile rows per raster group
+  int slices;   // K slices of 64
+  int parts;
+  int items;    // mt * nt * parts
+};
+
 struct ParamsX {
-  CUtensorMap map_a;
-  CUtensorMap map_b;
-  int M, N, K;       // product sizes
-  int mt, nt;        // pair-tile rows, tile columns
-  int raster;        // pair-tile rows per raster group
-  uint16_t* out;     // bf16 result (dx, dW) or the exponentials
-  float* out32;      // fp32 result (dW), instead of out
-  const float* add;  // fp32 partial result added to the accumulators, or NULL
-  int64_t ldo;       // row pitch of out / out32 / add
-  // JOB_LOGITS
+  CUtensorMap map_a;   // logits: x K-major;  gradients: E K-major (dx)
+  CUtensorMap map_b;   // logits: W K-major;  gradients: W MN-major (dx)
+  CUtensorMap map_a2;  // gradients: E MN-major (dW)
+  CUtensorMap map_b2;  // gradients: s x MN-major (dW)
+  int n, d, V;         // tokens of the piece, columns, vocabulary
+  int first_dx;        // gradients: grid[0] is dx's (else dW's)
+  int extra;           // gradients: see item_of()
+  Grid grid[2];        // logits: one grid;  gradients: the longer items first
   const int32_t* targets;
-  float2* pairs;     // [N / 128][ldp] (ref, sum)
+  int32_t* err;
+  // logits
+  uint16_t* E;         // [n][ldv] exponentials (NULL: the loss alone)
+  int64_t ldv;
+  float2* pairs;       // [V / 128][ldp] (ref, sum)
   int64_t ldp;
   float* target_logit;
-  int32_t* err;
+  float unbias;        // 1 + the mean truncation
+  // gradients
+  const float2* coef;  // (s_t, c_t)
+  const uint16_t* W;
+  const uint16_t* x;
+  uint16_t* dx;        // dx, or with parts > 1 the fp32 sums of each part:
+  float* dx_part;      // [parts][n][d]
+  uint16_t* dw;        // dW in bf16,
+  float* dw32;         // or in fp32
+  const float* dw_add; // fp32 dW of earlier pieces (or what the caller adds to)
+  const int32_t* skey;   // targets in ascending order
+  const int32_t* order;  // their tokens, ascending among equal targets
+  const float* runs;     // launch 4's sums, at the position of their first token
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -166,32 +216,106 @@ __device__ __forceinline__ void write_rows64(uint8_t* slabs, int lane, const flo
   __syncwarp();
 }
 
-// Tile t of the mt x nt grid, in groups of `raster` pair rows with the
-// columns outer and the rows inner: pairs working at the same time share B
-// columns while the group's A rows stay in L2.
-__device__ __forceinline__ void tile_at(const ParamsX& p, int t, int& m, int& n) {
-  const int per = p.raster * p.nt;
-  const int g = t / per;
-  const int r0 = g * p.raster;
-  const int h = min(p.raster, p.mt - r0);
-  const int l = t - g * per;
-  n = l / h;
-  m = r0 + l % h;
+// v[0..63] += k * 64 bf16 values of a row of which `cols` exist.
+__device__ __forceinline__ void add_row64(float* v, const uint16_t* a, float k, int cols) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (8 * j < cols) {
+      float f[8];
+      unpack8x(__ldg(reinterpret_cast<const uint4*>(a) + j), f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[8 * j + q] = fmaf(k, f[q], v[8 * j + q]);
+    }
+  }
 }
 
-// K major of the operands: the logits' product has both K-major (x and W
-// rows), dx has P K-major and W MN-major, dW has P and x MN-major.
-template <int JOB, int NS>
+// The same with fp32 values and k = 1 (plain loads: the row may be the one
+// the caller overwrites).
+__device__ __forceinline__ void add_row64(float* v, const float* a, int cols) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (4 * j < cols) {
+      const float4 q = *(reinterpret_cast<const float4*>(a) + j);
+      v[4 * j] += q.x, v[4 * j + 1] += q.y, v[4 * j + 2] += q.z, v[4 * j + 3] += q.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void store_rows64(float* o, const float* v, int cols) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (4 * j < cols)
+      *(reinterpret_cast<float4*>(o) + j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+
+// One unit of work: a tile of one product over a range of K slices.
+struct Item {
+  int dx;      // gradients: dx's or dW's
+  int m, n;    // pair-tile row, tile column
+  int k0, k1;  // K slices
+  int part;
+};
+
+// Tile t of a grid, in groups of `raster` pair rows with the columns outer
+// and the rows inner: pairs working at the same time share B columns while
+// the group's A rows stay in L2.
+__device__ __forceinline__ void tile_at(const Grid& g, int t, Item& it) {
+  const int tiles = g.mt * g.nt;
+  it.part = t / tiles;
+  t -= it.part * tiles;
+  const int per = g.raster * g.nt;
+  const int q = t / per;
+  const int r0 = q * g.raster;
+  const int h = min(g.raster, g.mt - r0);
+  const int l = t - q * per;
+  it.n = l / h;
+  it.m = r0 + l % h;
+  it.k0 = static_cast<int>(static_cast<int64_t>(g.slices) * it.part / g.parts);
+  it.k1 = static_cast<int>(static_cast<int64_t>(g.slices) * (it.part + 1) / g.parts);
+}
+
+// The j-th item of unit u of U (false: none left).  The items of grid[0],
+// the longer ones, are dealt round; the units that get one fewer of them
+// first take `extra` items of grid[1] each (about the length of one of
+// grid[0]), then those are dealt round as well, so all units end within about
+// one short item of each other.
+__device__ __forceinline__ bool item_of(const ParamsX& p, int u, int U, int j, Item& it) {
+  const int n0 = p.grid[0].items;
+  const int rem = n0 % U;
+  const int mine = n0 / U + (u < rem ? 1 : 0);
+  if (j < mine) {
+    it.dx = p.first_dx;
+    tile_at(p.grid[0], u + j * U, it);
+    return true;
+  }
+  j -= mine;
+  const int early = rem > 0 ? U - rem : 0;  // units with one item fewer
+  int i;
+  if (early > 0 && u >= rem) i = j < p.extra ? j * early + (u - rem) : p.extra * early + (j - p.extra) * U + u;
+  else i = (early > 0 ? p.extra * early : 0) + j * U + u;
+  if (i >= p.grid[1].items) return false;
+  it.dx = !p.first_dx;
+  tile_at(p.grid[1], i, it);
+  return true;
+}
+
+// First position of a sorted array whose key is not below v.
+__device__ __forceinline__ int lower_bound(const int32_t* __restrict__ a, int n, int v) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a + mid) < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The logits' product has both operands K-major (rows of x and of W); dx has
+// E K-major and W MN-major, dW has E and s x MN-major.
+template <bool GRAD, int NS>
 __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constant__ ParamsX p) {
   using PL = PlanX<NS>;
   constexpr int STAGES = PL::STAGES;
-  constexpr bool A_MN = JOB == JOB_DW;
-  constexpr bool B_MN = JOB != JOB_LOGITS;
-  constexpr uint32_t IDESC = idesc_bf16(2 * BM, BN, A_MN, B_MN);
-  constexpr uint64_t A_STEP = A_MN ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
-  constexpr uint64_t B_STEP = B_MN ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
-  constexpr uint32_t A_LBO = A_MN ? ATOM : 16;
-  constexpr uint32_t B_LBO = B_MN ? ATOM : 16;
   constexpr uint32_t TMEM_COLS = 512;
 
   extern __shared__ uint8_t smem_raw[];
@@ -223,6 +347,10 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&p.map_a);
     tma_prefetch_map(&p.map_b);
+    if (GRAD) {
+      tma_prefetch_map(&p.map_a2);
+      tma_prefetch_map(&p.map_b2);
+    }
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
   fence_before_sync();
@@ -232,10 +360,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
 
-  const int ntiles = p.mt * p.nt;
-  const int G = static_cast<int>(gridDim.x >> 1);
+  const int U = static_cast<int>(gridDim.x >> 1);
   const int unit = static_cast<int>(blockIdx.x >> 1);
-  const int kit = (p.K + BK - 1) / BK;
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
@@ -244,12 +370,14 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       uint32_t phase = 0;
       bool ok = true;
       const uint32_t full_pair = dsmem_addr(smem_u32(full), 0);  // rank 0 counts both CTAs' bytes
-      for (int t = unit; t < ntiles && ok; t += G) {
-        int m, n;
-        tile_at(p, t, m, n);
-        const int m0 = m * 2 * BM + rank * BM;
-        const int n0 = n * NS * BN + rank * (BN / 2);
-        for (int i = 0; i < kit; ++i) {
+      Item it;
+      for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
+        const int m0 = it.m * 2 * BM + rank * BM;
+        const int n0 = it.n * NS * BN + rank * (BN / 2);
+        const bool a_mn = GRAD && !it.dx;
+        const CUtensorMap* ma = a_mn ? &p.map_a2 : &p.map_a;
+        const CUtensorMap* mb = a_mn ? &p.map_b2 : &p.map_b;
+        for (int i = it.k0; i < it.k1; ++i) {
           ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * PL::STAGE);
@@ -257,19 +385,19 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           uint8_t* sa = smem + stage * PL::STAGE;
           uint8_t* sb = sa + A_BYTES;
           const int k0 = i * BK;
-          if (A_MN) {
-            tma_load_2d_pair(sa, &p.map_a, bar, m0, k0);
-            tma_load_2d_pair(sa + ATOM, &p.map_a, bar, m0 + 64, k0);
+          if (a_mn) {
+            tma_load_2d_pair(sa, ma, bar, m0, k0);
+            tma_load_2d_pair(sa + ATOM, ma, bar, m0 + 64, k0);
           } else {
-            tma_load_2d_pair(sa, &p.map_a, bar, k0, m0);
+            tma_load_2d_pair(sa, ma, bar, k0, m0);
           }
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            if (B_MN) {
-              tma_load_2d_pair(sb + s * B_BYTES, &p.map_b, bar, n0 + s * BN, k0);
-              tma_load_2d_pair(sb + s * B_BYTES + ATOM, &p.map_b, bar, n0 + s * BN + 64, k0);
+            if (GRAD) {
+              tma_load_2d_pair(sb + s * B_BYTES, mb, bar, n0 + s * BN, k0);
+              tma_load_2d_pair(sb + s * B_BYTES + ATOM, mb, bar, n0 + s * BN + 64, k0);
             } else {
-              tma_load_2d_pair(sb + s * B_BYTES, &p.map_b, bar, k0, n0 + s * BN);
+              tma_load_2d_pair(sb + s * B_BYTES, mb, bar, k0, n0 + s * BN);
             }
           }
           if (++stage == STAGES) {
@@ -298,16 +426,29 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       uint32_t phase = 0;
       uint32_t acc = 0, acc_phase = 0;
       bool ok = true;
+      // operand majors of the current item; B is MN-major in both gradients
+      constexpr uint64_t MN_STEP = (UMMA_K * 128) >> 4, K_STEP = (UMMA_K * 2) >> 4;  // 16-byte units
+      constexpr uint64_t B_STEP = GRAD ? MN_STEP : K_STEP;
+      constexpr uint32_t B_LBO = GRAD ? ATOM : 16;
+      uint64_t a_step = K_STEP;
+      uint32_t a_lbo = 16, idesc = idesc_bf16(2 * BM, BN, false, GRAD);
       // one K slice of sub-tile `s` from ring stage st into accumulator d
       auto mmas = [&](uint32_t d, int st, int s, bool first) {
         const uint32_t sa = smem_u32(smem + st * PL::STAGE);
-        const uint64_t adesc = sdesc_sw128(sa, A_LBO, 1024);
+        const uint64_t adesc = sdesc_sw128(sa, a_lbo, 1024);
         const uint64_t bdesc = sdesc_sw128(sa + A_BYTES + s * B_BYTES, B_LBO, 1024);
 #pragma unroll
         for (int kk = 0; kk < BK / UMMA_K; ++kk)
-          mma_bf16_pair(d, adesc + A_STEP * kk, bdesc + B_STEP * kk, IDESC, (!first || kk > 0) ? 1u : 0u);
+          mma_bf16_pair(d, adesc + a_step * kk, bdesc + B_STEP * kk, idesc, (!first || kk > 0) ? 1u : 0u);
       };
-      for (int t = unit; t < ntiles && ok; t += G) {
+      Item it;
+      for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
+        const int kit = it.k1 - it.k0;
+        if (GRAD) {
+          a_step = it.dx ? K_STEP : MN_STEP;
+          a_lbo = it.dx ? 16 : ATOM;
+          idesc = it.dx ? idesc_bf16(2 * BM, BN, false, true) : idesc_bf16(2 * BM, BN, true, true);
+        }
         if (NS == 2) {
           // both accumulators belong to this tile: sub-tile 0 starts once its
           // columns are drained, sub-tile 1's first slices stay in the ring
@@ -404,88 +545,114 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
         acc_phase ^= 1u;
       }
     };
-    for (int t = unit; t < ntiles && ok; t += G) {
-      int m, n;
-      tile_at(p, t, m, n);
-      const int row0 = m * 2 * BM + rank * BM + quad * 32;  // this warp's 32 rows
+    Item it;
+    for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
+      const int row0 = it.m * 2 * BM + rank * BM + quad * 32;  // this warp's 32 rows
       const int row = row0 + lane;
-      const int rows = p.M - row0;  // rows of them that exist (or fewer than 1)
+      const int M = GRAD && !it.dx ? p.V : p.n;
+      const int rows = M - row0;  // rows of them that exist (or fewer than 1)
+      // what the epilogue adds to its row, fetched while the product runs
       int target = -1;
-      if (JOB == JOB_LOGITS && row < p.M) target = __ldg(p.targets + row);
+      float2 cf = make_float2(0.f, 0.f);
+      int first = 0, tokens = 0;  // dW: the positions of this word's tokens
+      if (row < M) {
+        if (!GRAD || it.dx) {
+          target = __ldg(p.targets + row);
+          if (GRAD) cf = __ldg(p.coef + row);
+        } else {
+          first = lower_bound(p.skey, p.n, row);
+          tokens = lower_bound(p.skey, p.n, row + 1) - first;
+        }
+      }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int c0 = (n * NS + s) * BN + half * (BN / 2);  // this warp's first column
+        const int c0 = (it.n * NS + s) * BN + half * (BN / 2);  // this warp's first column
         if (NS == 1 || s == 0) {
           ok = mbar_wait_cluster(tfull + acc, acc_phase, abort_flag);
           if (!ok) break;
+          __syncwarp();
         }
         fence_after_sync();
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + half * (BN / 2);
-        if (JOB == JOB_LOGITS) {
+        if (!GRAD) {
           float v[128];
           tmem_load64(tb, v);
           tmem_load64(tb + 64, v + 64);
           release();
-          if (c0 >= p.N) continue;  // past the vocabulary: no such group
-          if (static_cast<unsigned>(target - c0) < 128u) {
+          if (c0 >= p.V) continue;  // past the vocabulary: no such group
+          const bool here = static_cast<unsigned>(target - c0) < 128u;
+          if (here) {
             float l = 0.f;
 #pragma unroll
-            for (int j = 0; j < 128; ++j) l = j == target - c0 ? v[j] : l;
-            p.target_logit[row] = l;
+            for (int q = 0; q < 128; ++q) l = q == target - c0 ? v[q] : l;
+            p.target_logit[row] = l * p.unbias;
           }
-          if (c0 + 128 > p.N) {
+          if (c0 + 128 > p.V) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (c0 + j >= p.N) v[j] = -INFINITY;
+            for (int q = 0; q < 128; ++q)
+              if (c0 + q >= p.V) v[q] = -INFINITY;
           }
           float top = v[0];
 #pragma unroll
-          for (int j = 1; j < 128; ++j) top = fmaxf(top, v[j]);
-          const float ref = (fabsf(top) > kRefLimit && top != -INFINITY) ? top : 0.f;
-          const float bias = -ref * kLog2e;
+          for (int q = 1; q < 128; ++q) top = fmaxf(top, v[q]);
+          const float ref = (top > kRefHigh || (top < kRefLow && top != -INFINITY)) ? top * p.unbias : 0.f;
+          const float k = kLog2e * p.unbias, bias = -ref * kLog2e;
           float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-          for (int j = 0; j < 128; j += 4) {
-            v[j] = ex2(fmaf(v[j], kLog2e, bias));
-            v[j + 1] = ex2(fmaf(v[j + 1], kLog2e, bias));
-            v[j + 2] = ex2(fmaf(v[j + 2], kLog2e, bias));
-            v[j + 3] = ex2(fmaf(v[j + 3], kLog2e, bias));
-            s0 += v[j];
-            s1 += v[j + 1];
-            s2 += v[j + 2];
-            s3 += v[j + 3];
+          for (int q = 0; q < 128; q += 4) {
+            v[q] = ex2(fmaf(v[q], k, bias));
+            v[q + 1] = ex2(fmaf(v[q + 1], k, bias));
+            v[q + 2] = ex2(fmaf(v[q + 2], k, bias));
+            v[q + 3] = ex2(fmaf(v[q + 3], k, bias));
+            s0 += v[q];
+            s1 += v[q + 1];
+            s2 += v[q + 2];
+            s3 += v[q + 3];
           }
-          if (row < p.M) p.pairs[static_cast<int64_t>(c0 / kGroup) * p.ldp + row] = make_float2(ref, (s0 + s1) + (s2 + s3));
-          if (p.out) {
-            uint16_t* o = p.out + static_cast<int64_t>(row0) * p.ldo + c0;
-            const int cols = static_cast<int>(p.ldo) - c0;
-            write_rows64(slabs, lane, v, o, p.ldo, rows, cols);
-            write_rows64(slabs, lane, v + 64, o + 64, p.ldo, rows, cols - 64);
+          if (row < p.n) p.pairs[static_cast<int64_t>(c0 / kGroup) * p.ldp + row] = make_float2(ref, (s0 + s1) + (s2 + s3));
+          if (p.E) {
+            if (here) {  // the target's own element is added in fp32 by the gradients
+#pragma unroll
+              for (int q = 0; q < 128; ++q)
+                if (q == target - c0) v[q] = 0.f;
+            }
+            uint16_t* o = p.E + static_cast<int64_t>(row0) * p.ldv + c0;
+            const int cols = static_cast<int>(p.ldv) - c0;
+            write_rows64(slabs, lane, v, o, p.ldv, rows, cols);
+            write_rows64(slabs, lane, v + 64, o + 64, p.ldv, rows, cols - 64);
           }
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             float v[64];
+            __syncwarp();  // the lanes took different numbers of tokens
             tmem_load64(tb + 64 * h, v);
             if (h == 1) release();
             const int c = c0 + 64 * h;
-            if (p.add && row < p.M) {
-              const float* a = p.add + static_cast<int64_t>(row) * p.ldo + c;
+            const int cols = p.d - c;  // columns that exist from here on (a multiple of 8)
+            if (cols <= 0) continue;
+            if (it.dx) {
+              if (p.dx_part) {
+                store_rows64(p.dx_part + (static_cast<int64_t>(it.part) * p.n + row) * p.d + c, v, row < M ? cols : 0);
+              } else {
 #pragma unroll
-              for (int j = 0; j < 64; j += 4)
-                if (c + j < p.N) {
-                  const float4 q = *reinterpret_cast<const float4*>(a + j);
-                  v[j] += q.x, v[j + 1] += q.y, v[j + 2] += q.z, v[j + 3] += q.w;
-                }
-            }
-            if (p.out32) {
-              float* o = p.out32 + static_cast<int64_t>(row) * p.ldo + c;
-#pragma unroll
-              for (int j = 0; j < 64; j += 4)
-                if (row < p.M && c + j < p.N)
-                  *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                for (int q = 0; q < 64; ++q) v[q] = cf.x == 0.f ? 0.f : v[q] * cf.x;
+                if (cf.y != 0.f) add_row64(v, p.W + static_cast<int64_t>(target) * p.d + c, cf.y, cols);
+                write_rows64(slabs, lane, v, p.dx + static_cast<int64_t>(row0) * p.d + c, p.d, rows, cols);
+              }
             } else {
-              write_rows64(slabs, lane, v, p.out + static_cast<int64_t>(row0) * p.ldo + c, p.ldo, rows, p.N - c);
+              if (tokens > kDirect) {
+                for (int q = 0; q < tokens; q += kRun)
+                  add_row64(v, p.runs + static_cast<int64_t>(first + q) * p.d + c, cols);
+              } else {
+                for (int q = 0; q < tokens; ++q) {
+                  const int t = __ldg(p.order + first + q);
+                  add_row64(v, p.x + static_cast<int64_t>(t) * p.d + c, __ldg(&p.coef[t].y), cols);
+                }
+              }
+              if (p.dw_add && row < M) add_row64(v, p.dw_add + static_cast<int64_t>(row) * p.d + c, cols);
+              if (p.dw32) store_rows64(p.dw32 + static_cast<int64_t>(row) * p.d + c, v, row < M ? cols : 0);
+              else write_rows64(slabs, lane, v, p.dw + static_cast<int64_t>(row0) * p.d + c, p.d, rows, cols);
             }
           }
         }
@@ -508,34 +675,101 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
   }
 }
 
+// ------------------------------------------------------- tokens by target
+
+__device__ __forceinline__ int key_of(int32_t target, int V, int ignore) {
+  return static_cast<unsigned>(target) < static_cast<unsigned>(V) && target != ignore ? target : V;
+}
+
+constexpr int kSortWarps = 8;
+
+// Stable sort of the piece's targets (those that do not count last): each
+// warp counts the tokens before its own.  n^2 comparisons, 8 us at 8192
+// tokens, a sixteenth of a percent of that many rows' products.  Block 0 also
+// counts the targets of the whole call that count.
+__global__ void __launch_bounds__(32 * kSortWarps)
+    sort_targets_kernel(const int32_t* __restrict__ targets, int n, int V, int ignore, int32_t* __restrict__ skey,
+                        int32_t* __restrict__ order, const int32_t* __restrict__ all, int T,
+                        int32_t* __restrict__ count) {
+  __shared__ int sh[kSortWarps];
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kSortWarps + warp;
+  if (t < n) {
+    const int key = key_of(__ldg(targets + t), V, ignore);
+    int before = 0;
+#pragma unroll 8
+    for (int u = lane; u < n; u += 32) {
+      const int k = key_of(__ldg(targets + u), V, ignore);
+      before += (k < key || (k == key && u < t)) ? 1 : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+      skey[before] = key;
+      order[before] = t;
+    }
+  }
+  if (blockIdx.x != 0 || !count) return;
+  int c = 0;
+#pragma unroll 8
+  for (int u = threadIdx.x; u < T; u += 32 * kSortWarps) c += key_of(__ldg(all + u), V, ignore) < V;
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (lane == 0) sh[warp] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kSortWarps; ++i) c += sh[i];
+    *count = c;
+  }
+}
+
+// runs[r] = sum of c_t x_t over the up to kRun tokens at positions r .. of a
+// word with more than kDirect tokens, r - (the word's first position) a
+// multiple of kRun.  One warp per position and kRunCols columns.
+constexpr int kRunCols = 512;
+__global__ void __launch_bounds__(256)
+    target_runs_kernel(const uint16_t* __restrict__ x, int n, int d, int V, const int32_t* __restrict__ skey,
+                       const int32_t* __restrict__ order, const float2* __restrict__ coef, float* __restrict__ runs) {
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= n) return;
+  const int key = __ldg(skey + r);
+  if (key >= V) return;
+  const int first = lower_bound(skey, n, key);
+  const int tokens = lower_bound(skey, n, key + 1) - first;
+  if (tokens <= kDirect || (r - first) % kRun != 0) return;
+  const int m = min(kRun, first + tokens - r);
+  const int mine = lane < m ? __ldg(order + r + lane) : 0;  // kRun tokens, one per lane
+  const float cm = lane < m ? __ldg(&coef[mine].y) : 0.f;
+#pragma unroll
+  for (int i = 0; i < kRunCols / 256; ++i) {
+    const int c = blockIdx.y * kRunCols + i * 256 + lane * 8;
+    float acc[8] = {};
+#pragma unroll 8
+    for (int q = 0; q < m; ++q) {
+      const int t = __shfl_sync(0xffffffffu, mine, q);
+      const float k = __shfl_sync(0xffffffffu, cm, q);
+      if (c < d) {
+        float f[8];
+        unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(k, f[j], acc[j]);
+      }
+    }
+    if (c < d) {
+      float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(r) * d + c);
+      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
+  }
+}
+
 // ------------------------------------------------------------ row statistics
 
 constexpr int kStatRows = 32, kStatSlices = 32;
-
-// How many targets count: one block over all T.
-__global__ void __launch_bounds__(1024) count_targets_kernel(const int32_t* __restrict__ targets, int T, int V,
-                                                             int ignore, int32_t* __restrict__ count, int32_t* err) {
-  __shared__ int sh[32];
-  dmoe::pdl_wait();
-  dmoe::pdl_launch_dependents();
-  int n = 0;
-  bool bad = false;
-#pragma unroll 8
-  for (int t = threadIdx.x; t < T; t += 1024) {
-    const int32_t v = __ldg(targets + t);
-    const bool in = static_cast<unsigned>(v) < static_cast<unsigned>(V);
-    n += in && v != ignore;
-    bad |= !in && v != ignore;
-  }
-  if (bad) dmoe::raise_error(err, DMOE_SITE_LOSS_TARGET | DMOE_ERR_DEVICE);
-  n = __reduce_add_sync(0xffffffffu, n);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    n = __reduce_add_sync(0xffffffffu, sh[threadIdx.x]);
-    if (threadIdx.x == 0) *count = n;
-  }
-}
 
 // (R, S) <- the pair of the union: S counts exp(l - R).
 __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
@@ -549,94 +783,149 @@ __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
   }
 }
 
-// 32 rows x 32 slices of the row's groups per block.
-__global__ void __launch_bounds__(kStatRows * kStatSlices)
-    row_stats_kernel(const float2* __restrict__ pairs, int64_t ldp, int groups, const float* __restrict__ target_logit,
-                     const int32_t* __restrict__ targets, int n, int V, int ignore, const float* __restrict__ d_loss,
-                     const int32_t* __restrict__ count, float* __restrict__ loss, float* __restrict__ lse,
-                     float4* __restrict__ factor) {
-  __shared__ float2 sh[kStatSlices][kStatRows];
+struct ParamsR {
+  const float2* pairs;
+  int64_t ldp;
+  int groups;
+  const float* target_logit;
+  const int32_t* targets;
+  int n, d, V, ignore;
+  const float* d_loss;
+  const int32_t* count;
+  float* loss;
+  float* lse;
+  float2* coef;       // NULL: the loss alone
+  const uint16_t* x;
+  uint16_t* xs;       // s x in bf16 (NULL: no dW)
+  uint16_t* E;
+  int64_t ldv;
+  int32_t* err;
+};
+
+// 32 rows per block: the row's groups by 32 slices, then a warp per row for
+// s x and, where a row's groups have different references, its E.
+__global__ void __launch_bounds__(kStatRows * kStatSlices) row_stats_kernel(const ParamsR p) {
+  __shared__ float4 sh[kStatSlices][kStatRows];
+  __shared__ float sh_s[kStatRows], sh_r[kStatRows];
+  __shared__ int sh_fix[kStatRows];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int slice = threadIdx.x >> 5;
   const int t = blockIdx.x * kStatRows + lane;
-  float R = -INFINITY, S = 0.f;
-  if (t < n) {
+  float R = -INFINITY, S = 0.f, low = INFINITY, high = -INFINITY;
+  if (t < p.n) {
 #pragma unroll 4
-    for (int g = slice; g < groups; g += kStatSlices) {
-      const float2 q = __ldg(pairs + g * ldp + t);
+    for (int g = slice; g < p.groups; g += kStatSlices) {
+      const float2 q = __ldg(p.pairs + g * p.ldp + t);
       join(R, S, q.x, q.y);
+      low = fminf(low, q.x);
+      high = fmaxf(high, q.x);
     }
   }
-  sh[slice][lane] = make_float2(R, S);
+  sh[slice][lane] = make_float4(R, S, low, high);
   __syncthreads();
-  if (slice != 0 || t >= n) return;
-  for (int i = 1; i < kStatSlices; ++i) {
-    const float2 q = sh[i][lane];
-    if (q.x != -INFINITY) join(R, S, q.x, q.y);  // a slice without groups
+  if (slice == 0 && t < p.n) {
+    for (int i = 1; i < kStatSlices; ++i) {
+      const float4 q = sh[i][lane];
+      if (q.x != -INFINITY) join(R, S, q.x, q.y);  // else a slice without groups
+      low = fminf(low, q.z);
+      high = fmaxf(high, q.w);
+    }
+    const float L = R + logf(S);
+    const int32_t v = __ldg(p.targets + t);
+    const bool counts = key_of(v, p.V, p.ignore) < p.V;
+    if (!counts && v != p.ignore) dmoe::raise_error(p.err, DMOE_SITE_LOSS_TARGET | DMOE_ERR_DEVICE);
+    const float nll = counts ? L - __ldg(p.target_logit + t) : 0.f;
+    p.loss[t] = nll;
+    if (p.lse) p.lse[t] = L;
+    if (p.coef) {
+      float g = 0.f;
+      if (counts) g = p.d_loss ? __ldg(p.d_loss + t) : 1.f / static_cast<float>(*p.count);
+      const float s = g == 0.f ? 0.f : g * expf(R - L);
+      // expm1: where the softmax at the target is close to 1 or to 0
+      p.coef[t] = make_float2(s, g == 0.f ? 0.f : g * expm1f(-nll));
+      sh_s[lane] = s;
+      sh_r[lane] = R;
+      // 1: bring the row's groups to one reference; 2: a row that does not
+      // count holds what is not finite, which times 0 would still spread
+      sh_fix[lane] = g == 0.f ? (isfinite(S) ? 0 : 2) : (low != high ? 1 : 0);
+    }
   }
-  const float L = R + logf(S);
-  const int32_t v = __ldg(targets + t);
-  const bool counts = static_cast<unsigned>(v) < static_cast<unsigned>(V) && v != ignore;
-  const float nll = counts ? L - __ldg(target_logit + t) : 0.f;
-  loss[t] = nll;
-  if (lse) lse[t] = L;
-  if (factor) {
-    float g = 0.f;
-    if (counts) g = d_loss ? __ldg(d_loss + t) : 1.f / static_cast<float>(*count);
-    // the target's own element from its fp32 logit: where the softmax is close
-    // to 1, its rounded exponential minus 1 would be all rounding
-    factor[t] = make_float4(L, g, g * expm1f(-nll), 0.f);
+  if (!p.coef) return;
+  __syncthreads();
+  const int row = blockIdx.x * kStatRows + slice;
+  if (row >= p.n) return;
+  if (p.xs) {
+    const float s = sh_s[slice];
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row) * p.d);
+    uint4* dst = reinterpret_cast<uint4*>(p.xs + static_cast<int64_t>(row) * p.d);
+#pragma unroll 4
+    for (int v = lane; v < p.d / 8; v += 32) {
+      float f[8];
+      unpack8x(__ldg(src + v), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = s == 0.f ? 0.f : f[j] * s;
+      dst[v] = pack8x(f);
+    }
+  }
+  const int fix = sh_fix[slice];
+  if (fix) {
+    const float top = sh_r[slice];
+    uint16_t* e = p.E + static_cast<int64_t>(row) * p.ldv;
+    for (int g = 0; g < p.groups; ++g) {
+      const float r = __ldg(&p.pairs[g * p.ldp + row].x);
+      const int c = g * kGroup + lane * 4;
+      if ((fix == 1 && r == top) || c >= p.ldv) continue;
+      const float k = fix == 2 ? 0.f : expf(r - top);
+      uint2 u = *reinterpret_cast<const uint2*>(e + c);
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float2 f = __bfloat1622float2(h[j]);
+        f.x = fix == 2 ? 0.f : f.x * k;
+        f.y = fix == 2 ? 0.f : f.y * k;
+        h[j] = __floats2bfloat162_rn(f.x, f.y);
+      }
+      *reinterpret_cast<uint2*>(e + c) = u;
+    }
   }
 }
 
-// G in place of the exponentials: one warp per row and 1024 columns.
-constexpr int kScaleCols = 1024;
+// dx from the fp32 sums of its parts: one thread per 8 columns.
 __global__ void __launch_bounds__(256)
-    scale_kernel(uint16_t* __restrict__ P, int64_t ld, int n, int V, const float2* __restrict__ pairs, int64_t ldp,
-                 const float4* __restrict__ factor, const int32_t* __restrict__ targets) {
+    join_dx_kernel(const float* __restrict__ part, int parts, int n, int d, const float2* __restrict__ coef,
+                   const int32_t* __restrict__ targets, const uint16_t* __restrict__ W, uint16_t* __restrict__ dx) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (t >= n) return;
-  const int c0 = blockIdx.x * kScaleCols;
-  const float4 f = __ldg(factor + t);
-  const int target = __ldg(targets + t);
-  uint4* row = reinterpret_cast<uint4*>(P + t * ld + c0);
-  uint4 u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + (i * 32 + lane) * 8;
-    if (c < ld) u[i] = row[i * 32 + lane];
+  const int nvec = d / 8;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(n) * nvec) return;
+  const int64_t t = i / nvec;
+  const int c = static_cast<int>(i - t * nvec) * 8;
+  const float2 cf = __ldg(coef + t);
+  float acc[8] = {};
+#pragma unroll 4
+  for (int q = 0; q < parts; ++q) {
+    const float4* a = reinterpret_cast<const float4*>(part + (static_cast<int64_t>(q) * n + t) * d + c);
+    const float4 u = __ldg(a), v = __ldg(a + 1);
+    acc[0] += u.x, acc[1] += u.y, acc[2] += u.z, acc[3] += u.w;
+    acc[4] += v.x, acc[5] += v.y, acc[6] += v.z, acc[7] += v.w;
   }
+  float f[8] = {};
+  if (cf.y != 0.f) unpack8x(__ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(__ldg(targets + t)) * d + c)), f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + (i * 32 + lane) * 8;
-    if (c >= ld) continue;
-    float v[8];
-    unpack8x(u[i], v);
-    // padding columns past the vocabulary have no pair, a row that does not
-    // count stays zero whatever it holds
-    const bool zero = c >= V || f.y == 0.f;
-    const float k = zero ? 0.f : expf(__ldg(&pairs[(c / kGroup) * ldp + t].x) - f.x) * f.y;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = zero ? 0.f : v[j] * k;
-      if (c + j == target) v[j] = f.z;
-    }
-    row[i * 32 + lane] = pack8x(v);
-  }
+  for (int j = 0; j < 8; ++j) f[j] = fmaf(cf.y, f[j], cf.x == 0.f ? 0.f : acc[j] * cf.x);
+  *reinterpret_cast<uint4*>(dx + t * d + c) = pack8x(f);
 }
 
 // ----------------------------------------------------------------- host side
 
 // Opt-in shared memory and the number of 2-CTA clusters that fit, once per
 // instantiation and device.
-template <int JOB, int NS>
+template <bool GRAD, int NS>
 dmoe_status launch_head(const ParamsX& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
-  auto kern = head_kernel<JOB, NS>;
+  auto kern = head_kernel<GRAD, NS>;
   const size_t smem = PlanX<NS>::SMEM;
   static std::atomic<int> clusters[64];
   int n = clusters[di.device].load(std::memory_order_acquire);
@@ -659,12 +948,49 @@ dmoe_status launch_head(const ParamsX& p, const dmoe::DeviceInfo& di, cudaStream
     if (n < 1) return DMOE_ERR_UNSUPPORTED;
     clusters[di.device].store(n, std::memory_order_release);
   }
-  const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt;
-  const int grid = 2 * static_cast<int>(std::min<int64_t>(n, tiles));
+  const int64_t items = static_cast<int64_t>(p.grid[0].items) + p.grid[1].items;
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(n, items));
   cudaError_t e = dmoe::launch_pdl_cluster(kern, dim3(grid), dim3(kThreadsX), smem, st, 2, p);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
+}
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+Grid make_grid(int M, int N, int K, int raster, int parts = 1) {
+  Grid g{};
+  g.mt = ceil_div(M, 2 * BM);
+  g.nt = ceil_div(N, 2 * BN);
+  g.raster = raster;
+  g.slices = ceil_div(K, BK);
+  g.parts = parts;
+  g.items = g.mt * g.nt * parts;
+  return g;
+}
+
+// Parts of dx's sum over the vocabulary.  dx has few tiles of V / 64 slices
+// each; in one part the last round of them can outlast everything else (512
+// tokens: 8 tiles for 76 pairs).  Takes the count whose longest unit is
+// shortest, in slices, charging each part the fp32 sums it writes and reads
+// back (a 256 x 512 tile's cost about two slices).
+int dx_parts(int n, int d, int V, bool dw) {
+  const Grid x = make_grid(n, d, V, 1), w = make_grid(V, d, n, 1);
+  const int64_t total = static_cast<int64_t>(x.items) * x.slices + (dw ? static_cast<int64_t>(w.items) * w.slices : 0);
+  int best = 1;
+  int64_t best_cost = -1;
+  for (int s = 1; s <= kMaxSplit && (s == 1 || x.slices / s >= 8); ++s) {
+    const int64_t items = static_cast<int64_t>(x.items) * s;
+    const int64_t longest = ceil_div(items, kUnits) * static_cast<int64_t>(ceil_div(x.slices, s));
+    int64_t cost = std::max<int64_t>(ceil_div(total, kUnits), longest);
+    if (s > 1) cost += 8 + ceil_div(2 * items, kUnits);
+    if (best_cost < 0 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
 }
 
 // Bytes of a workspace, in order (each part 256-byte aligned).
@@ -673,10 +999,8 @@ struct Layout {
   int64_t ldp;     // row pitch of the (ref, sum) pairs
   int64_t ldv;     // row pitch of the exponentials
   int64_t groups;
-  size_t count, pairs, target_logit, factor, acc, P, total;
+  size_t count, pairs, target_logit, coef, skey, order, xs, runs, part, acc, E, total;
 };
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
   Layout l{};
@@ -691,14 +1015,28 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
     at += static_cast<size_t>(round_up(static_cast<int64_t>(bytes), 256));
     return a;
   };
+  const size_t rows = static_cast<size_t>(l.piece);
   l.count = take(256);
   l.pairs = take(static_cast<size_t>(l.groups * l.ldp) * sizeof(float2));
-  l.target_logit = take(static_cast<size_t>(l.piece) * sizeof(float));
+  l.target_logit = take(rows * sizeof(float));
   if (grad) {
-    l.factor = take(static_cast<size_t>(l.piece) * sizeof(float4));
+    l.coef = take(rows * sizeof(float2));
+    l.skey = take(rows * sizeof(int32_t));
+    l.order = take(rows * sizeof(int32_t));
+    l.xs = take(rows * d * 2);
+    l.runs = take(rows * d * sizeof(float));
+    // the full pieces' and the last, shorter one's dx parts
+    size_t part = 0;
+    for (const int64_t n : {std::min<int64_t>(l.piece, T), T % l.piece}) {
+      for (const bool dw : {false, true}) {
+        const int s = n > 0 ? dx_parts(static_cast<int>(n), d, V, dw) : 1;
+        if (s > 1) part = std::max(part, static_cast<size_t>(n) * s * d * sizeof(float));
+      }
+    }
+    l.part = take(part);
     // dW of earlier pieces, when it does not fit the output's own type
     l.acc = take(dw_bf16 && T > l.piece ? static_cast<size_t>(V) * d * sizeof(float) : 0);
-    l.P = take(static_cast<size_t>(l.piece * l.ldv) * 2);
+    l.E = take(static_cast<size_t>(l.piece * l.ldv) * 2);
   }
   l.total = at;
   return l;
@@ -708,10 +1046,17 @@ bool sizes_ok(int T, int d, int V, int piece) {
   return T >= 0 && d >= 8 && (d & 7) == 0 && V >= 1 && V <= (1 << 24) && d <= (1 << 20) && piece >= 0;
 }
 
-#define DMOE_TRY(call)                 \
-  do {                                 \
-    const dmoe_status st__ = (call);   \
-    if (st__ != DMOE_OK) return st__;  \
+#define DMOE_TRY(call)                \
+  do {                                \
+    const dmoe_status st__ = (call);  \
+    if (st__ != DMOE_OK) return st__; \
+  } while (0)
+
+#define DMOE_TRY_LAUNCH(call)                          \
+  do {                                                 \
+    const cudaError_t e__ = (call);                    \
+    if (e__ != cudaSuccess) return dmoe::cuda_status(e__); \
+    dmoe::count_launches(1);                           \
   } while (0)
 
 }  // namespace
@@ -736,8 +1081,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
   const Layout l = layout_of(T, d, V, grad, dw && !dw_f32, piece);
   if (T > 0 && ws_bytes < l.total) return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;
-  dmoe_status s = dmoe::device_info(&di);
-  if (s != DMOE_OK) return s;
+  DMOE_TRY(dmoe::device_info(&di));
   cudaStream_t st = dmoe::as_stream(stream);
   if (T == 0) {
     if (dw && !accumulate)
@@ -745,87 +1089,99 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     return DMOE_OK;
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
+  auto at = [&](size_t off) { return grad ? base + off : nullptr; };
   int32_t* count = reinterpret_cast<int32_t*>(base + l.count);
   float2* pairs = reinterpret_cast<float2*>(base + l.pairs);
   float* target_logit = reinterpret_cast<float*>(base + l.target_logit);
-  float4* factor = grad ? reinterpret_cast<float4*>(base + l.factor) : nullptr;
-  uint16_t* P = grad ? reinterpret_cast<uint16_t*>(base + l.P) : nullptr;
-  float* acc = grad ? reinterpret_cast<float*>(base + l.acc) : nullptr;
-
-  cudaError_t e = dmoe::launch_pdl(count_targets_kernel, dim3(1), dim3(1024), 0, st, targets, T, V, ignore_index,
-                                   count, di.err_word);
-  if (e != cudaSuccess) return dmoe::cuda_status(e);
-  dmoe::count_launches(1);
+  float2* coef = reinterpret_cast<float2*>(at(l.coef));
+  int32_t* skey = reinterpret_cast<int32_t*>(at(l.skey));
+  int32_t* order = reinterpret_cast<int32_t*>(at(l.order));
+  uint16_t* xs = reinterpret_cast<uint16_t*>(at(l.xs));
+  float* runs = reinterpret_cast<float*>(at(l.runs));
+  float* part = reinterpret_cast<float*>(at(l.part));
+  float* acc = reinterpret_cast<float*>(at(l.acc));
+  uint16_t* E = reinterpret_cast<uint16_t*>(at(l.E));
 
   for (int64_t t0 = 0; t0 < T; t0 += l.piece) {
     const int n = static_cast<int>(std::min<int64_t>(l.piece, T - t0));
     const uint16_t* xp = x + t0 * d;
+    const int32_t* tp = targets + t0;
+    if (grad)
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(sort_targets_kernel, dim3(ceil_div(n, kSortWarps)), dim3(32 * kSortWarps), 0, st,
+                                       tp, n, V, ignore_index, skey, order, targets, T, t0 == 0 ? count : nullptr));
+    ParamsX p{};
+    p.n = n, p.d = d, p.V = V;
+    p.targets = tp;
+    p.err = di.err_word;
+    p.ldv = l.ldv;
     {
-      ParamsX p{};
-      if (!dmoe::make_map(&p.map_a, xp, n, d, BK, BM) || !dmoe::make_map(&p.map_b, w, V, d, BK, BN / 2))
+      ParamsX q = p;
+      if (!dmoe::make_map(&q.map_a, xp, n, d, BK, BM) || !dmoe::make_map(&q.map_b, w, V, d, BK, BN / 2))
         return DMOE_ERR_CUDA;
-      p.M = n, p.N = V, p.K = d;
-      p.mt = (n + 2 * BM - 1) / (2 * BM);
-      p.nt = (V + 2 * BN - 1) / (2 * BN);
-      p.raster = 16;
-      p.out = P;
-      p.ldo = l.ldv;
-      p.targets = targets + t0;
-      p.pairs = pairs;
-      p.ldp = l.ldp;
-      p.target_logit = target_logit;
-      p.err = di.err_word;
-      DMOE_TRY((launch_head<JOB_LOGITS, 2>(p, di, st)));
+      q.grid[0] = make_grid(n, V, d, 16);
+      q.E = E;
+      q.pairs = pairs;
+      q.ldp = l.ldp;
+      q.target_logit = target_logit;
+      q.unbias = 1.f + static_cast<float>(ceil_div(d, UMMA_K)) * kTruncation;
+      DMOE_TRY((launch_head<false, 2>(q, di, st)));
     }
-    e = dmoe::launch_pdl(row_stats_kernel, dim3((n + kStatRows - 1) / kStatRows), dim3(kStatRows * kStatSlices), 0, st,
-                         static_cast<const float2*>(pairs), l.ldp, static_cast<int>(l.groups),
-                         static_cast<const float*>(target_logit), targets + t0, n, V, ignore_index,
-                         d_loss ? d_loss + t0 : nullptr, static_cast<const int32_t*>(count), loss + t0,
-                         lse ? lse + t0 : nullptr, factor);
-    if (e != cudaSuccess) return dmoe::cuda_status(e);
-    dmoe::count_launches(1);
+    ParamsR r{};
+    r.pairs = pairs, r.ldp = l.ldp, r.groups = static_cast<int>(l.groups);
+    r.target_logit = target_logit, r.targets = tp;
+    r.n = n, r.d = d, r.V = V, r.ignore = ignore_index;
+    r.d_loss = d_loss ? d_loss + t0 : nullptr;
+    r.count = count;
+    r.loss = loss + t0, r.lse = lse ? lse + t0 : nullptr;
+    r.coef = coef;
+    r.x = xp, r.xs = dw ? xs : nullptr;
+    r.E = E, r.ldv = l.ldv;
+    r.err = di.err_word;
+    DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel, dim3(ceil_div(n, kStatRows)), dim3(kStatRows * kStatSlices), 0,
+                                     st, r));
     if (!grad) continue;
-    e = dmoe::launch_pdl(scale_kernel, dim3(static_cast<unsigned>((l.ldv + kScaleCols - 1) / kScaleCols), (n + 7) / 8),
-                         dim3(256), 0, st, P, l.ldv, n, V, static_cast<const float2*>(pairs), l.ldp,
-                         static_cast<const float4*>(factor), targets + t0);
-    if (e != cudaSuccess) return dmoe::cuda_status(e);
-    dmoe::count_launches(1);
+    if (dw)
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 8), ceil_div(d, kRunCols)), dim3(256), 0,
+                                       st, xp, n, d, V, static_cast<const int32_t*>(skey),
+                                       static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs));
+    const int parts = dx ? dx_parts(n, d, V, dw != nullptr) : 1;
+    Grid gx{}, gw{};
+    // E as [n, V] with row pitch ldv: the columns past V read as zero
     if (dx) {
-      ParamsX p{};
-      // P as [n, V] with row pitch ldv: the columns past V read as zero
-      if (!dmoe::make_map_ld(&p.map_a, P, n, V, l.ldv, BK, BM) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
+      if (!dmoe::make_map_ld(&p.map_a, E, n, V, l.ldv, BK, BM) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
         return DMOE_ERR_CUDA;
-      p.M = n, p.N = d, p.K = V;
-      p.mt = (n + 2 * BM - 1) / (2 * BM);
-      p.nt = (d + 2 * BN - 1) / (2 * BN);
-      p.raster = 16;
-      p.out = dx + t0 * d;
-      p.ldo = d;
-      p.err = di.err_word;
-      DMOE_TRY((launch_head<JOB_DX, 2>(p, di, st)));
+      gx = make_grid(n, d, V, 16, parts);
     }
     if (dw) {
-      ParamsX p{};
-      if (!dmoe::make_map_ld(&p.map_a, P, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b, xp, n, d, 64, BK))
+      if (!dmoe::make_map_ld(&p.map_a2, E, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b2, xs, n, d, 64, BK))
         return DMOE_ERR_CUDA;
-      p.M = V, p.N = d, p.K = n;
-      p.mt = (V + 2 * BM - 1) / (2 * BM);
-      p.nt = (d + 2 * BN - 1) / (2 * BN);
-      p.raster = 1;
-      p.ldo = d;
-      p.err = di.err_word;
-      const bool last = t0 + n >= T;
-      if (dw_f32) {
-        p.out32 = static_cast<float*>(dw);
-        p.add = (accumulate || t0 > 0) ? static_cast<const float*>(dw) : nullptr;
-      } else {
-        // fp32 until the last piece, then one rounding
-        p.add = t0 > 0 ? acc : nullptr;
-        if (last) p.out = static_cast<uint16_t*>(dw);
-        else p.out32 = acc;
-      }
-      DMOE_TRY((launch_head<JOB_DW, 2>(p, di, st)));
+      gw = make_grid(V, d, n, 1);
     }
+    p.first_dx = gx.items > 0 && (gw.items == 0 || gx.slices / gx.parts >= gw.slices);
+    p.grid[0] = p.first_dx ? gx : gw;
+    p.grid[1] = p.first_dx ? gw : gx;
+    if (p.grid[1].items > 0) {
+      const int s1 = std::max(1, p.grid[1].slices / p.grid[1].parts);
+      p.extra = (p.grid[0].slices / p.grid[0].parts + s1 / 2) / s1;
+    }
+    p.coef = coef, p.W = w, p.x = xp;
+    p.dx = dx ? dx + t0 * d : nullptr;
+    p.dx_part = parts > 1 ? part : nullptr;
+    p.skey = skey, p.order = order, p.runs = runs;
+    const bool last = t0 + n >= T;
+    if (dw_f32) {
+      p.dw32 = static_cast<float*>(dw);
+      p.dw_add = (accumulate || t0 > 0) ? p.dw32 : nullptr;
+    } else {  // fp32 until the last piece, then one rounding
+      p.dw = static_cast<uint16_t*>(dw);
+      p.dw32 = last ? nullptr : acc;
+      p.dw_add = t0 > 0 ? acc : nullptr;
+    }
+    DMOE_TRY((launch_head<true, 2>(p, di, st)));
+    if (parts > 1)
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(join_dx_kernel, dim3(ceil_div(static_cast<int64_t>(n) * (d / 8), 256)), dim3(256),
+                                       0, st, static_cast<const float*>(part), parts, n, d,
+                                       static_cast<const float2*>(coef), tp, w, dx + t0 * d));
   }
   return DMOE_OK;
 }
