@@ -19,15 +19,15 @@
 // Tokens go in pieces.  A piece's launches:
 //   1 sort     tokens ordered by target (with gradients)
 //   2 logits   x W^T on the tensor cores; the epilogue turns a tile's
-//              accumulators into E and, for each row and 128 columns, leaves
+//              accumulators into E and, for each row and 64 columns, leaves
 //              the pair (ref, sum of exp(l - ref)).  With gradients E goes to a
 //              [piece, V] bf16 array, the only thing of that size that ever
 //              exists; without, nothing is written.
 //   3 rows     the pairs of a row meet in lse_t; loss_t, s_t, c_t, s_t x_t
-//   4 targets  sums of c_t x_t, 32 tokens each, for words with many tokens
+//   4 targets  sums of c_t x_t, up to 32 tokens each, for words with many
 //   5 grads    the tiles of both products in one launch
 //
-// ref is 0 while the largest of a row's 128 logits lies in [kRefLow,
+// ref is 0 while the largest of a row's 64 logits lies in [kRefLow,
 // kRefHigh], else that maximum: exp of a moderate logit needs no maximum
 // subtracted, fp32 and bf16 reach from 1e-38 to 3e38, so in the usual case
 // every pair of a row has the reference 0 and E needs no second pass.  A row
@@ -69,12 +69,13 @@ constexpr int UMMA_K = 16;
 constexpr uint32_t A_BYTES = BM * BK * 2;        // this CTA's A rows
 constexpr uint32_t B_BYTES = (BN / 2) * BK * 2;  // this CTA's half of a sub-tile's B
 constexpr uint32_t ATOM = 64 * BK * 2;           // MN-major operands: 64 MN x 64 K boxes
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;  // four per TMEM lane quadrant, 64 columns of a sub-tile each
 constexpr int kThreadsX = 64 + 32 * kEpiWarps;
-constexpr uint32_t SLAB = 32 * 32 * 2;
-constexpr uint32_t SLAB_BYTES = kEpiWarps * 2 * SLAB;
+// One epilogue warp's output on its way out: 32 rows x 32 columns, or, where
+// it leaves by TMA, all 64 of its columns.
+constexpr uint32_t SLAB32 = 32 * 32 * 2, SLAB64 = 32 * 64 * 2;
 constexpr size_t kSmemMax = 232448;
-constexpr int kGroup = 128;          // columns that share a (ref, sum) pair
+constexpr int kGroup = 64;           // columns that share a (ref, sum) pair
 // Above: 2^24 exponentials of kRefHigh, times any sensible weights, stay far
 // below 3e38.  Below: what is 27 under kRefLow, 2e-12 of its group's largest
 // exponential, reaches the denormals.
@@ -83,14 +84,27 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kTruncation = 1.f / 67108864.f;  // 2^-26 of the sum per 16 products
 constexpr int kPieceDefault = 8192;  // tokens per piece when the caller names none
 constexpr int kPieceMax = 1 << 18;
+// Logits over at most so many columns run 256-wide tiles: their two
+// accumulators let a tile's exponentials overlap the next tile's product,
+// which 512-wide tiles, filling the TMEM, do only in part.  The logits of
+// 8192 x 32000, 256-wide against 512-wide: d = 64 92 against 110 us, 256 119
+// / 131, 512 193 / 215, 1024 322 / 325, 2048 562 / 570; at d = 4096, where the
+// exponentials are a small part, the operands that 512-wide tiles save
+// count: with its gradients 3828 / 3814 us.
+constexpr int kNarrowD = 1024;
 
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
 constexpr int kMaxSplit = 16;
-constexpr int kRun = 32;             // tokens of one word per partial sum of launch 4
+constexpr int kRun = 32;             // positions per partial sum of launch 4
 constexpr int kDirect = 4;           // words with up to so many tokens are summed by dW's epilogue itself
 
-template <int NS>
+template <bool GRAD, int NS>
 struct PlanX {
+  // the exponentials leave by TMA where the tiles' sums are short (NS = 1):
+  // storing them is then as long as the product, see write_tile()
+  static constexpr bool TMA_OUT = !GRAD && NS == 1;
+  static constexpr uint32_t SLAB = TMA_OUT ? SLAB64 : SLAB32;
+  static constexpr uint32_t SLAB_BYTES = kEpiWarps * SLAB;
   static constexpr uint32_t STAGE = A_BYTES + NS * B_BYTES;
   static constexpr int FIT = static_cast<int>((kSmemMax - 1536 - SLAB_BYTES) / STAGE);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -98,13 +112,39 @@ struct PlanX {
   static_assert(STAGES >= 4 && SMEM <= kSmemMax, "shared-memory plan");
 };
 
-// A grid of M x N tiles over K, cut into `parts` ranges of K slices.
+// Exact unsigned division by a number fixed on the host (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994,
+// figure 4.1): a multiplication instead of some forty instructions, which a
+// single issuing thread would wait for at every tile.
+struct FastDiv {
+  uint32_t d, m;
+  int s;  // ceil(log2 d)
+  void set(uint32_t v) {
+    d = v;
+    for (s = 0; (1ull << s) < v; ++s) {
+    }
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - v)) / v + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    const uint32_t t = __umulhi(m, n);
+    return s == 0 ? n : (t + ((n - t) >> 1)) >> (s - 1);
+  }
+};
+
+// A grid of M x N tiles over K, cut into `parts` ranges of K slices, in groups
+// of `raster` pair rows.
 struct Grid {
-  int mt, nt;   // pair-tile rows, tile columns
-  int raster;   // pair-tile rows per raster group
-  int slices;   // K slices of 64
+  int cols;       // N
+  int mt, nt;     // pair-tile rows, tile columns
+  int raster;     // pair-tile rows per raster group
+  int slices;     // K slices of 64
   int parts;
-  int items;    // mt * nt * parts
+  int per_part;   // K slices of a part (the last one's may be fewer)
+  int items;      // mt * nt * parts
+  FastDiv tiles;  // mt * nt
+  FastDiv group;  // tiles of a full raster group
+  FastDiv high;   // raster
+  FastDiv rest;   // pair rows of the last, smaller group
 };
 
 struct ParamsX {
@@ -112,16 +152,19 @@ struct ParamsX {
   CUtensorMap map_b;   // logits: W K-major;  gradients: W MN-major (dx)
   CUtensorMap map_a2;  // gradients: E MN-major (dW)
   CUtensorMap map_b2;  // gradients: s x MN-major (dW)
+  CUtensorMap map_e;   // logits: E, as the epilogue stores it
   int n, d, V;         // tokens of the piece, columns, vocabulary
   int first_dx;        // gradients: grid[0] is dx's (else dW's)
-  int extra;           // gradients: see item_of()
+  int full, rem;       // grid[0]'s items per unit, and the units that get one more
+  int early, extra;    // see item_of()
   Grid grid[2];        // logits: one grid;  gradients: the longer items first
   const int32_t* targets;
   int32_t* err;
   // logits
   uint16_t* E;         // [n][ldv] exponentials (NULL: the loss alone)
   int64_t ldv;
-  float2* pairs;       // [V / 128][ldp] (ref, sum)
+  float* sums;         // [V / 64][ldp] sums of exponentials, negative where the
+  float* refs;         // reference is not 0 but this one
   int64_t ldp;
   float* target_logit;
   float unbias;        // 1 + the mean truncation
@@ -143,6 +186,30 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// The largest of three (numbers before NaN).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two fp32 operations in one instruction, each rounded as the scalar one.
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
 }
 
 __device__ __forceinline__ uint4 pack8x(const float* f) {
@@ -189,37 +256,99 @@ __device__ __forceinline__ void tmem_load64(uint32_t ta, float* v) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Writes 32 rows x 64 columns held one row per lane (v[0..63]) as coalesced
-// 16-byte stores through the warp's two 2 KB slabs: each lane puts its row
-// into both (16-byte piece j of row r at piece j ^ ((r >> 1) & 3)), then each
-// store instruction writes 4 rows x 128 bytes.  Only rows below `rows` and
-// 8-column pieces below `cols` exist (both counted from this corner).
-__device__ __forceinline__ void write_rows64(uint8_t* slabs, int lane, const float* v, uint16_t* out, int64_t ld,
+// Waits for the loads of tmem_ld32; ties the registers to the wait, so that
+// no use moves above it.
+__device__ __forceinline__ void tmem_wait(float (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+        "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+        "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+        "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+        "+f"(r[30]), "+f"(r[31])::"memory");
+}
+
+// M = 256 MMA of the CTA pair, descriptors as (low, high) words; `add`: 0
+// overwrites the accumulator.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(add)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_pair_add(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                             uint32_t idesc) {
+  mma_pair(d, a, a_hi, b, b_hi, idesc, 1u);
+}
+
+__device__ __forceinline__ void st_shared(uint32_t a, const uint4& q) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t a) {
+  uint4 q;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "r"(a)
+               : "memory");
+  return q;
+}
+
+// 32 rows x 32 columns held one row per lane go to global memory as coalesced
+// 16-byte stores through the warp's 2 KB slab: every lane puts its row's
+// 16-byte piece j at piece j ^ ((r >> 1) & 3) of row r (free of bank
+// conflicts), then each store instruction writes 8 rows x 64 bytes.  Only
+// rows below `rows` and 8-column pieces below `cols` exist (both counted from
+// this corner).
+__device__ __forceinline__ void write_rows32(uint32_t slab, int lane, const float* v, uint16_t* out, int64_t ld,
                                              int rows, int cols) {
   const int sw = (lane >> 1) & 3;
+  const int j = lane & 3, r0 = lane >> 2;
+  out += r0 * ld + 8 * j;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    *reinterpret_cast<uint4*>(slabs + lane * 64 + ((j ^ sw) << 4)) = pack8x(v + 8 * j);
-    // the second slab keeps its rows pairwise swapped: the two reads of one
-    // instruction then hit different banks
-    *reinterpret_cast<uint4*>(slabs + SLAB + (lane ^ 1) * 64 + ((j ^ sw) << 4)) = pack8x(v + 32 + 8 * j);
-  }
+  for (int q = 0; q < 4; ++q) st_shared(slab + lane * 64 + ((q ^ sw) << 4), pack8x(v + 8 * q));
   __syncwarp();
-  const int j = lane & 7;
-  const uint8_t* sl = slabs + (j >> 2) * SLAB;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    const uint4 q = *reinterpret_cast<const uint4*>(sl + (r ^ (j >> 2)) * 64 + (((j & 3) ^ ((r >> 1) & 3)) << 4));
-    if (r < rows && 8 * j < cols) *reinterpret_cast<uint4*>(out + r * ld + 8 * j) = q;
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + r0;
+    const uint4 u = ld_shared(slab + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    if (r < rows && 8 * j < cols) *reinterpret_cast<uint4*>(out + 8 * i * ld) = u;
   }
   __syncwarp();
 }
 
-// v[0..63] += k * 64 bf16 values of a row of which `cols` exist.
-__device__ __forceinline__ void add_row64(float* v, const uint16_t* a, float k, int cols) {
+// The same for 64 columns at (x, y) of a tensor map with 64 x 32 boxes, by TMA
+// out of the warp's 4 KB slab in the 128-byte swizzle (16-byte piece j of row
+// r at piece j ^ (r & 7)): no second pass through registers.  The previous
+// store has read the slab (a tile ago) before it is written again; rows and
+// columns past the map are not written.  At d = 64 the logits of 8192 x 32000
+// take 92 us this way, 110 us through registers.
+__device__ __forceinline__ void write_tile(uint32_t slab, int lane, const float* v, const CUtensorMap* map, int x,
+                                           int y) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 8; ++j) st_shared(slab + lane * 128 + ((j ^ (lane & 7)) << 4), pack8x(v + 8 * j));
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(slab), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// v[0..31] += k * 32 bf16 values of a row of which `cols` exist.
+__device__ __forceinline__ void add_row32(float* v, const uint16_t* a, float k, int cols) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
     if (8 * j < cols) {
       float f[8];
       unpack8x(__ldg(reinterpret_cast<const uint4*>(a) + j), f);
@@ -231,9 +360,9 @@ __device__ __forceinline__ void add_row64(float* v, const uint16_t* a, float k, 
 
 // The same with fp32 values and k = 1 (plain loads: the row may be the one
 // the caller overwrites).
-__device__ __forceinline__ void add_row64(float* v, const float* a, int cols) {
+__device__ __forceinline__ void add_row32(float* v, const float* a, int cols) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
     if (4 * j < cols) {
       const float4 q = *(reinterpret_cast<const float4*>(a) + j);
       v[4 * j] += q.x, v[4 * j + 1] += q.y, v[4 * j + 2] += q.z, v[4 * j + 3] += q.w;
@@ -241,9 +370,9 @@ __device__ __forceinline__ void add_row64(float* v, const float* a, int cols) {
   }
 }
 
-__device__ __forceinline__ void store_rows64(float* o, const float* v, int cols) {
+__device__ __forceinline__ void store_row32(float* o, const float* v, int cols) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < 8; ++j)
     if (4 * j < cols)
       *(reinterpret_cast<float4*>(o) + j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
@@ -254,45 +383,50 @@ struct Item {
   int m, n;    // pair-tile row, tile column
   int k0, k1;  // K slices
   int part;
+  bool wide;   // the second sub-tile has columns (else it is left out)
 };
 
 // Tile t of a grid, in groups of `raster` pair rows with the columns outer
 // and the rows inner: pairs working at the same time share B columns while
 // the group's A rows stay in L2.
-__device__ __forceinline__ void tile_at(const Grid& g, int t, Item& it) {
-  const int tiles = g.mt * g.nt;
-  it.part = t / tiles;
-  t -= it.part * tiles;
-  const int per = g.raster * g.nt;
-  const int q = t / per;
-  const int r0 = q * g.raster;
-  const int h = min(g.raster, g.mt - r0);
-  const int l = t - q * per;
-  it.n = l / h;
-  it.m = r0 + l % h;
-  it.k0 = static_cast<int>(static_cast<int64_t>(g.slices) * it.part / g.parts);
-  it.k1 = static_cast<int>(static_cast<int64_t>(g.slices) * (it.part + 1) / g.parts);
+__device__ __forceinline__ void tile_at(const Grid& g, uint32_t t, Item& it) {
+  uint32_t part = 0;
+  if (g.parts > 1) {
+    part = g.tiles(t);
+    t -= part * g.tiles.d;
+  }
+  it.part = part;
+  it.k0 = part * g.per_part;
+  it.k1 = min(it.k0 + g.per_part, g.slices);
+  const uint32_t q = g.group(t);
+  const uint32_t l = t - q * g.group.d;
+  const uint32_t r0 = q * g.raster;
+  const bool last = r0 + g.raster > static_cast<uint32_t>(g.mt);
+  it.n = last ? g.rest(l) : g.high(l);
+  it.m = r0 + l - it.n * (last ? g.rest.d : g.high.d);
+  it.wide = (2 * it.n + 1) * BN < g.cols;
 }
 
 // The j-th item of unit u of U (false: none left).  The items of grid[0],
-// the longer ones, are dealt round; the units that get one fewer of them
-// first take `extra` items of grid[1] each (about the length of one of
+// the longer ones, are dealt round; the `early` units that get one fewer of
+// them first take `extra` items of grid[1] each (about the length of one of
 // grid[0]), then those are dealt round as well, so all units end within about
 // one short item of each other.
 __device__ __forceinline__ bool item_of(const ParamsX& p, int u, int U, int j, Item& it) {
-  const int n0 = p.grid[0].items;
-  const int rem = n0 % U;
-  const int mine = n0 / U + (u < rem ? 1 : 0);
+  const int mine = p.full + (u < p.rem ? 1 : 0);
   if (j < mine) {
     it.dx = p.first_dx;
     tile_at(p.grid[0], u + j * U, it);
     return true;
   }
   j -= mine;
-  const int early = rem > 0 ? U - rem : 0;  // units with one item fewer
   int i;
-  if (early > 0 && u >= rem) i = j < p.extra ? j * early + (u - rem) : p.extra * early + (j - p.extra) * U + u;
-  else i = (early > 0 ? p.extra * early : 0) + j * U + u;
+  if (p.early > 0 && u >= p.rem && j < p.extra) {
+    i = j * p.early + (u - p.rem);
+  } else {
+    if (u >= p.rem && p.early > 0) j -= p.extra;
+    i = p.early * p.extra + j * U + u;
+  }
   if (i >= p.grid[1].items) return false;
   it.dx = !p.first_dx;
   tile_at(p.grid[1], i, it);
@@ -314,14 +448,14 @@ __device__ __forceinline__ int lower_bound(const int32_t* __restrict__ a, int n,
 // E K-major and W MN-major, dW has E and s x MN-major.
 template <bool GRAD, int NS>
 __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constant__ ParamsX p) {
-  using PL = PlanX<NS>;
+  using PL = PlanX<GRAD, NS>;
   constexpr int STAGES = PL::STAGES;
   constexpr uint32_t TMEM_COLS = 512;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* slab_mem = smem + STAGES * PL::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(slab_mem + SLAB_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(slab_mem + PL::SLAB_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -380,7 +514,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
         for (int i = it.k0; i < it.k1; ++i) {
           ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * PL::STAGE);
+          const int subs = NS == 2 && it.wide ? 2 : 1;
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * (A_BYTES + subs * B_BYTES));
           const uint32_t bar = full_pair + 8u * stage;
           uint8_t* sa = smem + stage * PL::STAGE;
           uint8_t* sb = sa + A_BYTES;
@@ -393,6 +528,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           }
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
+            if (s == subs) break;
             if (GRAD) {
               tma_load_2d_pair(sb + s * B_BYTES, mb, bar, n0 + s * BN, k0);
               tma_load_2d_pair(sb + s * B_BYTES + ATOM, mb, bar, n0 + s * BN + 64, k0);
@@ -426,27 +562,32 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       uint32_t phase = 0;
       uint32_t acc = 0, acc_phase = 0;
       bool ok = true;
-      // operand majors of the current item; B is MN-major in both gradients
-      constexpr uint64_t MN_STEP = (UMMA_K * 128) >> 4, K_STEP = (UMMA_K * 2) >> 4;  // 16-byte units
-      constexpr uint64_t B_STEP = GRAD ? MN_STEP : K_STEP;
-      constexpr uint32_t B_LBO = GRAD ? ATOM : 16;
-      uint64_t a_step = K_STEP;
-      uint32_t a_lbo = 16, idesc = idesc_bf16(2 * BM, BN, false, GRAD);
+      // operand majors of the current item; B is MN-major in both gradients.
+      // Of a descriptor only the start address (the low word) moves: by a
+      // stage, a sub-tile or a K step, in 16-byte units.  This thread shares
+      // its scheduler with busy epilogue warps, so it adds little else.
+      constexpr uint32_t MN_STEP = (UMMA_K * 128) >> 4, K_STEP = (UMMA_K * 2) >> 4;
+      constexpr uint32_t B_STEP = GRAD ? MN_STEP : K_STEP;
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + A_BYTES, GRAD ? ATOM : 16, 1024);
+      const uint32_t a_hi = static_cast<uint32_t>(adesc0 >> 32), b_hi = static_cast<uint32_t>(bdesc0 >> 32);
+      uint32_t a_lo = static_cast<uint32_t>(adesc0);
+      const uint32_t b_lo = static_cast<uint32_t>(bdesc0);
+      uint32_t a_step = K_STEP, idesc = idesc_bf16(2 * BM, BN, false, GRAD);
       // one K slice of sub-tile `s` from ring stage st into accumulator d
       auto mmas = [&](uint32_t d, int st, int s, bool first) {
-        const uint32_t sa = smem_u32(smem + st * PL::STAGE);
-        const uint64_t adesc = sdesc_sw128(sa, a_lbo, 1024);
-        const uint64_t bdesc = sdesc_sw128(sa + A_BYTES + s * B_BYTES, B_LBO, 1024);
+        const uint32_t a = a_lo + st * (PL::STAGE >> 4);
+        const uint32_t b = b_lo + st * (PL::STAGE >> 4) + s * (B_BYTES >> 4);
+        mma_pair(d, a, a_hi, b, b_hi, idesc, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 0; kk < BK / UMMA_K; ++kk)
-          mma_bf16_pair(d, adesc + a_step * kk, bdesc + B_STEP * kk, idesc, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 1; kk < BK / UMMA_K; ++kk) mma_pair_add(d, a + a_step * kk, a_hi, b + B_STEP * kk, b_hi, idesc);
       };
       Item it;
       for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
         const int kit = it.k1 - it.k0;
         if (GRAD) {
           a_step = it.dx ? K_STEP : MN_STEP;
-          a_lbo = it.dx ? 16 : ATOM;
+          a_lo = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem), it.dx ? 16 : ATOM, 1024));
           idesc = it.dx ? idesc_bf16(2 * BM, BN, false, true) : idesc_bf16(2 * BM, BN, true, true);
         }
         if (NS == 2) {
@@ -456,6 +597,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           ok = mbar_wait_cluster(tempty, acc_phase ^ 1u, abort_flag);
           if (!ok) break;
           fence_after_sync();
+          // (without a second sub-tile its columns are still waited for below, so
+          // that the barrier's phases keep step with the tiles)
           bool free1 = false;
           int held = 0;
           const int hstage = stage;
@@ -472,6 +615,14 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
             if (!ok) break;
             fence_after_sync();
             mmas(tmem_base, stage, 0, i == 0);
+            if (!it.wide) {
+              mma_commit_pair(empty + stage);
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+              continue;
+            }
             if (!free1) free1 = mbar_try_wait_cluster(tempty + 1, acc_phase ^ 1u);
             if (!free1 && held + 1 == STAGES) {
               ok = mbar_wait_cluster(tempty + 1, acc_phase ^ 1u, abort_flag);
@@ -492,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
             }
           }
           if (!ok) break;
-          if (held > 0) {
+          if (held > 0 || !it.wide) {
             ok = mbar_wait_cluster(tempty + 1, acc_phase ^ 1u, abort_flag);
             if (!ok) break;
             fence_after_sync();
@@ -531,8 +682,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
   } else {
     // -------------------------------------------------------------- epilogue
     const int quad = warp & 3;                 // TMEM lanes 32 quad .. 32 quad + 31
-    const int half = (warp - 2) >> 2;          // columns 128 half .. + 127 of a sub-tile
-    uint8_t* const slabs = slab_mem + (warp - 2) * 2 * SLAB;
+    const int part = (warp - 2) >> 2;          // columns 64 part .. + 63 of a sub-tile
+    const uint32_t slab = smem_u32(slab_mem + (warp - 2) * PL::SLAB);
     const uint32_t tempty_pair = dsmem_addr(smem_u32(tempty), 0);
     uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
@@ -566,98 +717,117 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int c0 = (it.n * NS + s) * BN + half * (BN / 2);  // this warp's first column
+        const int c = (it.n * NS + s) * BN + part * 64;  // this warp's first column
         if (NS == 1 || s == 0) {
           ok = mbar_wait_cluster(tfull + acc, acc_phase, abort_flag);
           if (!ok) break;
           __syncwarp();
         }
-        fence_after_sync();
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + half * (BN / 2);
-        if (!GRAD) {
-          float v[128];
-          tmem_load64(tb, v);
-          tmem_load64(tb + 64, v + 64);
+        if (NS == 2 && s == 1 && !it.wide) {
           release();
-          if (c0 >= p.V) continue;  // past the vocabulary: no such group
-          const bool here = static_cast<unsigned>(target - c0) < 128u;
+          continue;
+        }
+        fence_after_sync();
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + part * 64;
+        if (!GRAD) {
+          float v[64];
+          tmem_load64(tb, v);
+          release();  // all of this warp's columns are in registers
+          const int cols = p.V - c;  // words from here on
+          if (cols <= 0) continue;
+          const int mine = target - c;  // the target's column, if it is one of these
+          const bool here = static_cast<unsigned>(mine) < 64u;
           if (here) {
             float l = 0.f;
 #pragma unroll
-            for (int q = 0; q < 128; ++q) l = q == target - c0 ? v[q] : l;
+            for (int q = 0; q < 64; ++q) l = q == mine ? v[q] : l;
             p.target_logit[row] = l * p.unbias;
           }
-          if (c0 + 128 > p.V) {
+          if (cols < 64) {
 #pragma unroll
-            for (int q = 0; q < 128; ++q)
-              if (c0 + q >= p.V) v[q] = -INFINITY;
+            for (int q = 0; q < 64; ++q) v[q] = q < cols ? v[q] : -INFINITY;
           }
-          float top = v[0];
+          float top = v[0], top2 = v[1];
 #pragma unroll
-          for (int q = 1; q < 128; ++q) top = fmaxf(top, v[q]);
-          const float ref = (top > kRefHigh || (top < kRefLow && top != -INFINITY)) ? top * p.unbias : 0.f;
-          const float k = kLog2e * p.unbias, bias = -ref * kLog2e;
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-          for (int q = 0; q < 128; q += 4) {
-            v[q] = ex2(fmaf(v[q], k, bias));
-            v[q + 1] = ex2(fmaf(v[q + 1], k, bias));
-            v[q + 2] = ex2(fmaf(v[q + 2], k, bias));
-            v[q + 3] = ex2(fmaf(v[q + 3], k, bias));
-            s0 += v[q];
-            s1 += v[q + 1];
-            s2 += v[q + 2];
-            s3 += v[q + 3];
+          for (int q = 2; q < 62; q += 4) {
+            top = max3(top, v[q], v[q + 1]);
+            top2 = max3(top2, v[q + 2], v[q + 3]);
           }
-          if (row < p.n) p.pairs[static_cast<int64_t>(c0 / kGroup) * p.ldp + row] = make_float2(ref, (s0 + s1) + (s2 + s3));
+          top = max3(top, max3(top2, v[62], v[63]), -INFINITY);
+          const bool shift = top > kRefHigh || (top < kRefLow && top != -INFINITY);
+          const float ref = shift ? top * p.unbias : 0.f;
+          const float2 k2 = make_float2(kLog2e * p.unbias, kLog2e * p.unbias);
+          const float2 bias2 = make_float2(-ref * kLog2e, -ref * kLog2e);
+          float2 sum2 = make_float2(0.f, 0.f), sum3 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 64; q += 4) {
+            float2 a = f2_fma(make_float2(v[q], v[q + 1]), k2, bias2);
+            float2 b = f2_fma(make_float2(v[q + 2], v[q + 3]), k2, bias2);
+            a = make_float2(ex2(a.x), ex2(a.y));
+            b = make_float2(ex2(b.x), ex2(b.y));
+            sum2 = f2_add(sum2, a);
+            sum3 = f2_add(sum3, b);
+            v[q] = a.x, v[q + 1] = a.y, v[q + 2] = b.x, v[q + 3] = b.y;
+          }
+          if (row < p.n) {
+            // a sum belongs to the reference 0, or, with its sign set, to one in refs
+            const float sum = (sum2.x + sum2.y) + (sum3.x + sum3.y);
+            const int64_t at = static_cast<int64_t>(c / kGroup) * p.ldp + row;
+            p.sums[at] = shift ? -fabsf(sum) : fabsf(sum);
+            if (shift) p.refs[at] = ref;
+          }
           if (p.E) {
             if (here) {  // the target's own element is added in fp32 by the gradients
 #pragma unroll
-              for (int q = 0; q < 128; ++q)
-                if (q == target - c0) v[q] = 0.f;
+              for (int q = 0; q < 64; ++q) v[q] = q == mine ? 0.f : v[q];
             }
-            uint16_t* o = p.E + static_cast<int64_t>(row0) * p.ldv + c0;
-            const int cols = static_cast<int>(p.ldv) - c0;
-            write_rows64(slabs, lane, v, o, p.ldv, rows, cols);
-            write_rows64(slabs, lane, v + 64, o + 64, p.ldv, rows, cols - 64);
+            if (PL::TMA_OUT) {
+              if (rows > 0) write_tile(slab, lane, v, &p.map_e, c, row0);
+            } else {
+              uint16_t* o = p.E + static_cast<int64_t>(row0) * p.ldv + c;  // ldv is a multiple of 64
+              write_rows32(slab, lane, v, o, p.ldv, rows, 32);
+              write_rows32(slab, lane, v + 32, o + 32, p.ldv, rows, 32);
+            }
           }
         } else {
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            float v[64];
-            __syncwarp();  // the lanes took different numbers of tokens
-            tmem_load64(tb + 64 * h, v);
-            if (h == 1) release();
-            const int c = c0 + 64 * h;
-            const int cols = p.d - c;  // columns that exist from here on (a multiple of 8)
+            float v[32];
+            __syncwarp();  // dW: the lanes took different numbers of tokens
+            tmem_ld32(tb + 32 * h, v);
+            tmem_wait(v);
+            if (h == 1) release();  // the last of this warp's columns are in registers
+            const int ch = c + 32 * h;
+            const int cols = p.d - ch;  // columns that exist from here on
             if (cols <= 0) continue;
             if (it.dx) {
               if (p.dx_part) {
-                store_rows64(p.dx_part + (static_cast<int64_t>(it.part) * p.n + row) * p.d + c, v, row < M ? cols : 0);
+                store_row32(p.dx_part + (static_cast<int64_t>(it.part) * p.n + row) * p.d + ch, v, row < M ? cols : 0);
               } else {
 #pragma unroll
-                for (int q = 0; q < 64; ++q) v[q] = cf.x == 0.f ? 0.f : v[q] * cf.x;
-                if (cf.y != 0.f) add_row64(v, p.W + static_cast<int64_t>(target) * p.d + c, cf.y, cols);
-                write_rows64(slabs, lane, v, p.dx + static_cast<int64_t>(row0) * p.d + c, p.d, rows, cols);
+                for (int q = 0; q < 32; ++q) v[q] = cf.x == 0.f ? 0.f : v[q] * cf.x;
+                if (cf.y != 0.f) add_row32(v, p.W + static_cast<int64_t>(target) * p.d + ch, cf.y, cols);
+                write_rows32(slab, lane, v, p.dx + static_cast<int64_t>(row0) * p.d + ch, p.d, rows, cols);
               }
             } else {
               if (tokens > kDirect) {
-                for (int q = 0; q < tokens; q += kRun)
-                  add_row64(v, p.runs + static_cast<int64_t>(first + q) * p.d + c, cols);
+                for (int q = first; q < first + tokens; q = (q / kRun + 1) * kRun)
+                  add_row32(v, p.runs + static_cast<int64_t>(q) * p.d + ch, cols);
               } else {
                 for (int q = 0; q < tokens; ++q) {
                   const int t = __ldg(p.order + first + q);
-                  add_row64(v, p.x + static_cast<int64_t>(t) * p.d + c, __ldg(&p.coef[t].y), cols);
+                  add_row32(v, p.x + static_cast<int64_t>(t) * p.d + ch, __ldg(&p.coef[t].y), cols);
                 }
               }
-              if (p.dw_add && row < M) add_row64(v, p.dw_add + static_cast<int64_t>(row) * p.d + c, cols);
-              if (p.dw32) store_rows64(p.dw32 + static_cast<int64_t>(row) * p.d + c, v, row < M ? cols : 0);
-              else write_rows64(slabs, lane, v, p.dw + static_cast<int64_t>(row0) * p.d + c, p.d, rows, cols);
+              if (p.dw_add && row < M) add_row32(v, p.dw_add + static_cast<int64_t>(row) * p.d + ch, cols);
+              if (p.dw32) store_row32(p.dw32 + static_cast<int64_t>(row) * p.d + ch, v, row < M ? cols : 0);
+              else write_rows32(slab, lane, v, p.dw + static_cast<int64_t>(row0) * p.d + ch, p.d, rows, cols);
             }
           }
         }
       }
     }
+    if (PL::TMA_OUT && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // all of it written
     if (!ok && lane == 0) {
       dmoe::raise_error(p.err, DMOE_SITE_GEMM_WAIT | DMOE_ERR_TIMEOUT);
       *abort_flag = 1;
@@ -682,39 +852,63 @@ __device__ __forceinline__ int key_of(int32_t target, int V, int ignore) {
 }
 
 constexpr int kSortWarps = 8;
+constexpr int kSortChunk = 2048;
 
-// Stable sort of the piece's targets (those that do not count last): each
-// warp counts the tokens before its own.  n^2 comparisons, 8 us at 8192
-// tokens, a sixteenth of a percent of that many rows' products.  Block 0 also
-// counts the targets of the whole call that count.
+// Stable sort of the piece's targets (those that do not count last) by
+// counting: each warp counts the tokens that come before two of its own, n^2
+// comparisons in all: 15 us at 8192 tokens.  skey[r], order[r]: the key
+// and the token at position r.  Block 0 also counts the targets of the whole
+// call that count.
 __global__ void __launch_bounds__(32 * kSortWarps)
     sort_targets_kernel(const int32_t* __restrict__ targets, int n, int V, int ignore, int32_t* __restrict__ skey,
                         int32_t* __restrict__ order, const int32_t* __restrict__ all, int T,
                         int32_t* __restrict__ count) {
+  __shared__ int4 keys[kSortChunk / 4];
   __shared__ int sh[kSortWarps];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kSortWarps + warp;
-  if (t < n) {
-    const int key = key_of(__ldg(targets + t), V, ignore);
-    int before = 0;
-#pragma unroll 8
-    for (int u = lane; u < n; u += 32) {
-      const int k = key_of(__ldg(targets + u), V, ignore);
-      before += (k < key || (k == key && u < t)) ? 1 : 0;
+  const int t0 = 2 * (blockIdx.x * kSortWarps + warp), t1 = t0 + 1;  // in one group of four
+  const int key0 = t0 < n ? key_of(__ldg(targets + t0), V, ignore) : 0;
+  const int key1 = t1 < n ? key_of(__ldg(targets + t1), V, ignore) : 0;
+  int r0 = 0, r1 = 0;
+  for (int base = 0; base < n; base += kSortChunk) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kSortChunk; i += 32 * kSortWarps)  // past the end: after every key
+      reinterpret_cast<int*>(keys)[i] = base + i < n ? key_of(__ldg(targets + base + i), V, ignore) : V + 1;
+    __syncthreads();
+    const int split = (t0 - base) >> 2;  // groups before the tokens' own also count equal keys
+#pragma unroll 4
+    for (int i = lane; i < kSortChunk / 4; i += 32) {
+      const int4 k = keys[i];
+      const int eq = i < split ? 1 : 0;
+      const int l0 = key0 + eq, l1 = key1 + eq;
+      r0 += (k.x < l0) + (k.y < l0) + (k.z < l0) + (k.w < l0);
+      r1 += (k.x < l1) + (k.y < l1) + (k.z < l1) + (k.w < l1);
     }
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) {
-      skey[before] = key;
-      order[before] = t;
+  }
+  // equal keys earlier in the tokens' own group of four
+  const int u = (t0 & ~3) + lane;
+  if (lane < 3 && u < n) {
+    const int k = key_of(__ldg(targets + u), V, ignore);
+    r0 += u < t0 && k == key0;
+    r1 += u < t1 && k == key1;
+  }
+  r0 = __reduce_add_sync(0xffffffffu, r0);
+  r1 = __reduce_add_sync(0xffffffffu, r1);
+  if (lane == 0 && t0 < n) {
+    skey[r0] = key0;
+    order[r0] = t0;
+    if (t1 < n) {
+      skey[r1] = key1;
+      order[r1] = t1;
     }
   }
   if (blockIdx.x != 0 || !count) return;
   int c = 0;
 #pragma unroll 8
-  for (int u = threadIdx.x; u < T; u += 32 * kSortWarps) c += key_of(__ldg(all + u), V, ignore) < V;
+  for (int i = threadIdx.x; i < T; i += 32 * kSortWarps) c += key_of(__ldg(all + i), V, ignore) < V;
   c = __reduce_add_sync(0xffffffffu, c);
   if (lane == 0) sh[warp] = c;
   __syncthreads();
@@ -724,43 +918,59 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   }
 }
 
-// runs[r] = sum of c_t x_t over the up to kRun tokens at positions r .. of a
-// word with more than kDirect tokens, r - (the word's first position) a
-// multiple of kRun.  One warp per position and kRunCols columns.
-constexpr int kRunCols = 512;
-__global__ void __launch_bounds__(256)
+// Sums of c_t x_t for words with more than kDirect tokens, in blocks of kRun =
+// 32 positions of the sorted order: runs[r], r a word's first position or a
+// multiple of 32, sums its tokens from there to the end of the block.  (A
+// word's few tokens on both sides of a block's edge get theirs as well.)  One
+// warp per block of positions and kRunCols columns.
+constexpr int kRunCols = 256;
+static_assert(kRun == 32, "a lane per position");
+__global__ void __launch_bounds__(128)
     target_runs_kernel(const uint16_t* __restrict__ x, int n, int d, int V, const int32_t* __restrict__ skey,
                        const int32_t* __restrict__ order, const float2* __restrict__ coef, float* __restrict__ runs) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= n) return;
-  const int key = __ldg(skey + r);
-  if (key >= V) return;
-  const int first = lower_bound(skey, n, key);
-  const int tokens = lower_bound(skey, n, key + 1) - first;
-  if (tokens <= kDirect || (r - first) % kRun != 0) return;
-  const int m = min(kRun, first + tokens - r);
-  const int mine = lane < m ? __ldg(order + r + lane) : 0;  // kRun tokens, one per lane
-  const float cm = lane < m ? __ldg(&coef[mine].y) : 0.f;
-#pragma unroll
-  for (int i = 0; i < kRunCols / 256; ++i) {
-    const int c = blockIdx.y * kRunCols + i * 256 + lane * 8;
+  const int base = (blockIdx.x * 4 + (threadIdx.x >> 5)) * kRun;
+  if (base >= n) return;
+  const int r = base + lane;
+  const int key = r < n ? __ldg(skey + r) : -1;
+  const int before = r > 0 && r < n ? __ldg(skey + r - 1) : -1;
+  const int after = base + kRun < n ? __ldg(skey + base + kRun) : -1;
+  const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 || key != before);
+  const int token = r < n && key < V ? __ldg(order + r) : 0;
+  const float weight = r < n && key < V ? __ldg(&coef[token].y) : 0.f;
+  const int c = blockIdx.y * kRunCols + lane * 8;
+  const uint16_t* col = x + (c < d ? c : 0);
+  for (uint32_t left = starts; left;) {
+    const int s = __ffs(left) - 1;  // a word's positions s .. e - 1 of this block
+    left &= left - 1;
+    const int e = left ? __ffs(left) - 1 : 32;
+    const int k = __shfl_sync(0xffffffffu, key, s);
+    const bool crosses = (s == 0 && __shfl_sync(0xffffffffu, before, 0) == k) || (e == 32 && after == k);
+    if (k < 0 || k >= V || (e - s <= kDirect && !crosses)) continue;
     float acc[8] = {};
-#pragma unroll 8
-    for (int q = 0; q < m; ++q) {
-      const int t = __shfl_sync(0xffffffffu, mine, q);
-      const float k = __shfl_sync(0xffffffffu, cm, q);
-      if (c < d) {
-        float f[8];
-        unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
+#pragma unroll 1
+    for (int q = s; q < e; q += 8) {  // eight rows in flight
+      uint4 u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = fmaf(k, f[j], acc[j]);
+      for (int j = 0; j < 8; ++j) {
+        const int t = __shfl_sync(0xffffffffu, token, min(q + j, 31));
+        u[j] = __ldg(reinterpret_cast<const uint4*>(col + static_cast<int64_t>(t) * d));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = __shfl_sync(0xffffffffu, weight, min(q + j, 31));
+        float f[8];
+        unpack8x(u[j], f);
+        if (q + j < e) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+        }
       }
     }
     if (c < d) {
-      float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(r) * d + c);
+      float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(base + s) * d + c);
       o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
       o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     }
@@ -784,7 +994,8 @@ __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
 }
 
 struct ParamsR {
-  const float2* pairs;
+  const float* sums;
+  const float* refs;
   int64_t ldp;
   int groups;
   const float* target_logit;
@@ -804,7 +1015,7 @@ struct ParamsR {
 
 // 32 rows per block: the row's groups by 32 slices, then a warp per row for
 // s x and, where a row's groups have different references, its E.
-__global__ void __launch_bounds__(kStatRows * kStatSlices) row_stats_kernel(const ParamsR p) {
+__global__ void __launch_bounds__(kStatRows * kStatSlices, 2) row_stats_kernel(const ParamsR p) {
   __shared__ float4 sh[kStatSlices][kStatRows];
   __shared__ float sh_s[kStatRows], sh_r[kStatRows];
   __shared__ int sh_fix[kStatRows];
@@ -815,12 +1026,22 @@ __global__ void __launch_bounds__(kStatRows * kStatSlices) row_stats_kernel(cons
   const int t = blockIdx.x * kStatRows + lane;
   float R = -INFINITY, S = 0.f, low = INFINITY, high = -INFINITY;
   if (t < p.n) {
-#pragma unroll 4
-    for (int g = slice; g < p.groups; g += kStatSlices) {
-      const float2 q = __ldg(p.pairs + g * p.ldp + t);
-      join(R, S, q.x, q.y);
-      low = fminf(low, q.x);
-      high = fmaxf(high, q.x);
+    for (int g0 = slice; g0 < p.groups; g0 += 4 * kStatSlices) {
+      float s[4];  // four loads in flight
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int g = g0 + i * kStatSlices;
+        s[i] = g < p.groups ? __ldg(p.sums + g * p.ldp + t) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int g = g0 + i * kStatSlices;
+        if (g >= p.groups) break;
+        const float r = signbit(s[i]) ? __ldg(p.refs + g * p.ldp + t) : 0.f;
+        join(R, S, r, fabsf(s[i]));
+        low = fminf(low, r);
+        high = fmaxf(high, r);
+      }
     }
   }
   sh[slice][lane] = make_float4(R, S, low, high);
@@ -874,20 +1095,14 @@ __global__ void __launch_bounds__(kStatRows * kStatSlices) row_stats_kernel(cons
     const float top = sh_r[slice];
     uint16_t* e = p.E + static_cast<int64_t>(row) * p.ldv;
     for (int g = 0; g < p.groups; ++g) {
-      const float r = __ldg(&p.pairs[g * p.ldp + row].x);
-      const int c = g * kGroup + lane * 4;
-      if ((fix == 1 && r == top) || c >= p.ldv) continue;
+      const float r = signbit(__ldg(p.sums + g * p.ldp + row)) ? __ldg(p.refs + g * p.ldp + row) : 0.f;
+      if (fix == 1 && r == top) continue;
       const float k = fix == 2 ? 0.f : expf(r - top);
-      uint2 u = *reinterpret_cast<const uint2*>(e + c);
-      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float2 f = __bfloat1622float2(h[j]);
-        f.x = fix == 2 ? 0.f : f.x * k;
-        f.y = fix == 2 ? 0.f : f.y * k;
-        h[j] = __floats2bfloat162_rn(f.x, f.y);
-      }
-      *reinterpret_cast<uint2*>(e + c) = u;
+      __nv_bfloat162* u = reinterpret_cast<__nv_bfloat162*>(e + g * kGroup) + lane;
+      float2 f = __bfloat1622float2(*u);
+      f.x = fix == 2 ? 0.f : f.x * k;
+      f.y = fix == 2 ? 0.f : f.y * k;
+      *u = __floats2bfloat162_rn(f.x, f.y);
     }
   }
 }
@@ -921,12 +1136,79 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------- host side
 
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+Grid make_grid(int M, int N, int K, int raster, int parts = 1, int width = 2 * BN) {
+  Grid g{};
+  g.cols = N;
+  g.mt = ceil_div(M, 2 * BM);
+  g.nt = ceil_div(N, width);
+  g.raster = raster;
+  g.slices = ceil_div(K, BK);
+  g.per_part = ceil_div(g.slices, parts);
+  g.parts = ceil_div(g.slices, g.per_part);  // none of them empty
+  g.items = g.mt * g.nt * g.parts;
+  g.tiles.set(static_cast<uint32_t>(g.mt) * g.nt);
+  g.group.set(static_cast<uint32_t>(raster) * g.nt);
+  g.high.set(raster);
+  g.rest.set(g.mt % raster ? g.mt % raster : raster);
+  return g;
+}
+
+// K slices per item of a grid (its longest).
+int item_slices(const Grid& g) { return g.per_part; }
+
+// Deals the items of two grids (the second may have none) to U units: the
+// longer ones into grid[0], and how many of the shorter ones the units with
+// one long item fewer take first (item_of()).  Returns the slices of the unit
+// that has most.
+int64_t deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
+  p.first_dx = gx.items > 0 && (gw.items == 0 || item_slices(gx) >= item_slices(gw));
+  p.grid[0] = p.first_dx ? gx : gw;
+  p.grid[1] = p.first_dx ? gw : gx;
+  const int n0 = p.grid[0].items, n1 = p.grid[1].items;
+  const int64_t l0 = item_slices(p.grid[0]), l1 = n1 > 0 ? item_slices(p.grid[1]) : 1;
+  p.full = n0 / U;
+  p.rem = n0 % U;
+  p.early = p.rem > 0 && n1 > 0 ? U - p.rem : 0;
+  p.extra = p.early > 0 ? static_cast<int>((l0 + l1 / 2) / l1) : 0;
+  const int64_t taken = std::min<int64_t>(n1, static_cast<int64_t>(p.early) * p.extra);
+  const int64_t rest = n1 - taken, round = rest / U, left = rest % U;
+  const int64_t a = (p.full + (p.rem > 0)) * l0 + (round + (left > 0)) * l1;
+  const int64_t b = p.early == 0 ? 0 : p.full * l0 + (ceil_div(taken, p.early) + round + (left > p.rem)) * l1;
+  return std::max(a, b);
+}
+
+// Parts of dx's sum over the vocabulary.  dx has few tiles of V / 64 slices
+// each; in one part the last of them can outlast everything else (512
+// tokens: 8 tiles for 76 pairs).  Takes the count whose busiest unit is
+// shortest, charging the fp32 sums that parts write and read back in slices
+// (about 0.5 us each): 12 bytes an element at 6.5 TB/s, and a launch.
+int dx_parts(int n, int d, int V, bool dw) {
+  ParamsX p{};
+  const Grid gw = dw ? make_grid(V, d, n, 1) : Grid{};
+  int best = 1;
+  int64_t best_cost = -1;
+  for (int s = 1; s <= kMaxSplit; ++s) {
+    const Grid gx = make_grid(n, d, V, 1, s);
+    if (s > 1 && gx.slices / s < 8) break;
+    int64_t cost = deal(p, gx, gw, kUnits);
+    if (s > 1) cost += 10 + static_cast<int64_t>(s) * n * d / 270000;
+    if (best_cost < 0 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // Opt-in shared memory and the number of 2-CTA clusters that fit, once per
 // instantiation and device.
 template <bool GRAD, int NS>
-dmoe_status launch_head(const ParamsX& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
+dmoe_status launch_head(ParamsX& p, const Grid& ga, const Grid& gb, const dmoe::DeviceInfo& di, cudaStream_t st) {
   auto kern = head_kernel<GRAD, NS>;
-  const size_t smem = PlanX<NS>::SMEM;
+  const size_t smem = PlanX<GRAD, NS>::SMEM;
   static std::atomic<int> clusters[64];
   int n = clusters[di.device].load(std::memory_order_acquire);
   if (n == 0) {
@@ -948,58 +1230,21 @@ dmoe_status launch_head(const ParamsX& p, const dmoe::DeviceInfo& di, cudaStream
     if (n < 1) return DMOE_ERR_UNSUPPORTED;
     clusters[di.device].store(n, std::memory_order_release);
   }
-  const int64_t items = static_cast<int64_t>(p.grid[0].items) + p.grid[1].items;
-  const int grid = 2 * static_cast<int>(std::min<int64_t>(n, items));
-  cudaError_t e = dmoe::launch_pdl_cluster(kern, dim3(grid), dim3(kThreadsX), smem, st, 2, p);
+  const int units = static_cast<int>(std::min<int64_t>(n, static_cast<int64_t>(ga.items) + gb.items));
+  deal(p, ga, gb, units);
+  cudaError_t e = dmoe::launch_pdl_cluster(kern, dim3(2 * units), dim3(kThreadsX), smem, st, 2, p);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
 }
 
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
-
-Grid make_grid(int M, int N, int K, int raster, int parts = 1) {
-  Grid g{};
-  g.mt = ceil_div(M, 2 * BM);
-  g.nt = ceil_div(N, 2 * BN);
-  g.raster = raster;
-  g.slices = ceil_div(K, BK);
-  g.parts = parts;
-  g.items = g.mt * g.nt * parts;
-  return g;
-}
-
-// Parts of dx's sum over the vocabulary.  dx has few tiles of V / 64 slices
-// each; in one part the last round of them can outlast everything else (512
-// tokens: 8 tiles for 76 pairs).  Takes the count whose longest unit is
-// shortest, in slices, charging each part the fp32 sums it writes and reads
-// back (a 256 x 512 tile's cost about two slices).
-int dx_parts(int n, int d, int V, bool dw) {
-  const Grid x = make_grid(n, d, V, 1), w = make_grid(V, d, n, 1);
-  const int64_t total = static_cast<int64_t>(x.items) * x.slices + (dw ? static_cast<int64_t>(w.items) * w.slices : 0);
-  int best = 1;
-  int64_t best_cost = -1;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || x.slices / s >= 8); ++s) {
-    const int64_t items = static_cast<int64_t>(x.items) * s;
-    const int64_t longest = ceil_div(items, kUnits) * static_cast<int64_t>(ceil_div(x.slices, s));
-    int64_t cost = std::max<int64_t>(ceil_div(total, kUnits), longest);
-    if (s > 1) cost += 8 + ceil_div(2 * items, kUnits);
-    if (best_cost < 0 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
-}
-
 // Bytes of a workspace, in order (each part 256-byte aligned).
 struct Layout {
   int64_t piece;   // tokens per piece
-  int64_t ldp;     // row pitch of the (ref, sum) pairs
+  int64_t ldp;     // row pitch of sums and refs
   int64_t ldv;     // row pitch of the exponentials
   int64_t groups;
-  size_t count, pairs, target_logit, coef, skey, order, xs, runs, part, acc, E, total;
+  size_t count, sums, refs, target_logit, coef, skey, order, xs, runs, part, acc, E, total;
 };
 
 Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
@@ -1017,7 +1262,8 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
   };
   const size_t rows = static_cast<size_t>(l.piece);
   l.count = take(256);
-  l.pairs = take(static_cast<size_t>(l.groups * l.ldp) * sizeof(float2));
+  l.sums = take(static_cast<size_t>(l.groups * l.ldp) * sizeof(float));
+  l.refs = take(static_cast<size_t>(l.groups * l.ldp) * sizeof(float));
   l.target_logit = take(rows * sizeof(float));
   if (grad) {
     l.coef = take(rows * sizeof(float2));
@@ -1091,7 +1337,8 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
   uint8_t* base = static_cast<uint8_t*>(ws);
   auto at = [&](size_t off) { return grad ? base + off : nullptr; };
   int32_t* count = reinterpret_cast<int32_t*>(base + l.count);
-  float2* pairs = reinterpret_cast<float2*>(base + l.pairs);
+  float* sums = reinterpret_cast<float*>(base + l.sums);
+  float* refs = reinterpret_cast<float*>(base + l.refs);
   float* target_logit = reinterpret_cast<float*>(base + l.target_logit);
   float2* coef = reinterpret_cast<float2*>(at(l.coef));
   int32_t* skey = reinterpret_cast<int32_t*>(at(l.skey));
@@ -1107,8 +1354,9 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     const uint16_t* xp = x + t0 * d;
     const int32_t* tp = targets + t0;
     if (grad)
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(sort_targets_kernel, dim3(ceil_div(n, kSortWarps)), dim3(32 * kSortWarps), 0, st,
-                                       tp, n, V, ignore_index, skey, order, targets, T, t0 == 0 ? count : nullptr));
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(sort_targets_kernel, dim3(ceil_div(n, 2 * kSortWarps)), dim3(32 * kSortWarps), 0,
+                                       st, tp, n, V, ignore_index, skey, order, targets, T,
+                                       t0 == 0 ? count : nullptr));
     ParamsX p{};
     p.n = n, p.d = d, p.V = V;
     p.targets = tp;
@@ -1118,16 +1366,18 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       ParamsX q = p;
       if (!dmoe::make_map(&q.map_a, xp, n, d, BK, BM) || !dmoe::make_map(&q.map_b, w, V, d, BK, BN / 2))
         return DMOE_ERR_CUDA;
-      q.grid[0] = make_grid(n, V, d, 16);
+      if (grad && !dmoe::make_map(&q.map_e, E, n, l.ldv, 64, 32)) return DMOE_ERR_CUDA;
       q.E = E;
-      q.pairs = pairs;
+      q.sums = sums;
+      q.refs = refs;
       q.ldp = l.ldp;
       q.target_logit = target_logit;
       q.unbias = 1.f + static_cast<float>(ceil_div(d, UMMA_K)) * kTruncation;
-      DMOE_TRY((launch_head<false, 2>(q, di, st)));
+      if (d <= kNarrowD) DMOE_TRY((launch_head<false, 1>(q, make_grid(n, V, d, 16, 1, BN), Grid{}, di, st)));
+      else DMOE_TRY((launch_head<false, 2>(q, make_grid(n, V, d, 16), Grid{}, di, st)));
     }
     ParamsR r{};
-    r.pairs = pairs, r.ldp = l.ldp, r.groups = static_cast<int>(l.groups);
+    r.sums = sums, r.refs = refs, r.ldp = l.ldp, r.groups = static_cast<int>(l.groups);
     r.target_logit = target_logit, r.targets = tp;
     r.n = n, r.d = d, r.V = V, r.ignore = ignore_index;
     r.d_loss = d_loss ? d_loss + t0 : nullptr;
@@ -1141,8 +1391,8 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
                                      st, r));
     if (!grad) continue;
     if (dw)
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 8), ceil_div(d, kRunCols)), dim3(256), 0,
-                                       st, xp, n, d, V, static_cast<const int32_t*>(skey),
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
+                                       dim3(128), 0, st, xp, n, d, V, static_cast<const int32_t*>(skey),
                                        static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs));
     const int parts = dx ? dx_parts(n, d, V, dw != nullptr) : 1;
     Grid gx{}, gw{};
@@ -1157,16 +1407,9 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
         return DMOE_ERR_CUDA;
       gw = make_grid(V, d, n, 1);
     }
-    p.first_dx = gx.items > 0 && (gw.items == 0 || gx.slices / gx.parts >= gw.slices);
-    p.grid[0] = p.first_dx ? gx : gw;
-    p.grid[1] = p.first_dx ? gw : gx;
-    if (p.grid[1].items > 0) {
-      const int s1 = std::max(1, p.grid[1].slices / p.grid[1].parts);
-      p.extra = (p.grid[0].slices / p.grid[0].parts + s1 / 2) / s1;
-    }
     p.coef = coef, p.W = w, p.x = xp;
     p.dx = dx ? dx + t0 * d : nullptr;
-    p.dx_part = parts > 1 ? part : nullptr;
+    p.dx_part = gx.parts > 1 ? part : nullptr;
     p.skey = skey, p.order = order, p.runs = runs;
     const bool last = t0 + n >= T;
     if (dw_f32) {
@@ -1177,10 +1420,10 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       p.dw32 = last ? nullptr : acc;
       p.dw_add = t0 > 0 ? acc : nullptr;
     }
-    DMOE_TRY((launch_head<true, 2>(p, di, st)));
-    if (parts > 1)
+    DMOE_TRY((launch_head<true, 2>(p, gx, gw, di, st)));
+    if (gx.parts > 1)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(join_dx_kernel, dim3(ceil_div(static_cast<int64_t>(n) * (d / 8), 256)), dim3(256),
-                                       0, st, static_cast<const float*>(part), parts, n, d,
+                                       0, st, static_cast<const float*>(part), gx.parts, n, d,
                                        static_cast<const float2*>(coef), tp, w, dx + t0 * d));
   }
   return DMOE_OK;
