@@ -128,16 +128,26 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the handle of the current stream without the Stream object around it
+# (torch.cuda.current_stream() takes 3 us on the host of a GB300)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _need(t, dtype, name, numel=None, shape=None):
+    if (t is not None and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (numel is None or t.numel() >= numel)):
+        return t  # the usual case; what follows only says what is wrong
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -419,6 +429,8 @@ def combine_backward(dy, y_perm, src_of_row, gate_w, P_dev, k: int, P_max: int, 
 
 def _rows(t, dtype, name, T, d):
     """Row pitch of a [T, d] tensor whose rows may lie apart."""
+    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == (T, d) and t.is_contiguous():
+        return d
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:

@@ -8,14 +8,15 @@
 // last element), so the floor is 3 passes over the bytes, 2 when the set
 // stays in L2.  Two launches: sums of squares, one double per block; then
 // every block adds the blocks' sums in the same order (the result does not
-// depend on which block ran when) and scales its share.  A block walks its
-// share forwards in the first launch and backwards in the second, so that
-// what it read last is still in L2 when it reads it again.
+// depend on which block ran when) and scales.  The chunks are walked forwards
+// in the first launch and backwards in the second, so that what was read last
+// is still in L2 when it is read again, and both times by all blocks side by
+// side (runs of their own per block: DISCARD).
 //
 // The tensors are cut into chunks of kChunk elements, counted from each
 // tensor's address rounded down to 16 bytes: chunks then load whole vectors
 // wherever a tensor begins, and only a tensor's two ragged ends go by
-// elements.  Blocks take equal runs of chunks, whatever the tensors' sizes.
+// elements.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -136,17 +137,25 @@ __device__ void chunk_scale(const dmoe_grad& g, int64_t chunk, float c) {
   for (int64_t i = s.vhi + threadIdx.x; i < s.hi; i += kClipThreads) store1<F32>(g.out, i, load1<F32>(g.in, i) * c);
 }
 
-// The tensor that holds chunk ch: the last one whose first chunk is <= ch.
-// (Tensors without elements own no chunk and are passed over.)
-__device__ __forceinline__ int tensor_of(const dmoe_grad* __restrict__ g, int n, int64_t ch) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (g[mid].first_chunk <= ch) lo = mid;
-    else hi = mid - 1;
+// The tensor of a chunk, kept from one chunk to the next.
+struct Cursor {
+  dmoe_grad g;
+  int64_t end;  // first chunk after it
+
+  // Moves to the tensor that holds chunk ch: the last one whose first chunk is
+  // <= ch (tensors without elements own no chunk and are passed over).
+  __device__ __forceinline__ void seek(const dmoe_grad* __restrict__ grads, int n, int64_t chunks, int64_t ch) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(&grads[mid].first_chunk) <= ch) lo = mid;
+      else hi = mid - 1;
+    }
+    g = grads[lo];
+    end = lo + 1 < n ? grads[lo + 1].first_chunk : chunks;
   }
-  return lo;
-}
+  __device__ __forceinline__ bool holds(int64_t ch) const { return ch >= g.first_chunk && ch < end; }
+};
 
 __device__ __forceinline__ double block_sum(double v, double* sh) {
 #pragma unroll
@@ -164,23 +173,13 @@ __global__ void __launch_bounds__(kClipThreads, kBlocksPerSm)
   __shared__ double sh[kClipThreads / 32];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  const int64_t c0 = chunks * blockIdx.x / gridDim.x;
-  const int64_t c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-  // a thread's sum of at most chunk / 256 squares in fp32, the sums of
-  // chunks, threads and blocks in fp64
+  // a thread's sum of at most kChunk / kClipThreads squares in fp32, the sums
+  // of chunks, threads and blocks in fp64
   double acc = 0.0;
-  if (c0 < c1) {
-    int i = tensor_of(grads, n, c0);
-    dmoe_grad g = grads[i];
-    int64_t next = i + 1 < n ? grads[i + 1].first_chunk : chunks;
-    for (int64_t ch = c0; ch < c1; ++ch) {
-      while (ch >= next) {
-        ++i;
-        g = grads[i];
-        next = i + 1 < n ? grads[i + 1].first_chunk : chunks;
-      }
-      acc += g.f32 ? chunk_squares<true>(g, ch - g.first_chunk) : chunk_squares<false>(g, ch - g.first_chunk);
-    }
+  Cursor at{};
+  for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+    if (!at.holds(ch)) at.seek(grads, n, chunks, ch);
+    acc += at.g.f32 ? chunk_squares<true>(at.g, ch - at.g.first_chunk) : chunk_squares<false>(at.g, ch - at.g.first_chunk);
   }
   acc = block_sum(acc, sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = acc;
@@ -198,16 +197,12 @@ __global__ void __launch_bounds__(kClipThreads, kBlocksPerSm)
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
   float c = max_norm / (nrm + eps);
   if (c > 1.f) c = 1.f;  // (a norm that is not a number stays one, and reaches every gradient)
-  const int64_t c0 = chunks * blockIdx.x / gridDim.x;
-  const int64_t c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-  if (c0 >= c1) return;
-  int i = tensor_of(grads, n, c1 - 1);
-  dmoe_grad g = grads[i];
-  for (int64_t ch = c1 - 1; ch >= c0; --ch) {
-    while (ch < g.first_chunk) g = grads[--i];
-    if (c == 1.f && g.in == g.out) continue;  // in place and within the limit: nothing changes
-    if (g.f32) chunk_scale<true>(g, ch - g.first_chunk, c);
-    else chunk_scale<false>(g, ch - g.first_chunk, c);
+  Cursor at{};
+  for (int64_t ch = chunks - 1 - blockIdx.x; ch >= 0; ch -= gridDim.x) {
+    if (!at.holds(ch)) at.seek(grads, n, chunks, ch);
+    if (c == 1.f && at.g.in == at.g.out) continue;  // in place and within the limit: nothing changes
+    if (at.g.f32) chunk_scale<true>(at.g, ch - at.g.first_chunk, c);
+    else chunk_scale<false>(at.g, ch - at.g.first_chunk, c);
   }
 }
 

@@ -17,8 +17,10 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace {
 
@@ -26,6 +28,17 @@ constexpr int kNormThreads = 256;  // block size while a row takes at most 256 t
 constexpr int kMaxD = 32768;
 constexpr int kQGroup = 128;       // columns that share a scale in the 8-bit rows
 constexpr float kE4M3Max = 448.f;
+constexpr int kMaxStages = 4;      // backward: units of rows in flight per block
+constexpr size_t kRingBytes = 100 * 1024;  // of shared memory for them where more than one fits: two blocks per SM
+
+// Copies bytes (a multiple of 16) between 16-byte aligned addresses,
+// asynchronously; completes them on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   dmoe::tc::smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(dmoe::tc::smem_u32(bar))
+               : "memory");
+}
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
@@ -158,95 +171,160 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads)
   }
 }
 
-// Rows dealt round-robin over the grid's row groups; every thread adds its
-// columns of dw over its rows, a block's row groups meet in shared memory,
-// and the block writes one fp32 row of partial[gridDim.x][d].
+// Backward.  A persistent block walks units of RPB rows (BLOCK / TPR), dealt
+// round-robin; a ring of `stages` units of dy, h and dh is filled ahead by bulk
+// copies (one per row and tensor), so that the loads in flight do not depend
+// on registers or on the barrier each row's sum needs: 16381 x 4096 measured
+// DISCARD.  Every thread keeps its columns of the weight and adds its columns
+// of dw over its rows; a block's row groups meet in shared memory, and the
+// block writes one fp32 row of partial[gridDim.x][d].
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads)
-    add_rms_norm_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* __restrict__ h,
-                                 const void* __restrict__ weight, const float* __restrict__ rstd, const uint16_t* dh,
-                                 int64_t lddh, int T, int d, uint16_t* dx, float* __restrict__ partial) {
+__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR > 512 ? 1 : 2)
+    add_rms_norm_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* h, const void* __restrict__ weight,
+                                 const float* __restrict__ rstd, const uint16_t* dh, int64_t lddh, int T, int d,
+                                 int stages, uint16_t* dx, float* __restrict__ partial, int32_t* err) {
+  using namespace dmoe::tc;
   constexpr int BLOCK = TPR > kNormThreads ? TPR : kNormThreads;
   constexpr int RPB = BLOCK / TPR;
   __shared__ float red[2][BLOCK / 32];
-  extern __shared__ float dw_sh[];  // [RPB - 1][d] when a block holds several rows
-  dmoe::pdl_wait();
-  dmoe::pdl_launch_dependents();
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int gave_up;
+  extern __shared__ __align__(16) uint8_t ring[];  // [stages][dy, h, dh][RPB][d], then reused for dw
   const int c = threadIdx.x % TPR;
   const int rg = threadIdx.x / TPR;
   const int nvec = d >> 3;
-  float dw[VPT][8] = {};
-  int flip = 0;
-  // every row group of a block makes the same number of trips (barriers inside)
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * RPB; t0 < T; t0 += static_cast<int64_t>(gridDim.x) * RPB) {
-    const int64_t t = t0 + rg;
+  const uint32_t row_bytes = static_cast<uint32_t>(d) * 2;
+  const uint32_t part_bytes = RPB * row_bytes;
+  const int64_t units = (static_cast<int64_t>(T) + RPB - 1) / RPB;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(full + s, 1);
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  float w[VPT][8], dw[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = c + i * TPR;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
+    if (v < nvec) load_w<WF32>(weight, v, w[i]);
+  }
+  // thread 0: the rows of unit u into stage s
+  auto fill = [&](int64_t u, int s) {
+    if (u >= units) return;
+    const int64_t t0 = u * RPB;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(RPB), T - t0));
+    uint8_t* at = ring + s * 3 * part_bytes;
+    mbar_arrive_expect_tx(full + s, rows * row_bytes * (dh ? 3 : 2));
+    for (int r = 0; r < rows; ++r) {
+      bulk_load(at + r * row_bytes, dy + (t0 + r) * lddy, row_bytes, full + s);
+      bulk_load(at + part_bytes + r * row_bytes, h + (t0 + r) * d, row_bytes, full + s);
+      if (dh) bulk_load(at + 2 * part_bytes + r * row_bytes, dh + (t0 + r) * lddh, row_bytes, full + s);
+    }
+  };
+  int64_t u = blockIdx.x;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages; ++s) fill(u + static_cast<int64_t>(s) * gridDim.x, s);
+  int stage = 0, flip = 0;
+  uint32_t phase = 0;
+  for (; u < units; u += gridDim.x) {
+    const int64_t t = u * RPB + rg;
     const bool live = t < T;
     const float r = live ? __ldg(rstd + t) : 0.f;
-    uint4 a[VPT], b[VPT], e[VPT];
+    if (!mbar_wait(full + stage, phase, &gave_up)) gave_up = 1;
+    const uint8_t* at = ring + stage * 3 * part_bytes + rg * row_bytes;
     float s = 0.f;
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = c + i * TPR;
-      a[i] = b[i] = e[i] = make_uint4(0, 0, 0, 0);
-      if (live && v < nvec) {
-        a[i] = *(reinterpret_cast<const uint4*>(dy + t * lddy) + v);
-        b[i] = __ldg(reinterpret_cast<const uint4*>(h + t * d) + v);
-        if (dh) e[i] = *(reinterpret_cast<const uint4*>(dh + t * lddh) + v);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = c + i * TPR;
-      float f[8], g[8], w[8];
-      unpack8(a[i], f);
-      unpack8(b[i], g);
-      if (v < nvec) {
-        load_w<WF32>(weight, v, w);
+      for (int i = 0; i < VPT; ++i) {
+        const int v = c + i * TPR;
+        if (v >= nvec) continue;
+        float f[8], g[8];
+        unpack8(*(reinterpret_cast<const uint4*>(at) + v), f);
+        unpack8(*(reinterpret_cast<const uint4*>(at + part_bytes) + v), g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s = fmaf(f[j] * w[j], g[j], s);
+          s = fmaf(f[j] * w[i][j], g[j], s);
           dw[i][j] = fmaf(f[j] * r, g[j], dw[i][j]);
         }
       }
     }
     s = row_sum<TPR>(s, red[flip]);
+    if (TPR == 32) __syncthreads();
+    if (gave_up) break;
+    // past this barrier every thread is done with the unit before this one
+    if (stages > 1 && threadIdx.x == 0 && u != static_cast<int64_t>(blockIdx.x))
+      fill(u + static_cast<int64_t>(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
     flip ^= 1;
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
     const float m = s / static_cast<float>(d) * r * r;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    for (int i = 0; i < VPT; ++i) {  // the unit again, from shared memory: registers hold w and dw
       const int v = c + i * TPR;
       if (!live || v >= nvec) continue;
-      float f[8], g[8], w[8], o[8];
-      unpack8(a[i], f);
-      unpack8(b[i], g);
-      unpack8(e[i], o);
-      load_w<WF32>(weight, v, w);
+      float f[8], g[8], o[8] = {};
+      unpack8(*(reinterpret_cast<const uint4*>(at) + v), f);
+      unpack8(*(reinterpret_cast<const uint4*>(at + part_bytes) + v), g);
+      if (dh) unpack8(*(reinterpret_cast<const uint4*>(at + 2 * part_bytes) + v), o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = fmaf(r, fmaf(f[j], w[j], -g[j] * m), o[j]);
+      for (int j = 0; j < 8; ++j) o[j] = fmaf(r, fmaf(f[j], w[i][j], -g[j] * m), o[j]);
       *(reinterpret_cast<uint4*>(dx + t * d) + v) = pack8(o);
     }
+    if (stages == 1) {
+      __syncthreads();
+      if (threadIdx.x == 0) fill(u + gridDim.x, 0);
+    }
+  }
+  __syncthreads();
+  if (gave_up) {  // a copy that did not arrive: nothing more is written
+    if (threadIdx.x == 0) {
+      dmoe::raise_error(err, DMOE_SITE_NORM_WAIT | DMOE_ERR_TIMEOUT);
+      volatile int go_on = 0;
+      for (int i = 0; i < stages; ++i) {  // the copies still on their way, as far as they come
+        mbar_wait(full + stage, phase, &go_on);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    return;
   }
   if (!partial) return;
   if (RPB > 1) {
+    float* sh = reinterpret_cast<float*>(ring);  // [RPB - 1][d]: every unit has been read
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
       if (rg > 0 && v < nvec) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw_sh[static_cast<int64_t>(rg - 1) * d + 8 * v + j] = dw[i][j];
+        for (int j = 0; j < 8; ++j) sh[static_cast<int64_t>(rg - 1) * d + 8 * v + j] = dw[i][j];
       }
     }
     __syncthreads();
+    if (rg == 0) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = c + i * TPR;
+        if (v >= nvec) continue;
+        for (int g = 1; g < RPB; ++g) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dw[i][j] += sh[static_cast<int64_t>(g - 1) * d + 8 * v + j];
+        }
+      }
+    }
   }
   if (rg == 0) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
       if (v >= nvec) continue;
-      for (int g = 1; g < RPB; ++g) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] += dw_sh[static_cast<int64_t>(g - 1) * d + 8 * v + j];
-      }
       float4* o = reinterpret_cast<float4*>(partial + static_cast<int64_t>(blockIdx.x) * d) + 2 * v;
       o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
       o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
@@ -290,12 +368,23 @@ int threads_per_row(int d) {
 
 int rows_per_block(int d) { return std::max(1, kNormThreads / threads_per_row(d)); }
 
-// Blocks of the backward: each leaves one partial row of dw, so no more than
-// keep the GPU busy.
+// Bytes of one unit of the backward's ring, and its units: as many as fit in
+// kRingBytes, for wide rows two in what a block can have, or one.
+constexpr size_t kRingMax = 200 * 1024;
+size_t unit_bytes(int d) { return static_cast<size_t>(rows_per_block(d)) * d * 2 * 3; }
+int ring_stages(int d) {
+  const size_t fit = kRingBytes / unit_bytes(d);
+  if (fit >= 2) return static_cast<int>(std::min<size_t>(kMaxStages, fit));
+  return 2 * unit_bytes(d) <= kRingMax ? 2 : 1;
+}
+
+// Blocks of the backward: what is resident (two per SM, one where the ring
+// takes more), each leaving one partial row of dw.
 int backward_blocks(int T, int d, int sms) {
   const int rpb = rows_per_block(d);
   const int64_t need = (static_cast<int64_t>(T) + rpb - 1) / rpb;
-  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(sms) * 4));
+  const int per_sm = ring_stages(d) * unit_bytes(d) <= kRingBytes ? 2 : 1;
+  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(sms) * per_sm));
 }
 
 // Calls f.template operator()<TPR, VPT>() for rows of d columns.
@@ -350,17 +439,31 @@ struct Backward {
   uint16_t* dx;
   float* partial;
   int blocks;
+  int device;
+  int32_t* err;
   cudaStream_t st;
+
+  template <int TPR, int VPT, bool WF32>
+  cudaError_t launch() const {
+    constexpr int block = TPR > kNormThreads ? TPR : kNormThreads;
+    auto kern = add_rms_norm_backward_kernel<TPR, VPT, WF32>;
+    // the ring also holds the row groups' dw: (RPB - 1) fp32 rows in 3 RPB bf16 ones
+    const size_t smem = ring_stages(d) * unit_bytes(d);
+    static std::atomic<uint64_t> opted{0};
+    const uint64_t bit = uint64_t(1) << device;
+    if (!(opted.load(std::memory_order_acquire) & bit)) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(kRingMax));
+      if (e != cudaSuccess) return e;
+      opted.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return dmoe::launch_pdl(kern, dim3(blocks), dim3(block), smem, st, dy, lddy, h, weight, rstd, dh, lddh, T, d,
+                            ring_stages(d), dx, partial, err);
+  }
 
   template <int TPR, int VPT>
   cudaError_t operator()() const {
-    constexpr int block = TPR > kNormThreads ? TPR : kNormThreads;
-    constexpr int rpb = block / TPR;
-    // at most (8 - 1) rows of 512 columns: 14 KB
-    const size_t smem = static_cast<size_t>(rpb - 1) * d * sizeof(float);
-    auto kern = wf32 ? add_rms_norm_backward_kernel<TPR, VPT, true> : add_rms_norm_backward_kernel<TPR, VPT, false>;
-    return dmoe::launch_pdl(kern, dim3(blocks), dim3(block), smem, st, dy, lddy, h, weight, rstd, dh, lddh, T, d, dx,
-                            partial);
+    return wf32 ? launch<TPR, VPT, true>() : launch<TPR, VPT, false>();
   }
 };
 
@@ -416,7 +519,7 @@ DMOE_API dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy
   const int blocks = backward_blocks(T, d, di.sm_count);
   if (dw && (!ws || ws_bytes < static_cast<size_t>(blocks) * d * sizeof(float))) return DMOE_ERR_INVALID_ARG;
   const Backward b{dy, lddy, h, weight, weight_f32, rstd, dh, lddh, T, d, dx, dw ? static_cast<float*>(ws) : nullptr,
-                   blocks, st};
+                   blocks, di.device, di.err_word, st};
   cudaError_t e = by_width(d, b);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);

@@ -74,6 +74,7 @@ typedef enum dmoe_status {
 #define DMOE_SITE_ROUTE_INDEX (5 << 8)
 #define DMOE_SITE_SELFTEST (6 << 8)
 #define DMOE_SITE_LOSS_TARGET (7 << 8)
+#define DMOE_SITE_NORM_WAIT (8 << 8)
 
 /* Block-sparse topology (section 1.3, hybrid BCSR-COO + transpose index).
  * Plain device arrays, all int32, owned by the caller; filled by
