@@ -25,9 +25,9 @@
 
 namespace {
 
-constexpr int kClipThreads = 256;
+constexpr int kClipThreads = 128;  // eight 16-byte vectors of a bf16 chunk each, all in flight
 constexpr int kChunk = DMOE_GRAD_CHUNK;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 8;
 constexpr int kMaxBlocks = 2048;
 
 template <bool F32>
@@ -97,7 +97,7 @@ __device__ float chunk_squares(const dmoe_grad& g, int64_t chunk) {
   float acc = 0.f;
   const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(g.in) + s.vlo * (F32 ? 4 : 2));
   const int nv = static_cast<int>((s.vhi - s.vlo) / V);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.x; i < nv; i += kClipThreads) {
     float f[V];
     unpack<F32>(__ldg(p + i), f);
@@ -125,7 +125,7 @@ __device__ void chunk_scale(const dmoe_grad& g, int64_t chunk, float c) {
   const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(g.in) + s.vlo * ES);
   uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<char*>(g.out) + s.vlo * ES);
   const int nv = static_cast<int>((s.vhi - s.vlo) / V);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.x; i < nv; i += kClipThreads) {
     float f[V];
     unpack<F32>(p[i], f);

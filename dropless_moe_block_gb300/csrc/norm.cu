@@ -91,8 +91,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 }
 
 // One row per TPR threads; BLOCK / TPR rows per block.
-template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads)
+template <int TPR, int VPT, bool WF32, bool Q8>
+__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR > kNormThreads ? 1536 / TPR : 6)
     add_rms_norm_kernel(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
                         const void* __restrict__ weight, float eps, int T, int d, uint16_t* h, uint16_t* y,
                         float* __restrict__ rstd, uint8_t* __restrict__ q, float* __restrict__ q_scale) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads)
       for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
       if (y) *(reinterpret_cast<uint4*>(y + t * d) + v) = pack8(f);
     }
-    if (q) {
+    if (Q8) {
       // 16 neighbouring lanes hold the 128 columns of one scale (TPR and the
       // row's first vector are multiples of 16); lanes past the row hold 0
       float top = 0.f;
@@ -237,19 +237,22 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR >
     if (!mbar_wait(full + stage, phase, &gave_up)) gave_up = 1;
     const uint8_t* at = ring + stage * 3 * part_bytes + rg * row_bytes;
     float s = 0.f;
-    if (live) {
+    uint4 a[VPT], b[VPT];  // kept packed for the second use
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = c + i * TPR;
-        if (v >= nvec) continue;
-        float f[8], g[8];
-        unpack8(*(reinterpret_cast<const uint4*>(at) + v), f);
-        unpack8(*(reinterpret_cast<const uint4*>(at + part_bytes) + v), g);
+    for (int i = 0; i < VPT; ++i) {
+      const int v = c + i * TPR;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (live && v < nvec) {
+        a[i] = *(reinterpret_cast<const uint4*>(at) + v);
+        b[i] = *(reinterpret_cast<const uint4*>(at + part_bytes) + v);
+      }
+      float f[8], g[8];
+      unpack8(a[i], f);
+      unpack8(b[i], g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s = fmaf(f[j] * w[i][j], g[j], s);
-          dw[i][j] = fmaf(f[j] * r, g[j], dw[i][j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        s = fmaf(f[j] * w[i][j], g[j], s);
+        dw[i][j] = fmaf(f[j] * r, g[j], dw[i][j]);
       }
     }
     s = row_sum<TPR>(s, red[flip]);
@@ -265,12 +268,15 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR >
     }
     const float m = s / static_cast<float>(d) * r * r;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {  // the unit again, from shared memory: registers hold w and dw
+    for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
       if (!live || v >= nvec) continue;
+      // unpacked anew (the compiler would carry 16 floats over the barrier instead)
+      asm volatile("" : "+r"(a[i].x), "+r"(a[i].y), "+r"(a[i].z), "+r"(a[i].w));
+      asm volatile("" : "+r"(b[i].x), "+r"(b[i].y), "+r"(b[i].z), "+r"(b[i].w));
       float f[8], g[8], o[8] = {};
-      unpack8(*(reinterpret_cast<const uint4*>(at) + v), f);
-      unpack8(*(reinterpret_cast<const uint4*>(at + part_bytes) + v), g);
+      unpack8(a[i], f);
+      unpack8(b[i], g);
       if (dh) unpack8(*(reinterpret_cast<const uint4*>(at + 2 * part_bytes) + v), o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = fmaf(r, fmaf(f[j], w[i][j], -g[j] * m), o[j]);
@@ -420,7 +426,8 @@ struct Forward {
     constexpr int block = TPR > kNormThreads ? TPR : kNormThreads;
     const int rpb = block / TPR;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + rpb - 1) / rpb));
-    auto kern = wf32 ? add_rms_norm_kernel<TPR, VPT, true> : add_rms_norm_kernel<TPR, VPT, false>;
+    auto kern = wf32 ? (q ? add_rms_norm_kernel<TPR, VPT, true, true> : add_rms_norm_kernel<TPR, VPT, true, false>)
+                     : (q ? add_rms_norm_kernel<TPR, VPT, false, true> : add_rms_norm_kernel<TPR, VPT, false, false>);
     return dmoe::launch_pdl(kern, grid, dim3(block), 0, st, x, ldx, residual, ldr, weight, eps, T, d, h, y, rstd, q,
                             q_scale);
   }
