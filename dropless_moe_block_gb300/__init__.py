@@ -563,7 +563,7 @@ class GradList:
             self.chunks += int(lib().dmoe_grad_chunks(g.data_ptr(), g.numel(), f32))
         device = self.grads[0].device if self.grads else "cuda"
         self.table = torch.tensor(rows or [[0] * 5], dtype=torch.int64).to(device)
-        self.ws = torch.empty(int(lib().dmoe_clip_grad_norm_workspace_size()), dtype=torch.uint8, device=device)
+        self.ws = torch.zeros(int(lib().dmoe_clip_grad_norm_workspace_size()), dtype=torch.uint8, device=device)
 
     def __len__(self):
         return len(self.grads)

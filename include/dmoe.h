@@ -572,7 +572,8 @@ typedef struct dmoe_grad {
  * bytes).  Host-only, no CUDA call. */
 int64_t dmoe_grad_chunks(const void* in, int64_t n, int f32);
 
-/* Bytes of scratch of dmoe_clip_grad_norm. */
+/* Bytes of scratch of dmoe_clip_grad_norm: zero-filled before its first use;
+ * every call leaves it ready for the next one. */
 size_t dmoe_clip_grad_norm_workspace_size(void);
 
 /* norm = sqrt(sum over all tensors of the squares of their elements);
