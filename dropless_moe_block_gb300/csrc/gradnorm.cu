@@ -99,8 +99,7 @@ __device__ __forceinline__ Span span_of(const dmoe_grad& g, int64_t chunk) {
   return s;
 }
 
-// Vectors of a whole chunk per thread: all of them are loaded before the first
-// is used (or stored: source and destination may be the same).
+// Vectors of a whole chunk per thread.
 template <bool F32>
 __host__ __device__ constexpr int whole() {
   return kChunk / (F32 ? 4 : 8) / kClipThreads;
@@ -113,6 +112,9 @@ __device__ float chunk_squares(const dmoe_grad& g, int64_t chunk) {
   float acc = 0.f;
   const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(g.in) + s.vlo * (F32 ? 4 : 2));
   const int nv = static_cast<int>((s.vhi - s.vlo) / V);
+  // eight loads in flight, also of a chunk that is not whole (400 small
+  // tensors 11.5 us; 14.5 by a loop with a remainder, which in turn takes 411
+  // instead of 430 us for 2.8 GB)
 #pragma unroll
   for (int b = 0; b < N; b += 8) {
     uint4 u[8];
@@ -152,6 +154,7 @@ __device__ void chunk_scale(const dmoe_grad& g, int64_t chunk, float c) {
   const int nv = static_cast<int>((s.vhi - s.vlo) / V);
 #pragma unroll
   for (int b = 0; b < N; b += 8) {
+    // loaded before the first is stored: source and destination may be the same
     uint4 u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
