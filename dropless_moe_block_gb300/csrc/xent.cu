@@ -17,21 +17,21 @@
 // the large one, never passes through 16 bits: it is added in fp32.
 //
 // Tokens go in pieces.  A piece's launches:
-//   1 sort     tokens ordered by target (with gradients)
-//   2 logits   x W^T on the tensor cores; the epilogue turns a tile's
+//   1 logits   x W^T on the tensor cores; the epilogue turns a tile's
 //              accumulators into E and, for each row and 64 columns, leaves
 //              the pair (ref, sum of exp(l - ref)).  With gradients E goes to a
 //              [piece, V] bf16 array, the only thing of that size that ever
 //              exists; without, nothing is written.
-//   3 rows     the pairs of a row meet in lse_t; loss_t, s_t, c_t, s_t x_t
-//   4 targets  sums of c_t x_t, up to 32 tokens each, for words with many
-//   5 grads    the tiles of both products in one launch
+//   2 rows     the pairs of a row meet in lse_t; loss_t, s_t, c_t, s_t x_t; the
+//              tokens ordered by target
+//   3 targets  sums of c_t x_t, up to 32 tokens each, for words with many
+//   4 grads    the tiles of both products in one launch
 //
 // ref is 0 while the largest of a row's 64 logits lies in [kRefLow,
 // kRefHigh], else that maximum: exp of a moderate logit needs no maximum
 // subtracted, fp32 and bf16 reach from 1e-38 to 3e38, so in the usual case
 // every pair of a row has the reference 0 and E needs no second pass.  A row
-// whose groups disagree is brought to its largest reference by launch 3.
+// whose groups disagree is brought to its largest reference by launch 2.
 // What bf16 costs is one rounding of E and one of s x (2^-8 of an element
 // at most, independent from element to element).
 //
@@ -54,6 +54,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <utility>
 
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -94,8 +95,8 @@ constexpr int kPieceMax = 1 << 18;
 constexpr int kNarrowD = 1024;
 
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
-constexpr int kMaxSplit = 16;
-constexpr int kRun = 32;             // positions per partial sum of launch 4
+constexpr int kMaxSplit = 64;
+constexpr int kRun = 32;             // positions per partial sum of launch 3
 constexpr int kDirect = 4;           // words with up to so many tokens are summed by dW's epilogue itself
 
 template <bool GRAD, int NS>
@@ -135,6 +136,7 @@ struct FastDiv {
 // of `raster` pair rows.
 struct Grid {
   int cols;       // N
+  int width;      // columns of a sub-tile: BN, for the logits also 128 or 64
   int mt, nt;     // pair-tile rows, tile columns
   int raster;     // pair-tile rows per raster group
   int slices;     // K slices of 64
@@ -154,6 +156,7 @@ struct ParamsX {
   CUtensorMap map_b2;  // gradients: s x MN-major (dW)
   CUtensorMap map_e;   // logits: E, as the epilogue stores it
   int n, d, V;         // tokens of the piece, columns, vocabulary
+  int a_rows;          // rows of map_a's box: what lies past n is not loaded (it only reaches rows past n)
   int first_dx;        // gradients: grid[0] is dx's (else dW's)
   int full, rem;       // grid[0]'s items per unit, and the units that get one more
   int early, extra;    // see item_of()
@@ -168,6 +171,9 @@ struct ParamsX {
   int64_t ldp;
   float* target_logit;
   float unbias;        // 1 + the mean truncation
+  const int32_t* all;  // the whole call's targets, to be counted (NULL: not here)
+  int T, ignore;
+  int32_t* count;
   // gradients
   const float2* coef;  // (s_t, c_t)
   const uint16_t* W;
@@ -179,7 +185,7 @@ struct ParamsX {
   const float* dw_add; // fp32 dW of earlier pieces (or what the caller adds to)
   const int32_t* skey;   // targets in ascending order
   const int32_t* order;  // their tokens, ascending among equal targets
-  const float* runs;     // launch 4's sums, at the position of their first token
+  const float* runs;     // launch 3's sums, at the position of their first token
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -444,6 +450,11 @@ __device__ __forceinline__ int lower_bound(const int32_t* __restrict__ a, int n,
   return lo;
 }
 
+// A target's word, V for one that does not count.
+__device__ __forceinline__ int key_of(int32_t target, int V, int ignore) {
+  return static_cast<unsigned>(target) < static_cast<unsigned>(V) && target != ignore ? target : V;
+}
+
 // The logits' product has both operands K-major (rows of x and of W); dx has
 // E K-major and W MN-major, dW has E and s x MN-major.
 template <bool GRAD, int NS>
@@ -507,15 +518,20 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       Item it;
       for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
         const int m0 = it.m * 2 * BM + rank * BM;
-        const int n0 = it.n * NS * BN + rank * (BN / 2);
+        const int width = GRAD || NS == 2 ? BN : p.grid[0].width;
+        const int n0 = it.n * NS * width + rank * (width / 2);
         const bool a_mn = GRAD && !it.dx;
+        // the bytes of both CTAs' A rows, and whether this one has any
+        const bool a_none = !a_mn && m0 >= p.n;
+        const uint32_t a_bytes =
+            a_mn || it.m * 2 * BM + BM < p.n ? 2 * A_BYTES : static_cast<uint32_t>(p.a_rows) * BK * 2;
         const CUtensorMap* ma = a_mn ? &p.map_a2 : &p.map_a;
         const CUtensorMap* mb = a_mn ? &p.map_b2 : &p.map_b;
         for (int i = it.k0; i < it.k1; ++i) {
           ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
           if (!ok) break;
           const int subs = NS == 2 && it.wide ? 2 : 1;
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * (A_BYTES + subs * B_BYTES));
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, a_bytes + subs * width * BK * 2);
           const uint32_t bar = full_pair + 8u * stage;
           uint8_t* sa = smem + stage * PL::STAGE;
           uint8_t* sb = sa + A_BYTES;
@@ -523,7 +539,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           if (a_mn) {
             tma_load_2d_pair(sa, ma, bar, m0, k0);
             tma_load_2d_pair(sa + ATOM, ma, bar, m0 + 64, k0);
-          } else {
+          } else if (!a_none) {
             tma_load_2d_pair(sa, ma, bar, k0, m0);
           }
 #pragma unroll
@@ -556,6 +572,14 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       }
     }
   } else if (warp == 1) {
+    if (!GRAD && rank == 1 && unit == 0 && p.all) {
+      // a warp without other work counts the targets that count
+      int c = 0;
+#pragma unroll 8
+      for (int i = lane; i < p.T; i += 32) c += key_of(__ldg(p.all + i), p.V, p.ignore) < p.V;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) *p.count = c;
+    }
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------------------ MMA issue
       int stage = 0;
@@ -574,6 +598,10 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       uint32_t a_lo = static_cast<uint32_t>(adesc0);
       const uint32_t b_lo = static_cast<uint32_t>(bdesc0);
       uint32_t a_step = K_STEP, idesc = idesc_bf16(2 * BM, BN, false, GRAD);
+      if (!GRAD && NS == 1)
+        idesc = p.grid[0].width == BN ? idesc_bf16(2 * BM, BN, false, false)
+                                      : p.grid[0].width == 128 ? idesc_bf16(2 * BM, 128, false, false)
+                                                               : idesc_bf16(2 * BM, 64, false, false);
       // one K slice of sub-tile `s` from ring stage st into accumulator d
       auto mmas = [&](uint32_t d, int st, int s, bool first) {
         const uint32_t a = a_lo + st * (PL::STAGE >> 4);
@@ -717,14 +745,15 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int c = (it.n * NS + s) * BN + part * 64;  // this warp's first column
+        const int width = GRAD || NS == 2 ? BN : p.grid[0].width;
+        const int c = (it.n * NS + s) * width + part * 64;  // this warp's first column
         if (NS == 1 || s == 0) {
           ok = mbar_wait_cluster(tfull + acc, acc_phase, abort_flag);
           if (!ok) break;
           __syncwarp();
         }
-        if (NS == 2 && s == 1 && !it.wide) {
-          release();
+        if ((NS == 2 && s == 1 && !it.wide) || (NS == 1 && part * 64 >= width)) {
+          release();  // no such columns
           continue;
         }
         fence_after_sync();
@@ -847,76 +876,6 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
 
 // ------------------------------------------------------- tokens by target
 
-__device__ __forceinline__ int key_of(int32_t target, int V, int ignore) {
-  return static_cast<unsigned>(target) < static_cast<unsigned>(V) && target != ignore ? target : V;
-}
-
-constexpr int kSortWarps = 8;
-constexpr int kSortChunk = 2048;
-
-// Stable sort of the piece's targets (those that do not count last) by
-// counting: each warp counts the tokens that come before two of its own, n^2
-// comparisons in all: 15 us at 8192 tokens.  skey[r], order[r]: the key
-// and the token at position r.  Block 0 also counts the targets of the whole
-// call that count.
-__global__ void __launch_bounds__(32 * kSortWarps)
-    sort_targets_kernel(const int32_t* __restrict__ targets, int n, int V, int ignore, int32_t* __restrict__ skey,
-                        int32_t* __restrict__ order, const int32_t* __restrict__ all, int T,
-                        int32_t* __restrict__ count) {
-  __shared__ int4 keys[kSortChunk / 4];
-  __shared__ int sh[kSortWarps];
-  dmoe::pdl_wait();
-  dmoe::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
-  const int t0 = 2 * (blockIdx.x * kSortWarps + warp), t1 = t0 + 1;  // in one group of four
-  const int key0 = t0 < n ? key_of(__ldg(targets + t0), V, ignore) : 0;
-  const int key1 = t1 < n ? key_of(__ldg(targets + t1), V, ignore) : 0;
-  int r0 = 0, r1 = 0;
-  for (int base = 0; base < n; base += kSortChunk) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kSortChunk; i += 32 * kSortWarps)  // past the end: after every key
-      reinterpret_cast<int*>(keys)[i] = base + i < n ? key_of(__ldg(targets + base + i), V, ignore) : V + 1;
-    __syncthreads();
-    const int split = (t0 - base) >> 2;  // groups before the tokens' own also count equal keys
-#pragma unroll 4
-    for (int i = lane; i < kSortChunk / 4; i += 32) {
-      const int4 k = keys[i];
-      const int eq = i < split ? 1 : 0;
-      const int l0 = key0 + eq, l1 = key1 + eq;
-      r0 += (k.x < l0) + (k.y < l0) + (k.z < l0) + (k.w < l0);
-      r1 += (k.x < l1) + (k.y < l1) + (k.z < l1) + (k.w < l1);
-    }
-  }
-  // equal keys earlier in the tokens' own group of four
-  const int u = (t0 & ~3) + lane;
-  if (lane < 3 && u < n) {
-    const int k = key_of(__ldg(targets + u), V, ignore);
-    r0 += u < t0 && k == key0;
-    r1 += u < t1 && k == key1;
-  }
-  r0 = __reduce_add_sync(0xffffffffu, r0);
-  r1 = __reduce_add_sync(0xffffffffu, r1);
-  if (lane == 0 && t0 < n) {
-    skey[r0] = key0;
-    order[r0] = t0;
-    if (t1 < n) {
-      skey[r1] = key1;
-      order[r1] = t1;
-    }
-  }
-  if (blockIdx.x != 0 || !count) return;
-  int c = 0;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < T; i += 32 * kSortWarps) c += key_of(__ldg(all + i), V, ignore) < V;
-  c = __reduce_add_sync(0xffffffffu, c);
-  if (lane == 0) sh[warp] = c;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kSortWarps; ++i) c += sh[i];
-    *count = c;
-  }
-}
 
 // Sums of c_t x_t for words with more than kDirect tokens, in blocks of kRun =
 // 32 positions of the sorted order: runs[r], r a word's first position or a
@@ -979,7 +938,6 @@ __global__ void __launch_bounds__(128)
 
 // ------------------------------------------------------------ row statistics
 
-constexpr int kStatRows = 32, kStatSlices = 32;
 
 // (R, S) <- the pair of the union: S counts exp(l - R).
 __device__ __forceinline__ void join(float& R, float& S, float r, float s) {
@@ -1010,32 +968,96 @@ struct ParamsR {
   uint16_t* xs;       // s x in bf16 (NULL: no dW)
   uint16_t* E;
   int64_t ldv;
+  int32_t* skey;
+  int32_t* order;
   int32_t* err;
 };
 
-// 32 rows per block: the row's groups by 32 slices, then a warp per row for
-// s x and, where a row's groups have different references, its E.
-__global__ void __launch_bounds__(kStatRows * kStatSlices, 2) row_stats_kernel(const ParamsR p) {
-  __shared__ float4 sh[kStatSlices][kStatRows];
-  __shared__ float sh_s[kStatRows], sh_r[kStatRows];
-  __shared__ int sh_fix[kStatRows];
+constexpr int kStatThreads = 1024;
+constexpr int kSortTokens = 2 * kStatThreads / 32;  // per block
+constexpr int kSortChunk = 2048;
+
+// Stable sort of the piece's targets (those that do not count last) by
+// counting: each warp counts the tokens that come before two of its own, n^2
+// comparisons in all: 15 us at 8192 tokens alone, most of it hidden beside
+// the rows' blocks.  skey[r], order[r]: the key and the token at position r.
+__device__ void sort_targets(const ParamsR& p, int block, int4* keys) {
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int t0 = block * kSortTokens + 2 * warp, t1 = t0 + 1;  // in one group of four
+  const int key0 = t0 < p.n ? key_of(__ldg(p.targets + t0), p.V, p.ignore) : 0;
+  const int key1 = t1 < p.n ? key_of(__ldg(p.targets + t1), p.V, p.ignore) : 0;
+  int r0 = 0, r1 = 0;
+  for (int base = 0; base < p.n; base += kSortChunk) {
+    const int groups = min(kSortChunk, (p.n - base + 3) & ~3) / 4;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 4 * groups; i += kStatThreads)  // past the end: after every key
+      reinterpret_cast<int*>(keys)[i] = base + i < p.n ? key_of(__ldg(p.targets + base + i), p.V, p.ignore) : p.V + 1;
+    __syncthreads();
+    const int split = (t0 - base) >> 2;  // groups before the tokens' own also count equal keys
+#pragma unroll 4
+    for (int i = lane; i < groups; i += 32) {
+      const int4 k = keys[i];
+      const int eq = i < split ? 1 : 0;
+      const int l0 = key0 + eq, l1 = key1 + eq;
+      r0 += (k.x < l0) + (k.y < l0) + (k.z < l0) + (k.w < l0);
+      r1 += (k.x < l1) + (k.y < l1) + (k.z < l1) + (k.w < l1);
+    }
+  }
+  // equal keys earlier in the tokens' own group of four
+  const int u = (t0 & ~3) + lane;
+  if (lane < 3 && u < p.n) {
+    const int k = key_of(__ldg(p.targets + u), p.V, p.ignore);
+    r0 += u < t0 && k == key0;
+    r1 += u < t1 && k == key1;
+  }
+  r0 = __reduce_add_sync(0xffffffffu, r0);
+  r1 = __reduce_add_sync(0xffffffffu, r1);
+  if (lane == 0 && t0 < p.n) {
+    p.skey[r0] = key0;
+    p.order[r0] = t0;
+    if (t1 < p.n) {
+      p.skey[r1] = key1;
+      p.order[r1] = t1;
+    }
+  }
+}
+
+// ROWS rows per block (32, or 8 where those leave SMs idle): 1024 / ROWS
+// threads share a row's groups, then its warps write s x and, where the row's
+// groups have different references, bring its E to one.  Blocks past the rows'
+// sort the targets.
+constexpr int kStatFewRows = 2048;  // 26 rows of 85000 words: 12.8 us by 32, 6.2 by 8
+template <int ROWS>
+__global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const ParamsR p) {
+  constexpr int SLICES = kStatThreads / ROWS;
+  constexpr int WARPS = 32 / ROWS;  // per row, for the second half
+  __shared__ float4 sh[SLICES][ROWS];
+  __shared__ float sh_s[ROWS], sh_r[ROWS];
+  __shared__ int sh_fix[ROWS];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int slice = threadIdx.x >> 5;
-  const int t = blockIdx.x * kStatRows + lane;
+  const int row_blocks = (p.n + ROWS - 1) / ROWS;
+  if (static_cast<int>(blockIdx.x) >= row_blocks) {
+    static_assert(sizeof(sh) >= kSortChunk * sizeof(int), "the keys share the rows' scratch");
+    sort_targets(p, static_cast<int>(blockIdx.x) - row_blocks, reinterpret_cast<int4*>(&sh[0][0]));
+    return;
+  }
+  const int r0 = threadIdx.x % ROWS;
+  const int slice = threadIdx.x / ROWS;
+  const int t = blockIdx.x * ROWS + r0;
   float R = -INFINITY, S = 0.f, low = INFINITY, high = -INFINITY;
   if (t < p.n) {
-    for (int g0 = slice; g0 < p.groups; g0 += 4 * kStatSlices) {
+    for (int g0 = slice; g0 < p.groups; g0 += 4 * SLICES) {
       float s[4];  // four loads in flight
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int g = g0 + i * kStatSlices;
+        const int g = g0 + i * SLICES;
         s[i] = g < p.groups ? __ldg(p.sums + g * p.ldp + t) : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int g = g0 + i * kStatSlices;
+        const int g = g0 + i * SLICES;
         if (g >= p.groups) break;
         const float r = signbit(s[i]) ? __ldg(p.refs + g * p.ldp + t) : 0.f;
         join(R, S, r, fabsf(s[i]));
@@ -1044,15 +1066,19 @@ __global__ void __launch_bounds__(kStatRows * kStatSlices, 2) row_stats_kernel(c
       }
     }
   }
-  sh[slice][lane] = make_float4(R, S, low, high);
-  __syncthreads();
-  if (slice == 0 && t < p.n) {
-    for (int i = 1; i < kStatSlices; ++i) {
-      const float4 q = sh[i][lane];
-      if (q.x != -INFINITY) join(R, S, q.x, q.y);  // else a slice without groups
+  sh[slice][r0] = make_float4(R, S, low, high);
+#pragma unroll 1
+  for (int half = SLICES / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (slice < half) {
+      const float4 q = sh[slice + half][r0];
+      if (q.x != -INFINITY) join(R, S, q.x, q.y);  // else no groups
       low = fminf(low, q.z);
       high = fmaxf(high, q.w);
+      sh[slice][r0] = make_float4(R, S, low, high);
     }
+  }
+  if (slice == 0 && t < p.n) {
     const float L = R + logf(S);
     const int32_t v = __ldg(p.targets + t);
     const bool counts = key_of(v, p.V, p.ignore) < p.V;
@@ -1066,23 +1092,25 @@ __global__ void __launch_bounds__(kStatRows * kStatSlices, 2) row_stats_kernel(c
       const float s = g == 0.f ? 0.f : g * expf(R - L);
       // expm1: where the softmax at the target is close to 1 or to 0
       p.coef[t] = make_float2(s, g == 0.f ? 0.f : g * expm1f(-nll));
-      sh_s[lane] = s;
-      sh_r[lane] = R;
+      sh_s[r0] = s;
+      sh_r[r0] = R;
       // 1: bring the row's groups to one reference; 2: a row that does not
       // count holds what is not finite, which times 0 would still spread
-      sh_fix[lane] = g == 0.f ? (isfinite(S) ? 0 : 2) : (low != high ? 1 : 0);
+      sh_fix[r0] = g == 0.f ? (isfinite(S) ? 0 : 2) : (low != high ? 1 : 0);
     }
   }
   if (!p.coef) return;
   __syncthreads();
-  const int row = blockIdx.x * kStatRows + slice;
+  const int lane = threadIdx.x & 31;
+  const int rw = (threadIdx.x >> 5) / WARPS, sub = (threadIdx.x >> 5) % WARPS;
+  const int row = blockIdx.x * ROWS + rw;
   if (row >= p.n) return;
   if (p.xs) {
-    const float s = sh_s[slice];
+    const float s = sh_s[rw];
     const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(row) * p.d);
     uint4* dst = reinterpret_cast<uint4*>(p.xs + static_cast<int64_t>(row) * p.d);
 #pragma unroll 4
-    for (int v = lane; v < p.d / 8; v += 32) {
+    for (int v = sub * 32 + lane; v < p.d / 8; v += 32 * WARPS) {
       float f[8];
       unpack8x(__ldg(src + v), f);
 #pragma unroll
@@ -1090,11 +1118,11 @@ __global__ void __launch_bounds__(kStatRows * kStatSlices, 2) row_stats_kernel(c
       dst[v] = pack8x(f);
     }
   }
-  const int fix = sh_fix[slice];
+  const int fix = sh_fix[rw];
   if (fix) {
-    const float top = sh_r[slice];
+    const float top = sh_r[rw];
     uint16_t* e = p.E + static_cast<int64_t>(row) * p.ldv;
-    for (int g = 0; g < p.groups; ++g) {
+    for (int g = sub; g < p.groups; g += WARPS) {
       const float r = signbit(__ldg(p.sums + g * p.ldp + row)) ? __ldg(p.refs + g * p.ldp + row) : 0.f;
       if (fix == 1 && r == top) continue;
       const float k = fix == 2 ? 0.f : expf(r - top);
@@ -1139,11 +1167,12 @@ __global__ void __launch_bounds__(256)
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-Grid make_grid(int M, int N, int K, int raster, int parts = 1, int width = 2 * BN) {
+Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN) {
   Grid g{};
   g.cols = N;
+  g.width = std::min(tile, BN);
   g.mt = ceil_div(M, 2 * BM);
-  g.nt = ceil_div(N, width);
+  g.nt = ceil_div(N, tile);
   g.raster = raster;
   g.slices = ceil_div(K, BK);
   g.per_part = ceil_div(g.slices, parts);
@@ -1156,8 +1185,30 @@ Grid make_grid(int M, int N, int K, int raster, int parts = 1, int width = 2 * B
   return g;
 }
 
-// K slices per item of a grid (its longest).
-int item_slices(const Grid& g) { return g.per_part; }
+// Columns of a logits tile.  Few tokens and words make few tiles; then narrower
+// ones spread the reading of W over more SMs: the width whose busiest pair is
+// shortest, in 256-wide slices (0.28 us; a narrower one's loads of x and its
+// latency stay).  2 tokens, 4492 words, d = 3296: 18 tiles of 256 34 us, 71 of
+// 64 DISCARD us.
+int logits_tile(int n, int d, int V) {
+  const int64_t mt = ceil_div(n, 2 * BM);
+  auto cost = [&](int tile, int per_slice) {  // in hundredths
+    return static_cast<int64_t>(ceil_div(mt * ceil_div(V, tile), kUnits)) * per_slice;
+  };
+  int best = d <= kNarrowD ? BN : 2 * BN;
+  int64_t least = best == BN ? cost(BN, 100) : cost(2 * BN, 190);
+  for (const auto& w : {std::pair<int, int>{BN, 100}, {128, 60}, {64, 45}})
+    if (cost(w.first, w.second) < least) {
+      best = w.first;
+      least = cost(w.first, w.second);
+    }
+  return best;
+}
+
+// Time of a gradient item in K slices: its product, or, where K is short, its
+// epilogue (256 x 512 outputs take as long as about 9 slices).
+constexpr int kEpilogueSlices = 9;
+int item_slices(const Grid& g) { return std::max(g.per_part, g.cols > BN ? kEpilogueSlices : kEpilogueSlices / 2 + 1); }
 
 // Deals the items of two grids (the second may have none) to U units: the
 // longer ones into grid[0], and how many of the shorter ones the units with
@@ -1353,18 +1404,17 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     const int n = static_cast<int>(std::min<int64_t>(l.piece, T - t0));
     const uint16_t* xp = x + t0 * d;
     const int32_t* tp = targets + t0;
-    if (grad)
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(sort_targets_kernel, dim3(ceil_div(n, 2 * kSortWarps)), dim3(32 * kSortWarps), 0,
-                                       st, tp, n, V, ignore_index, skey, order, targets, T,
-                                       t0 == 0 ? count : nullptr));
     ParamsX p{};
     p.n = n, p.d = d, p.V = V;
+    p.a_rows = static_cast<int>(std::min<int64_t>(BM, round_up(n, 8)));
     p.targets = tp;
     p.err = di.err_word;
     p.ldv = l.ldv;
     {
       ParamsX q = p;
-      if (!dmoe::make_map(&q.map_a, xp, n, d, BK, BM) || !dmoe::make_map(&q.map_b, w, V, d, BK, BN / 2))
+      const int tile = logits_tile(n, d, V);
+      if (!dmoe::make_map(&q.map_a, xp, n, d, BK, p.a_rows) ||
+          !dmoe::make_map(&q.map_b, w, V, d, BK, std::min(tile, BN) / 2))
         return DMOE_ERR_CUDA;
       if (grad && !dmoe::make_map(&q.map_e, E, n, l.ldv, 64, 32)) return DMOE_ERR_CUDA;
       q.E = E;
@@ -1372,9 +1422,12 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       q.refs = refs;
       q.ldp = l.ldp;
       q.target_logit = target_logit;
+      q.all = grad && !d_loss && t0 == 0 ? targets : nullptr;
+      q.T = T, q.ignore = ignore_index, q.count = count;
       q.unbias = 1.f + static_cast<float>(ceil_div(d, UMMA_K)) * kTruncation;
-      if (d <= kNarrowD) DMOE_TRY((launch_head<false, 1>(q, make_grid(n, V, d, 16, 1, BN), Grid{}, di, st)));
-      else DMOE_TRY((launch_head<false, 2>(q, make_grid(n, V, d, 16), Grid{}, di, st)));
+      const Grid g = make_grid(n, V, d, 16, 1, tile);
+      if (tile > BN) DMOE_TRY((launch_head<false, 2>(q, g, Grid{}, di, st)));
+      else DMOE_TRY((launch_head<false, 1>(q, g, Grid{}, di, st)));
     }
     ParamsR r{};
     r.sums = sums, r.refs = refs, r.ldp = l.ldp, r.groups = static_cast<int>(l.groups);
@@ -1386,9 +1439,13 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     r.coef = coef;
     r.x = xp, r.xs = dw ? xs : nullptr;
     r.E = E, r.ldv = l.ldv;
+    r.skey = skey, r.order = order;
     r.err = di.err_word;
-    DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel, dim3(ceil_div(n, kStatRows)), dim3(kStatRows * kStatSlices), 0,
-                                     st, r));
+    const int sorting = dw ? ceil_div(n, kSortTokens) : 0;
+    if (n <= kStatFewRows)
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<8>, dim3(ceil_div(n, 8) + sorting), dim3(kStatThreads), 0, st, r));
+    else
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<32>, dim3(ceil_div(n, 32) + sorting), dim3(kStatThreads), 0, st, r));
     if (!grad) continue;
     if (dw)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
@@ -1398,7 +1455,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     Grid gx{}, gw{};
     // E as [n, V] with row pitch ldv: the columns past V read as zero
     if (dx) {
-      if (!dmoe::make_map_ld(&p.map_a, E, n, V, l.ldv, BK, BM) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
+      if (!dmoe::make_map_ld(&p.map_a, E, n, V, l.ldv, BK, p.a_rows) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
         return DMOE_ERR_CUDA;
       gx = make_grid(n, d, V, 16, parts);
     }
