@@ -256,7 +256,9 @@ def test_norm_backward_against_differences(dm):
 # ------------------------------------------------------------- loss (GPU tests)
 
 LOSS_SIZES = [(1, 1, 8), (1, 2, 8), (5, 7, 16), (3, 129, 72), (33, 1009, 256), (130, 300, 64), (257, 513, 136),
-              (300, 1024, 520), (513, 2050, 64), (64, 5003, 1032)]
+              (300, 1024, 520), (513, 2050, 64), (64, 5003, 1032),
+              # enough tiles for the widest ones, several a unit, a narrow last column
+              (300, 38900, 1032), (2, 6000, 1288)]
 
 
 def run_loss(dm, x, w, t, dx=True, dw=torch.bfloat16, **kw):
@@ -310,6 +312,44 @@ def test_loss_and_gradients(dm, T, V, d):
         assert torch.equal(out[k], again[k]), f"{k} differs between two runs"
     alone = run_loss(dm, xs, wsd, ts, dx=False, dw=None)
     assert torch.equal(alone["loss"], out["loss"]) and torch.equal(alone["lse"], out["lse"])
+
+
+@pytest.mark.gpu
+def test_loss_one_gradient_at_a_time_on_another_stream(dm):
+    T, V, d = 300, 900, 264
+    x, w = randn(56, T, d), randn(57, V, d, scale=0.2)
+    t = torch.randint(0, V, (T,), generator=gen(58), dtype=torch.int32)
+    xs, wsd, ts = cuda(x), cuda(w), cuda(t)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        a = run_loss(dm, xs, wsd, ts, dw=None)
+        b = run_loss(dm, xs, wsd, ts, dx=False)
+    c = run_loss(dm, xs, wsd, ts, dw=None, stream=torch.cuda.current_stream())
+    stream.synchronize()
+    check_loss(a, x, w, t)
+    check_loss(b, x, w, t)
+    assert torch.equal(a["dx"], c["dx"]) and torch.equal(a["loss"], b["loss"])
+
+
+@pytest.mark.gpu
+def test_loss_in_a_graph(dm):
+    """Captured and replayed with other inputs in the same places."""
+    T, V, d = 70, 300, 72
+    x, w = randn(70, T, d), randn(71, V, d, scale=0.2)
+    t = torch.randint(0, V, (T,), generator=gen(72), dtype=torch.int32)
+    xs, wsd, ts = cuda(x), cuda(w), cuda(t)
+    out = run_loss(dm, xs, wsd, ts)
+    ws = torch.empty(dm.linear_cross_entropy_workspace_size(T, d, V), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        dm.linear_cross_entropy(xs, wsd, ts, out["loss"], out["lse"], ws, dx=out["dx"], dw=out["dw"])
+    x = randn(73, T, d)
+    t = torch.full((T,), 5, dtype=torch.int32)
+    xs.copy_(x)
+    ts.copy_(t)
+    graph.replay()
+    check_loss(out, x, w, t)
 
 
 @pytest.mark.gpu
