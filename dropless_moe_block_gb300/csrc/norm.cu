@@ -28,12 +28,12 @@ namespace {
 // sooner (rows of 512 columns, 16384 of them: 11.6 us at 256, 11.2 at 128;
 // 4093 rows of 3584 in 8 bits: 19.4 and 18.7 us).
 constexpr int kFwdThreads = 128;
-constexpr int kNormThreads = 256;  // backward
+constexpr int kNormThreads = 128;  // backward (8192 x 512: 15.7 us at 256, 13.9 at 128)
 constexpr int kMaxD = 32768;
 constexpr int kQGroup = 128;       // columns that share a scale in the 8-bit rows
 constexpr float kE4M3Max = 448.f;
 constexpr int kMaxStages = 4;      // backward: units of rows in flight per block
-constexpr size_t kRingBytes = 100 * 1024;  // of shared memory for them where more than one fits: two blocks per SM
+constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(TPR > kFwdThreads ? TPR : kFwdThreads, 1536 / 
 // of dw over its rows; a block's row groups meet in shared memory, and the
 // block writes one fp32 row of partial[gridDim.x][d].
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR > 512 ? 1 : 2)
+__global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR > 256 ? 1 : TPR > kNormThreads ? 2 : 4)
     add_rms_norm_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* h, const void* __restrict__ weight,
                                  const float* __restrict__ rstd, const uint16_t* dh, int64_t lddh, int T, int d,
                                  int stages, uint16_t* dx, float* __restrict__ partial, int32_t* err) {
@@ -214,14 +214,27 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR >
   __syncthreads();
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  float w[VPT][8], dw[VPT][8];
+  // the weight's columns stay in registers, except where four vectors a thread
+  // leave too few (they come from L1 then)
+  constexpr bool KEEP = VPT == 2;
+  float kept[KEEP ? VPT : 1][8], dw[VPT][8] = {};
+  if (KEEP) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = c + i * TPR;
+    for (int i = 0; i < VPT; ++i) {
+      const int v = c + i * TPR;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.f;
-    if (v < nvec) load_w<WF32>(weight, v, w[i]);
+      for (int j = 0; j < 8; ++j) kept[i][j] = 0.f;
+      if (v < nvec) load_w<WF32>(weight, v, kept[i]);
+    }
   }
+  auto weights = [&](int i, float* w) {
+    if (KEEP) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = kept[i][j];
+    } else if (c + i * TPR < nvec) {
+      load_w<WF32>(weight, c + i * TPR, w);
+    }
+  };
   // thread 0: the rows of unit u into stage s
   auto fill = [&](int64_t u, int s) {
     if (u >= units) return;
@@ -256,12 +269,13 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR >
         a[i] = *(reinterpret_cast<const uint4*>(at) + v);
         b[i] = *(reinterpret_cast<const uint4*>(at + part_bytes) + v);
       }
-      float f[8], g[8];
+      float f[8], g[8], w[8] = {};
       unpack8(a[i], f);
       unpack8(b[i], g);
+      weights(i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        s = fmaf(f[j] * w[i][j], g[j], s);
+        s = fmaf(f[j] * w[j], g[j], s);
         dw[i][j] = fmaf(f[j] * r, g[j], dw[i][j]);
       }
     }
@@ -284,12 +298,13 @@ __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR >
       // unpacked anew (the compiler would carry 16 floats over the barrier instead)
       asm volatile("" : "+r"(a[i].x), "+r"(a[i].y), "+r"(a[i].z), "+r"(a[i].w));
       asm volatile("" : "+r"(b[i].x), "+r"(b[i].y), "+r"(b[i].z), "+r"(b[i].w));
-      float f[8], g[8], o[8] = {};
+      float f[8], g[8], w[8] = {}, o[8] = {};
       unpack8(a[i], f);
       unpack8(b[i], g);
+      weights(i, w);
       if (dh) unpack8(*(reinterpret_cast<const uint4*>(at + 2 * part_bytes) + v), o);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = fmaf(r, fmaf(f[j], w[i][j], -g[j] * m), o[j]);
+      for (int j = 0; j < 8; ++j) o[j] = fmaf(r, fmaf(f[j], w[j], -g[j] * m), o[j]);
       *(reinterpret_cast<uint4*>(dx + t * d) + v) = pack8(o);
     }
     if (stages == 1) {
@@ -374,33 +389,33 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 }
 
 // Threads per row: the smallest power of two from 32 on that holds the row
-// at two vectors a thread (four for the widest rows).
+// at two vectors a thread; over 8192 columns at four.
 int threads_per_row(int d) {
   const int nvec = d >> 3;
+  if (nvec > 2048) return 1024;
   int tpr = 32;
-  while (tpr < 1024 && 2 * tpr < nvec) tpr *= 2;
+  while (tpr < 512 && 2 * tpr < nvec) tpr *= 2;
   return tpr;
 }
 
 int rows_per_block(int d) { return std::max(1, kNormThreads / threads_per_row(d)); }
 
-// Bytes of one unit of the backward's ring, and its units: as many as fit in
-// kRingBytes, for wide rows two in what a block can have, or one.
-constexpr size_t kRingMax = 200 * 1024;
+// Bytes of one unit of the backward's ring, blocks per SM, and units per block:
+// as many as fit, for wide rows two in what a block can have, or one.
 size_t unit_bytes(int d) { return static_cast<size_t>(rows_per_block(d)) * d * 2 * 3; }
+int blocks_per_sm(int d) {
+  const int tpr = threads_per_row(d);
+  return tpr <= kNormThreads ? 4 : tpr <= 256 ? 2 : 1;  // what their registers allow
+}
 int ring_stages(int d) {
-  const size_t fit = kRingBytes / unit_bytes(d);
-  if (fit >= 2) return static_cast<int>(std::min<size_t>(kMaxStages, fit));
-  return 2 * unit_bytes(d) <= kRingMax ? 2 : 1;
+  return static_cast<int>(std::clamp<size_t>(kRingBytes / blocks_per_sm(d) / unit_bytes(d), 1, kMaxStages));
 }
 
-// Blocks of the backward: what is resident (two per SM, one where the ring
-// takes more), each leaving one partial row of dw.
+// Blocks of the backward: what is resident, each leaving one partial row of dw.
 int backward_blocks(int T, int d, int sms) {
   const int rpb = rows_per_block(d);
   const int64_t need = (static_cast<int64_t>(T) + rpb - 1) / rpb;
-  const int per_sm = ring_stages(d) * unit_bytes(d) <= kRingBytes ? 2 : 1;
-  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(sms) * per_sm));
+  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(sms) * blocks_per_sm(d)));
 }
 
 // Calls f.template operator()<TPR, VPT>() for rows of d columns.
@@ -411,8 +426,8 @@ cudaError_t by_width(int d, F&& f) {
     case 64: return f.template operator()<64, 2>();
     case 128: return f.template operator()<128, 2>();
     case 256: return f.template operator()<256, 2>();
-    case 512: return f.template operator()<512, 2>();
-    default: return (d >> 3) <= 2048 ? f.template operator()<1024, 2>() : f.template operator()<1024, 4>();
+    case 512: return (d >> 3) <= 1024 ? f.template operator()<512, 2>() : f.template operator()<512, 4>();
+    default: return f.template operator()<1024, 4>();
   }
 }
 
@@ -470,7 +485,7 @@ struct Backward {
     const uint64_t bit = uint64_t(1) << device;
     if (!(opted.load(std::memory_order_acquire) & bit)) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(kRingMax));
+                                                 static_cast<int>(kRingBytes));
       if (e != cudaSuccess) return e;
       opted.fetch_or(bit, std::memory_order_acq_rel);
     }

@@ -1189,7 +1189,7 @@ Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN
 // ones spread the reading of W over more SMs: the width whose busiest pair is
 // shortest, in 256-wide slices (0.28 us; a narrower one's loads of x and its
 // latency stay).  2 tokens, 4492 words, d = 3296: 18 tiles of 256 34 us, 71 of
-// 64 DISCARD us.
+// 64 19 us.
 int logits_tile(int n, int d, int V) {
   const int64_t mt = ceil_div(n, 2 * BM);
   auto cost = [&](int tile, int per_slice) {  // in hundredths
