@@ -968,6 +968,7 @@ struct ParamsR {
   uint16_t* xs;       // s x in bf16 (NULL: no dW)
   uint16_t* E;
   int64_t ldv;
+  int sorting;        // blocks that sort
   int32_t* skey;
   int32_t* order;
   int32_t* err;
@@ -979,31 +980,35 @@ constexpr int kSortChunk = 2048;
 
 // Stable sort of the piece's targets (those that do not count last) by
 // counting: each warp counts the tokens that come before two of its own, n^2
-// comparisons in all: 15 us at 8192 tokens alone, most of it hidden beside
-// the rows' blocks.  skey[r], order[r]: the key and the token at position r.
-__device__ void sort_targets(const ParamsR& p, int block, int4* keys) {
+// comparisons in all.  The keys are held in fp32 (exact to 2^24): a comparison
+// is then saturate(limit - key), 1 or 0, and runs at the full rate of the
+// FMA pipe, where integer comparisons have half.  skey[r], order[r]: the key
+// and the token at position r.
+__device__ void sort_targets(const ParamsR& p, int block, float4* keys) {
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int t0 = block * kSortTokens + 2 * warp, t1 = t0 + 1;  // in one group of four
   const int key0 = t0 < p.n ? key_of(__ldg(p.targets + t0), p.V, p.ignore) : 0;
   const int key1 = t1 < p.n ? key_of(__ldg(p.targets + t1), p.V, p.ignore) : 0;
-  int r0 = 0, r1 = 0;
+  float f0 = 0.f, f1 = 0.f;
   for (int base = 0; base < p.n; base += kSortChunk) {
     const int groups = min(kSortChunk, (p.n - base + 3) & ~3) / 4;
     __syncthreads();
     for (int i = threadIdx.x; i < 4 * groups; i += kStatThreads)  // past the end: after every key
-      reinterpret_cast<int*>(keys)[i] = base + i < p.n ? key_of(__ldg(p.targets + base + i), p.V, p.ignore) : p.V + 1;
+      reinterpret_cast<float*>(keys)[i] =
+          base + i < p.n ? static_cast<float>(key_of(__ldg(p.targets + base + i), p.V, p.ignore)) : 3e7f;
     __syncthreads();
     const int split = (t0 - base) >> 2;  // groups before the tokens' own also count equal keys
 #pragma unroll 4
     for (int i = lane; i < groups; i += 32) {
-      const int4 k = keys[i];
-      const int eq = i < split ? 1 : 0;
-      const int l0 = key0 + eq, l1 = key1 + eq;
-      r0 += (k.x < l0) + (k.y < l0) + (k.z < l0) + (k.w < l0);
-      r1 += (k.x < l1) + (k.y < l1) + (k.z < l1) + (k.w < l1);
+      const float4 k = keys[i];
+      const float eq = i < split ? 1.f : 0.f;
+      const float l0 = static_cast<float>(key0) + eq, l1 = static_cast<float>(key1) + eq;
+      f0 += (__saturatef(l0 - k.x) + __saturatef(l0 - k.y)) + (__saturatef(l0 - k.z) + __saturatef(l0 - k.w));
+      f1 += (__saturatef(l1 - k.x) + __saturatef(l1 - k.y)) + (__saturatef(l1 - k.z) + __saturatef(l1 - k.w));
     }
   }
+  int r0 = static_cast<int>(f0), r1 = static_cast<int>(f1);
   // equal keys earlier in the tokens' own group of four
   const int u = (t0 & ~3) + lane;
   if (lane < 3 && u < p.n) {
@@ -1025,8 +1030,8 @@ __device__ void sort_targets(const ParamsR& p, int block, int4* keys) {
 
 // ROWS rows per block (32, or 8 where those leave SMs idle): 1024 / ROWS
 // threads share a row's groups, then its warps write s x and, where the row's
-// groups have different references, bring its E to one.  Blocks past the rows'
-// sort the targets.
+// groups have different references, bring its E to one.  The first blocks, the
+// longer ones, sort the targets.
 constexpr int kStatFewRows = 2048;  // 26 rows of 85000 words: 12.8 us by 32, 6.2 by 8
 template <int ROWS>
 __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const ParamsR p) {
@@ -1037,15 +1042,15 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
   __shared__ int sh_fix[ROWS];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  const int row_blocks = (p.n + ROWS - 1) / ROWS;
-  if (static_cast<int>(blockIdx.x) >= row_blocks) {
-    static_assert(sizeof(sh) >= kSortChunk * sizeof(int), "the keys share the rows' scratch");
-    sort_targets(p, static_cast<int>(blockIdx.x) - row_blocks, reinterpret_cast<int4*>(&sh[0][0]));
+  if (static_cast<int>(blockIdx.x) < p.sorting) {
+    static_assert(sizeof(sh) >= kSortChunk * sizeof(float), "the keys share the rows' scratch");
+    sort_targets(p, static_cast<int>(blockIdx.x), &sh[0][0]);
     return;
   }
+  const int block = static_cast<int>(blockIdx.x) - p.sorting;
   const int r0 = threadIdx.x % ROWS;
   const int slice = threadIdx.x / ROWS;
-  const int t = blockIdx.x * ROWS + r0;
+  const int t = block * ROWS + r0;
   float R = -INFINITY, S = 0.f, low = INFINITY, high = -INFINITY;
   if (t < p.n) {
     for (int g0 = slice; g0 < p.groups; g0 += 4 * SLICES) {
@@ -1103,7 +1108,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int rw = (threadIdx.x >> 5) / WARPS, sub = (threadIdx.x >> 5) % WARPS;
-  const int row = blockIdx.x * ROWS + rw;
+  const int row = block * ROWS + rw;
   if (row >= p.n) return;
   if (p.xs) {
     const float s = sh_s[rw];
@@ -1340,7 +1345,7 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
 }
 
 bool sizes_ok(int T, int d, int V, int piece) {
-  return T >= 0 && d >= 8 && (d & 7) == 0 && V >= 1 && V <= (1 << 24) && d <= (1 << 20) && piece >= 0;
+  return T >= 0 && d >= 8 && (d & 7) == 0 && V >= 1 && V < (1 << 24) && d <= (1 << 20) && piece >= 0;
 }
 
 #define DMOE_TRY(call)                \
@@ -1441,11 +1446,11 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     r.E = E, r.ldv = l.ldv;
     r.skey = skey, r.order = order;
     r.err = di.err_word;
-    const int sorting = dw ? ceil_div(n, kSortTokens) : 0;
+    r.sorting = dw ? ceil_div(n, kSortTokens) : 0;
     if (n <= kStatFewRows)
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<8>, dim3(ceil_div(n, 8) + sorting), dim3(kStatThreads), 0, st, r));
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<8>, dim3(ceil_div(n, 8) + r.sorting), dim3(kStatThreads), 0, st, r));
     else
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<32>, dim3(ceil_div(n, 32) + sorting), dim3(kStatThreads), 0, st, r));
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<32>, dim3(ceil_div(n, 32) + r.sorting), dim3(kStatThreads), 0, st, r));
     if (!grad) continue;
     if (dw)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),

@@ -545,7 +545,7 @@ size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, i
  *   aligned; calls sharing one must not overlap.
  * A target outside [0, V) other than ignore_index counts as ignored and sets
  * DMOE_SITE_LOSS_TARGET | DMOE_ERR_DEVICE.  When no target counts, the losses
- * and gradients are zero.  d a multiple of 8; 1 <= V <= 2^24; T == 0 writes
+ * and gradients are zero.  d a multiple of 8; 1 <= V < 2^24; T == 0 writes
  * only dw = 0 (unless accumulating). */
 dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, const int32_t* targets, int T, int d,
                                       int V, int ignore_index, const float* d_loss, float* loss, float* lse,
