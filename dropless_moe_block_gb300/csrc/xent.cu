@@ -1140,6 +1140,73 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
   }
 }
 
+// dW of a few tokens (n <= NT <= kFewTokens): rows of dW are then sums of a few
+// multiples of rows of x, bound by writing them, and need neither the tensor
+// cores nor the sort.  A block takes kFewRows words; their coefficients
+// s_t E_tv (c_t at a token's target) meet in shared memory in fp32, every
+// thread holds 8 columns of the n tokens' x.  32000 words, d = 4096: 54 us
+// for 8 tokens beside 59 for dx; with 9 tokens the tensor cores take 115 us
+// for both, and a launch before it.
+constexpr int kFewTokens = 8;
+constexpr int kFewRows = 64;
+constexpr int kFewThreads = 128;
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads)
+    few_dw_kernel(const uint16_t* __restrict__ E, int64_t ldv, const float2* __restrict__ coef,
+                  const int32_t* __restrict__ targets, const uint16_t* __restrict__ x, int n, int d, int V,
+                  int per_row, uint16_t* dw, float* dw32, const float* add) {
+  __shared__ float a[kFewRows][NT];
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  const int v0 = blockIdx.x * kFewRows;
+  for (int i = threadIdx.x; i < kFewRows * NT; i += kFewThreads) {
+    const int t = i / kFewRows, r = i % kFewRows, v = v0 + r;
+    float k = 0.f;
+    if (t < n && v < V) {
+      const float2 cf = __ldg(coef + t);
+      if (__ldg(targets + t) == v) k = cf.y;
+      else if (cf.x != 0.f) k = cf.x * __uint_as_float(static_cast<uint32_t>(__ldg(E + t * ldv + v)) << 16);
+    }
+    a[r][t] = k;
+  }
+  // per_row threads (a power of two) share a row, the others take further rows
+  const int c = (blockIdx.y * per_row + threadIdx.x % per_row) * 8;
+  float2 xf[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float f[8] = {};
+    if (t < n && c < d) unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xf[t][j] = make_float2(f[2 * j], f[2 * j + 1]);
+  }
+  __syncthreads();
+  if (c >= d) return;
+  const int rows = min(kFewRows, V - v0);
+#pragma unroll 2
+  for (int r = threadIdx.x / per_row; r < rows; r += kFewThreads / per_row) {
+    float2 o[4] = {};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float2 k = make_float2(a[r][t], a[r][t]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = f2_fma(k, xf[t][j], o[j]);
+    }
+    const int64_t at = static_cast<int64_t>(v0 + r) * d + c;
+    float f[8] = {o[0].x, o[0].y, o[1].x, o[1].y, o[2].x, o[2].y, o[3].x, o[3].y};
+    if (add) {
+      const float4 p = *reinterpret_cast<const float4*>(add + at), q = *reinterpret_cast<const float4*>(add + at + 4);
+      f[0] += p.x, f[1] += p.y, f[2] += p.z, f[3] += p.w;
+      f[4] += q.x, f[5] += q.y, f[6] += q.z, f[7] += q.w;
+    }
+    if (dw32) {
+      *reinterpret_cast<float4*>(dw32 + at) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(dw32 + at + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      *reinterpret_cast<uint4*>(dw + at) = pack8x(f);
+    }
+  }
+}
+
 // dx from the fp32 sums of its parts: one thread per 8 columns.
 __global__ void __launch_bounds__(256)
     join_dx_kernel(const float* __restrict__ part, int parts, int n, int d, const float2* __restrict__ coef,
@@ -1442,21 +1509,22 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     r.count = count;
     r.loss = loss + t0, r.lse = lse ? lse + t0 : nullptr;
     r.coef = coef;
-    r.x = xp, r.xs = dw ? xs : nullptr;
+    const bool few = n <= kFewTokens;
+    r.x = xp, r.xs = dw && !few ? xs : nullptr;
     r.E = E, r.ldv = l.ldv;
     r.skey = skey, r.order = order;
     r.err = di.err_word;
-    r.sorting = dw ? ceil_div(n, kSortTokens) : 0;
+    r.sorting = dw && !few ? ceil_div(n, kSortTokens) : 0;
     if (n <= kStatFewRows)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<8>, dim3(ceil_div(n, 8) + r.sorting), dim3(kStatThreads), 0, st, r));
     else
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(row_stats_kernel<32>, dim3(ceil_div(n, 32) + r.sorting), dim3(kStatThreads), 0, st, r));
     if (!grad) continue;
-    if (dw)
+    if (dw && !few)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
                                        dim3(128), 0, st, xp, n, d, V, static_cast<const int32_t*>(skey),
                                        static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs));
-    const int parts = dx ? dx_parts(n, d, V, dw != nullptr) : 1;
+    const int parts = dx ? dx_parts(n, d, V, dw && !few) : 1;
     Grid gx{}, gw{};
     // E as [n, V] with row pitch ldv: the columns past V read as zero
     if (dx) {
@@ -1464,7 +1532,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
         return DMOE_ERR_CUDA;
       gx = make_grid(n, d, V, 16, parts);
     }
-    if (dw) {
+    if (dw && !few) {
       if (!dmoe::make_map_ld(&p.map_a2, E, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b2, xs, n, d, 64, BK))
         return DMOE_ERR_CUDA;
       gw = make_grid(V, d, n, 1);
@@ -1482,7 +1550,16 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       p.dw32 = last ? nullptr : acc;
       p.dw_add = t0 > 0 ? acc : nullptr;
     }
-    DMOE_TRY((launch_head<true, 2>(p, gx, gw, di, st)));
+    if (dw && few) {
+      int per_row = 1;
+      while (per_row < kFewThreads && per_row * 8 < d) per_row *= 2;
+      const dim3 grid(ceil_div(V, kFewRows), ceil_div(d, per_row * 8));
+      auto kern = n <= 2 ? few_dw_kernel<2> : n <= 4 ? few_dw_kernel<4> : few_dw_kernel<kFewTokens>;
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(kern, grid, dim3(kFewThreads), 0, st, static_cast<const uint16_t*>(E), l.ldv,
+                                       static_cast<const float2*>(coef), tp, xp, n, d, V, per_row, p.dw, p.dw32,
+                                       p.dw_add));
+    }
+    if (gx.items + gw.items > 0) DMOE_TRY((launch_head<true, 2>(p, gx, gw, di, st)));
     if (gx.parts > 1)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(join_dx_kernel, dim3(ceil_div(static_cast<int64_t>(n) * (d / 8), 256)), dim3(256),
                                        0, st, static_cast<const float*>(part), gx.parts, n, d,

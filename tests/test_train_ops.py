@@ -258,7 +258,9 @@ def test_norm_backward_against_differences(dm):
 LOSS_SIZES = [(1, 1, 8), (1, 2, 8), (5, 7, 16), (3, 129, 72), (33, 1009, 256), (130, 300, 64), (257, 513, 136),
               (300, 1024, 520), (513, 2050, 64), (64, 5003, 1032),
               # enough tiles for the widest ones, several a unit, a narrow last column
-              (300, 38900, 1032), (2, 6000, 1288)]
+              (300, 38900, 1032), (2, 6000, 1288),
+              # the last counts of the few-token form, and the first beyond it
+              (8, 130, 1096), (4, 65, 24), (9, 130, 1096)]
 
 
 def run_loss(dm, x, w, t, dx=True, dw=torch.bfloat16, **kw):
@@ -354,8 +356,9 @@ def test_loss_in_a_graph(dm):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_loss_in_pieces(dm, dtype):
-    T, V, d = 700, 391, 88
+@pytest.mark.parametrize("T", [700, 517])  # the last piece of 517 has 5 tokens
+def test_loss_in_pieces(dm, dtype, T):
+    V, d = 391, 88
     x, w = randn(34, T, d), randn(35, V, d, scale=0.3)
     t = torch.randint(0, V, (T,), generator=gen(36), dtype=torch.int32)
     t[200:500] = -1  # a whole piece without a target that counts
