@@ -95,7 +95,6 @@ constexpr int kPieceMax = 1 << 18;
 constexpr int kNarrowD = 1024;
 
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
-constexpr int kMaxSplit = 64;
 constexpr int kRun = 32;             // positions per partial sum of launch 3
 constexpr int kDirect = 4;           // words with up to so many tokens are summed by dW's epilogue itself
 
@@ -1280,27 +1279,38 @@ int logits_tile(int n, int d, int V) {
 // Time of a gradient item in K slices: its product, or, where K is short, its
 // epilogue (256 x 512 outputs take as long as about 9 slices).
 constexpr int kEpilogueSlices = 9;
-int item_slices(const Grid& g) { return std::max(g.per_part, g.cols > BN ? kEpilogueSlices : kEpilogueSlices / 2 + 1); }
+int item_time(int slices, int cols) { return std::max(slices, cols > BN ? kEpilogueSlices : kEpilogueSlices / 2 + 1); }
+int item_slices(const Grid& g) { return item_time(g.per_part, g.cols); }
 
 // Deals the items of two grids (the second may have none) to U units: the
 // longer ones into grid[0], and how many of the shorter ones the units with
-// one long item fewer take first (item_of()).  Returns the slices of the unit
+// one long item fewer take first (item_of()).  busiest: the slices of the unit
 // that has most.
-int64_t deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
+struct Dealt {
+  int full, rem, early, extra;
+  int64_t busiest;
+};
+Dealt dealt(int n0, int64_t l0, int n1, int64_t l1, int U) {  // the longer items first
+  Dealt r{};
+  r.full = n0 / U;
+  r.rem = n0 % U;
+  r.early = r.rem > 0 && n1 > 0 ? U - r.rem : 0;
+  r.extra = r.early > 0 ? static_cast<int>((l0 + l1 / 2) / l1) : 0;
+  const int64_t taken = std::min<int64_t>(n1, static_cast<int64_t>(r.early) * r.extra);
+  const int64_t rest = n1 - taken, round = rest / U, left = rest % U;
+  const int64_t a = (r.full + (r.rem > 0)) * l0 + (round + (left > 0)) * l1;
+  const int64_t b = r.early == 0 ? 0 : r.full * l0 + (ceil_div(taken, r.early) + round + (left > r.rem)) * l1;
+  r.busiest = std::max(a, b);
+  return r;
+}
+
+void deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
   p.first_dx = gx.items > 0 && (gw.items == 0 || item_slices(gx) >= item_slices(gw));
   p.grid[0] = p.first_dx ? gx : gw;
   p.grid[1] = p.first_dx ? gw : gx;
-  const int n0 = p.grid[0].items, n1 = p.grid[1].items;
-  const int64_t l0 = item_slices(p.grid[0]), l1 = n1 > 0 ? item_slices(p.grid[1]) : 1;
-  p.full = n0 / U;
-  p.rem = n0 % U;
-  p.early = p.rem > 0 && n1 > 0 ? U - p.rem : 0;
-  p.extra = p.early > 0 ? static_cast<int>((l0 + l1 / 2) / l1) : 0;
-  const int64_t taken = std::min<int64_t>(n1, static_cast<int64_t>(p.early) * p.extra);
-  const int64_t rest = n1 - taken, round = rest / U, left = rest % U;
-  const int64_t a = (p.full + (p.rem > 0)) * l0 + (round + (left > 0)) * l1;
-  const int64_t b = p.early == 0 ? 0 : p.full * l0 + (ceil_div(taken, p.early) + round + (left > p.rem)) * l1;
-  return std::max(a, b);
+  const Dealt r = dealt(p.grid[0].items, item_slices(p.grid[0]), p.grid[1].items,
+                        p.grid[1].items > 0 ? item_slices(p.grid[1]) : 1, U);
+  p.full = r.full, p.rem = r.rem, p.early = r.early, p.extra = r.extra;
 }
 
 // Parts of dx's sum over the vocabulary.  dx has few tiles of V / 64 slices
@@ -1309,14 +1319,15 @@ int64_t deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
 // shortest, charging the fp32 sums that parts write and read back in slices
 // (about 0.5 us each): 12 bytes an element at 6.5 TB/s, and a launch.
 int dx_parts(int n, int d, int V, bool dw) {
-  ParamsX p{};
-  const Grid gw = dw ? make_grid(V, d, n, 1) : Grid{};
+  const int tiles = ceil_div(n, 2 * BM) * ceil_div(d, 2 * BN), slices = ceil_div(V, BK);
+  const int nw = dw ? ceil_div(V, 2 * BM) * ceil_div(d, 2 * BN) : 0;
+  const int64_t lw = item_time(ceil_div(n, BK), d);
   int best = 1;
   int64_t best_cost = -1;
-  for (int s = 1; s <= kMaxSplit; ++s) {
-    const Grid gx = make_grid(n, d, V, 1, s);
-    if (s > 1 && gx.slices / s < 8) break;
-    int64_t cost = deal(p, gx, gw, kUnits);
+  for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+    if (s > 1 && slices / s < 8) break;
+    const int64_t lx = item_time(ceil_div(slices, s), d);
+    int64_t cost = (nw == 0 || lx >= lw ? dealt(tiles * s, lx, nw, lw, kUnits) : dealt(nw, lw, tiles * s, lx, kUnits)).busiest;
     if (s > 1) cost += 10 + static_cast<int64_t>(s) * n * d / 270000;
     if (best_cost < 0 || cost < best_cost) {
       best = s;
@@ -1367,7 +1378,7 @@ struct Layout {
   int64_t ldp;     // row pitch of sums and refs
   int64_t ldv;     // row pitch of the exponentials
   int64_t groups;
-  size_t count, sums, refs, target_logit, coef, skey, order, xs, runs, part, acc, E, total;
+  size_t count, sums, refs, target_logit, coef, skey, order, xs, runs, acc, E, part;
 };
 
 Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
@@ -1394,21 +1405,22 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
     l.order = take(rows * sizeof(int32_t));
     l.xs = take(rows * d * 2);
     l.runs = take(rows * d * sizeof(float));
-    // the full pieces' and the last, shorter one's dx parts
-    size_t part = 0;
-    for (const int64_t n : {std::min<int64_t>(l.piece, T), T % l.piece}) {
-      for (const bool dw : {false, true}) {
-        const int s = n > 0 ? dx_parts(static_cast<int>(n), d, V, dw) : 1;
-        if (s > 1) part = std::max(part, static_cast<size_t>(n) * s * d * sizeof(float));
-      }
-    }
-    l.part = take(part);
     // dW of earlier pieces, when it does not fit the output's own type
     l.acc = take(dw_bf16 && T > l.piece ? static_cast<size_t>(V) * d * sizeof(float) : 0);
     l.E = take(static_cast<size_t>(l.piece * l.ldv) * 2);
   }
-  l.total = at;
+  l.part = at;  // dx's parts come last, see part_bytes()
   return l;
+}
+
+// Bytes of dx's fp32 parts: the full pieces' or the last, shorter one's.
+size_t part_bytes(const Layout& l, int T, int d, int V, bool dw) {
+  size_t most = 0;
+  for (const int64_t n : {std::min<int64_t>(l.piece, T), T % l.piece}) {
+    const int s = n > 0 ? dx_parts(static_cast<int>(n), d, V, dw && n > kFewTokens) : 1;
+    if (s > 1) most = std::max(most, static_cast<size_t>(n) * s * d * sizeof(float));
+  }
+  return most;
 }
 
 bool sizes_ok(int T, int d, int V, int piece) {
@@ -1432,7 +1444,8 @@ bool sizes_ok(int T, int d, int V, int piece) {
 
 DMOE_API size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, int dw_f32, int piece) {
   if (!sizes_ok(T, d, V, piece)) return 0;
-  return layout_of(T, d, V, grad != 0, !dw_f32, piece).total;
+  const Layout l = layout_of(T, d, V, grad != 0, !dw_f32, piece);
+  return l.part + (grad ? std::max(part_bytes(l, T, d, V, false), part_bytes(l, T, d, V, true)) : 0);
 }
 
 DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, const int32_t* targets, int T,
@@ -1448,7 +1461,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
         reinterpret_cast<uintptr_t>(loss) | reinterpret_cast<uintptr_t>(lse)) & 3))
     return DMOE_ERR_INVALID_ARG;
   const Layout l = layout_of(T, d, V, grad, dw && !dw_f32, piece);
-  if (T > 0 && ws_bytes < l.total) return DMOE_ERR_INVALID_ARG;
+  if (T > 0 && ws_bytes < l.part + (dx ? part_bytes(l, T, d, V, dw != nullptr) : 0)) return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;
   DMOE_TRY(dmoe::device_info(&di));
   cudaStream_t st = dmoe::as_stream(stream);
