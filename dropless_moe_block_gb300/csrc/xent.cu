@@ -24,7 +24,7 @@
 //              exists; without, nothing is written.
 //   2 rows     the pairs of a row meet in lse_t; loss_t, s_t, c_t, s_t x_t; the
 //              tokens ordered by target
-//   3 targets  sums of c_t x_t, up to 32 tokens each, for words with many
+//   3 targets  sums of c_t x_t by word, up to 32 tokens each
 //   4 grads    the tiles of both products in one launch
 //
 // ref is 0 while the largest of a row's 64 logits lies in [kRefLow,
@@ -96,7 +96,13 @@ constexpr int kNarrowD = 1024;
 
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
 constexpr int kRun = 32;             // positions per partial sum of launch 3
-constexpr int kDirect = 4;           // words with up to so many tokens are summed by dW's epilogue itself
+// Words with at most so many tokens are summed by dW's epilogue itself, token
+// by token.  From kDirectFrom tokens on that hides behind the tile's product,
+// and keeps launch 3 from writing a row for every token (34 MB at 8192 x 512).
+// With fewer tokens the product is short, and the epilogue adds launch 3's
+// rows only (1216 x 736 x 41031: gradients 166 us with 4, DISCARD with 0).
+constexpr int kDirect = 4;
+constexpr int kDirectFrom = 4096;
 
 template <bool GRAD, int NS>
 struct PlanX {
@@ -184,6 +190,7 @@ struct ParamsX {
   const float* dw_add; // fp32 dW of earlier pieces (or what the caller adds to)
   const int32_t* skey;   // targets in ascending order
   const int32_t* order;  // their tokens, ascending among equal targets
+  int direct;            // words with more tokens have sums in runs
   const float* runs;     // launch 3's sums, at the position of their first token
 };
 
@@ -375,11 +382,29 @@ __device__ __forceinline__ void add_row32(float* v, const float* a, int cols) {
   }
 }
 
-__device__ __forceinline__ void store_row32(float* o, const float* v, int cols) {
+// write_rows32 with fp32 values: 16 columns at a time fill the slab's rows.
+__device__ __forceinline__ void write_rows32(uint32_t slab, int lane, const float* v, float* out, int64_t ld, int rows,
+                                             int cols) {
+  const int sw = (lane >> 1) & 3;
+  const int j = lane & 3, r0 = lane >> 2;
+  out += r0 * ld + 4 * j;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (4 * j < cols)
-      *(reinterpret_cast<float4*>(o) + j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float* f = v + 16 * h + 4 * q;
+      st_shared(slab + lane * 64 + ((q ^ sw) << 4), make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                                              __float_as_uint(f[2]), __float_as_uint(f[3])));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + r0;
+      const uint4 u = ld_shared(slab + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+      if (r < rows && 16 * h + 4 * j < cols) *reinterpret_cast<uint4*>(out + 8 * i * ld + 16 * h) = u;
+    }
+    __syncwarp();
+  }
 }
 
 // One unit of work: a tile of one product over a range of K slices.
@@ -830,7 +855,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
             if (cols <= 0) continue;
             if (it.dx) {
               if (p.dx_part) {
-                store_row32(p.dx_part + (static_cast<int64_t>(it.part) * p.n + row) * p.d + ch, v, row < M ? cols : 0);
+                write_rows32(slab, lane, v, p.dx_part + (static_cast<int64_t>(it.part) * p.n + row0) * p.d + ch, p.d,
+                             rows, cols);
               } else {
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = cf.x == 0.f ? 0.f : v[q] * cf.x;
@@ -838,7 +864,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
                 write_rows32(slab, lane, v, p.dx + static_cast<int64_t>(row0) * p.d + ch, p.d, rows, cols);
               }
             } else {
-              if (tokens > kDirect) {
+              if (tokens > p.direct) {
                 for (int q = first; q < first + tokens; q = (q / kRun + 1) * kRun)
                   add_row32(v, p.runs + static_cast<int64_t>(q) * p.d + ch, cols);
               } else {
@@ -848,7 +874,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
                 }
               }
               if (p.dw_add && row < M) add_row32(v, p.dw_add + static_cast<int64_t>(row) * p.d + ch, cols);
-              if (p.dw32) store_row32(p.dw32 + static_cast<int64_t>(row) * p.d + ch, v, row < M ? cols : 0);
+              if (p.dw32) write_rows32(slab, lane, v, p.dw32 + static_cast<int64_t>(row0) * p.d + ch, p.d, rows, cols);
               else write_rows32(slab, lane, v, p.dw + static_cast<int64_t>(row0) * p.d + ch, p.d, rows, cols);
             }
           }
@@ -876,16 +902,17 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
 // ------------------------------------------------------- tokens by target
 
 
-// Sums of c_t x_t for words with more than kDirect tokens, in blocks of kRun =
-// 32 positions of the sorted order: runs[r], r a word's first position or a
-// multiple of 32, sums its tokens from there to the end of the block.  (A
-// word's few tokens on both sides of a block's edge get theirs as well.)  One
-// warp per block of positions and kRunCols columns.
+// Sums of c_t x_t by word, in blocks of kRun = 32 positions of the sorted
+// order: runs[r], r a word's first position or a multiple of 32, sums its
+// tokens from there to the end of the block.  Words of at most `direct` tokens
+// inside one block are left out.  One warp per block of positions and kRunCols
+// columns, eight rows in flight.
 constexpr int kRunCols = 256;
 static_assert(kRun == 32, "a lane per position");
 __global__ void __launch_bounds__(128)
-    target_runs_kernel(const uint16_t* __restrict__ x, int n, int d, int V, const int32_t* __restrict__ skey,
-                       const int32_t* __restrict__ order, const float2* __restrict__ coef, float* __restrict__ runs) {
+    target_runs_kernel(const uint16_t* __restrict__ x, int n, int d, int V, int direct,
+                       const int32_t* __restrict__ skey, const int32_t* __restrict__ order,
+                       const float2* __restrict__ coef, float* __restrict__ runs) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -893,44 +920,49 @@ __global__ void __launch_bounds__(128)
   if (base >= n) return;
   const int r = base + lane;
   const int key = r < n ? __ldg(skey + r) : -1;
-  const int before = r > 0 && r < n ? __ldg(skey + r - 1) : -1;
+  const int before = r > 0 && r <= n ? __ldg(skey + r - 1) : -1;  // (the end of the tokens starts a "word", too)
   const int after = base + kRun < n ? __ldg(skey + base + kRun) : -1;
+  const bool word = r < n && key < V;
+  const int token = word ? __ldg(order + r) : 0;
+  const float weight = word ? __ldg(&coef[token].y) : 0.f;
+  // this position's word: positions s .. e - 1 of the block
   const uint32_t starts = __ballot_sync(0xffffffffu, lane == 0 || key != before);
-  const int token = r < n && key < V ? __ldg(order + r) : 0;
-  const float weight = r < n && key < V ? __ldg(&coef[token].y) : 0.f;
+  const int s = 31 - __clz(starts & (0xffffffffu >> (31 - lane)));
+  const uint32_t later = lane == 31 ? 0u : starts >> (lane + 1);
+  const int e = later ? lane + __ffs(later) : 32;
+  const int left = __shfl_sync(0xffffffffu, before, 0);  // the key before the block
+  const bool crosses = (s == 0 && left == key) || (e == 32 && after == key);
+  const uint32_t need = __ballot_sync(0xffffffffu, word && (e - s > direct || crosses));
   const int c = blockIdx.y * kRunCols + lane * 8;
   const uint16_t* col = x + (c < d ? c : 0);
-  for (uint32_t left = starts; left;) {
-    const int s = __ffs(left) - 1;  // a word's positions s .. e - 1 of this block
-    left &= left - 1;
-    const int e = left ? __ffs(left) - 1 : 32;
-    const int k = __shfl_sync(0xffffffffu, key, s);
-    const bool crosses = (s == 0 && __shfl_sync(0xffffffffu, before, 0) == k) || (e == 32 && after == k);
-    if (k < 0 || k >= V || (e - s <= kDirect && !crosses)) continue;
-    float acc[8] = {};
+  float acc[8] = {};
 #pragma unroll 1
-    for (int q = s; q < e; q += 8) {  // eight rows in flight
-      uint4 u[8];
+  for (int b = 0; b < 32; b += 8) {
+    if (!((need >> b) & 0xffu)) continue;
+    uint4 u[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = __shfl_sync(0xffffffffu, token, min(q + j, 31));
-        u[j] = __ldg(reinterpret_cast<const uint4*>(col + static_cast<int64_t>(t) * d));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = __shfl_sync(0xffffffffu, weight, min(q + j, 31));
-        float f[8];
-        unpack8x(u[j], f);
-        if (q + j < e) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
-        }
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int t = __shfl_sync(0xffffffffu, token, b + j);
+      u[j] = __ldg(reinterpret_cast<const uint4*>(col + static_cast<int64_t>(t) * d));
     }
-    if (c < d) {
-      float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(base + s) * d + c);
-      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float w = __shfl_sync(0xffffffffu, weight, b + j);
+      const int from = __shfl_sync(0xffffffffu, s, b + j), end = __shfl_sync(0xffffffffu, e, b + j);
+      if (!((need >> (b + j)) & 1u)) continue;
+      float f[8];
+      unpack8x(u[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      if (b + j + 1 == end) {  // the word's last position here
+        if (c < d) {
+          float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(base + from) * d + c);
+          o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+      }
     }
   }
 }
@@ -1206,28 +1238,39 @@ __global__ void __launch_bounds__(kFewThreads)
   }
 }
 
-// dx from the fp32 sums of its parts: one thread per 8 columns.
+// dx from the fp32 sums of its parts: SHARE threads (1, or 8 where there are
+// many parts) per 8 columns.
+template <int SHARE>
 __global__ void __launch_bounds__(256)
     join_dx_kernel(const float* __restrict__ part, int parts, int n, int d, const float2* __restrict__ coef,
                    const int32_t* __restrict__ targets, const uint16_t* __restrict__ W, uint16_t* __restrict__ dx) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int nvec = d / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(n) * nvec) return;
+  const int64_t all = static_cast<int64_t>(n) * nvec;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / SHARE;
+  const int mine = threadIdx.x % SHARE;
+  const int64_t i = at < all ? at : all - 1;  // every lane takes part in the sum
   const int64_t t = i / nvec;
   const int c = static_cast<int>(i - t * nvec) * 8;
   const float2 cf = __ldg(coef + t);
+  const int target = __ldg(targets + t);
   float acc[8] = {};
 #pragma unroll 4
-  for (int q = 0; q < parts; ++q) {
+  for (int q = mine; q < parts; q += SHARE) {
     const float4* a = reinterpret_cast<const float4*>(part + (static_cast<int64_t>(q) * n + t) * d + c);
     const float4 u = __ldg(a), v = __ldg(a + 1);
     acc[0] += u.x, acc[1] += u.y, acc[2] += u.z, acc[3] += u.w;
     acc[4] += v.x, acc[5] += v.y, acc[6] += v.z, acc[7] += v.w;
   }
+#pragma unroll
+  for (int o = SHARE / 2; o > 0; o /= 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+  }
+  if (mine != 0 || at >= all) return;
   float f[8] = {};
-  if (cf.y != 0.f) unpack8x(__ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(__ldg(targets + t)) * d + c)), f);
+  if (cf.y != 0.f) unpack8x(__ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(target) * d + c)), f);
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = fmaf(cf.y, f[j], cf.x == 0.f ? 0.f : acc[j] * cf.x);
   *reinterpret_cast<uint4*>(dx + t * d + c) = pack8x(f);
@@ -1491,6 +1534,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     const int32_t* tp = targets + t0;
     ParamsX p{};
     p.n = n, p.d = d, p.V = V;
+    p.direct = n >= kDirectFrom ? kDirect : 0;
     p.a_rows = static_cast<int>(std::min<int64_t>(BM, round_up(n, 8)));
     p.targets = tp;
     p.err = di.err_word;
@@ -1535,7 +1579,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     if (!grad) continue;
     if (dw && !few)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
-                                       dim3(128), 0, st, xp, n, d, V, static_cast<const int32_t*>(skey),
+                                       dim3(128), 0, st, xp, n, d, V, p.direct, static_cast<const int32_t*>(skey),
                                        static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs));
     const int parts = dx ? dx_parts(n, d, V, dw && !few) : 1;
     Grid gx{}, gw{};
@@ -1573,10 +1617,13 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
                                        p.dw_add));
     }
     if (gx.items + gw.items > 0) DMOE_TRY((launch_head<true, 2>(p, gx, gw, di, st)));
-    if (gx.parts > 1)
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(join_dx_kernel, dim3(ceil_div(static_cast<int64_t>(n) * (d / 8), 256)), dim3(256),
-                                       0, st, static_cast<const float*>(part), gx.parts, n, d,
+    if (gx.parts > 1) {
+      const int share = gx.parts >= 8 ? 8 : 1;
+      auto kern = share == 8 ? join_dx_kernel<8> : join_dx_kernel<1>;
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(kern, dim3(ceil_div(static_cast<int64_t>(n) * (d / 8) * share, 256)), dim3(256), 0,
+                                       st, static_cast<const float*>(part), gx.parts, n, d,
                                        static_cast<const float2*>(coef), tp, w, dx + t0 * d));
+    }
   }
   return DMOE_OK;
 }
