@@ -100,7 +100,7 @@ constexpr int kRun = 32;             // positions per partial sum of launch 3
 // by token.  From kDirectFrom tokens on that hides behind the tile's product,
 // and keeps launch 3 from writing a row for every token (34 MB at 8192 x 512).
 // With fewer tokens the product is short, and the epilogue adds launch 3's
-// rows only (1216 x 736 x 41031: gradients 166 us with 4, DISCARD with 0).
+// rows only (1216 x 736 x 41031: gradients 169 us with 4, 162 with 0).
 constexpr int kDirect = 4;
 constexpr int kDirectFrom = 4096;
 
@@ -189,6 +189,7 @@ struct ParamsX {
   float* dw32;         // or in fp32
   const float* dw_add; // fp32 dW of earlier pieces (or what the caller adds to)
   const int32_t* skey;   // targets in ascending order
+  const int2* words;     // positions [x, y) of a word's tokens, for words that have some
   const int32_t* order;  // their tokens, ascending among equal targets
   int direct;            // words with more tokens have sums in runs
   const float* runs;     // launch 3's sums, at the position of their first token
@@ -463,15 +464,8 @@ __device__ __forceinline__ bool item_of(const ParamsX& p, int u, int U, int j, I
   return true;
 }
 
-// First position of a sorted array whose key is not below v.
-__device__ __forceinline__ int lower_bound(const int32_t* __restrict__ a, int n, int v) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a + mid) < v) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
+__device__ __forceinline__ void prefetch_l1(const void* a) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<uint64_t>(a)) : "memory");
 }
 
 // A target's word, V for one that does not count.
@@ -763,8 +757,22 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           target = __ldg(p.targets + row);
           if (GRAD) cf = __ldg(p.coef + row);
         } else {
-          first = lower_bound(p.skey, p.n, row);
-          tokens = lower_bound(p.skey, p.n, row + 1) - first;
+          // a word without tokens holds what an earlier call left there
+          const int2 at = __ldg(p.words + row);
+          if (static_cast<unsigned>(at.x) < static_cast<unsigned>(p.n) && __ldg(p.skey + at.x) == row) {
+            first = at.x;
+            tokens = at.y - at.x;
+            // the sums it will add (1216 x 736 x 41031: gradients 152 us with
+            // two binary searches and no prefetch, 149 so; 126 without the
+            // additions, which registers are too few to fetch earlier)
+            if (tokens > p.direct) {
+              const float* a = p.runs + static_cast<int64_t>(first) * p.d + it.n * NS * BN + part * 64;
+              const int cols = p.d - (it.n * NS * BN + part * 64);
+#pragma unroll
+              for (int i = 0; i < 2 * NS; ++i)
+                if ((i >> 1) * BN + (i & 1) * 32 < cols) prefetch_l1(a + (i >> 1) * BN + (i & 1) * 32);
+            }
+          }
         }
       }
 #pragma unroll
@@ -904,7 +912,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
 
 // Sums of c_t x_t by word, in blocks of kRun = 32 positions of the sorted
 // order: runs[r], r a word's first position or a multiple of 32, sums its
-// tokens from there to the end of the block.  Words of at most `direct` tokens
+// tokens from there to the end of the block; and words[v], where a word's
+// tokens begin and end.  Words of at most `direct` tokens
 // inside one block are left out.  One warp per block of positions and kRunCols
 // columns, eight rows in flight.
 constexpr int kRunCols = 256;
@@ -912,7 +921,7 @@ static_assert(kRun == 32, "a lane per position");
 __global__ void __launch_bounds__(128)
     target_runs_kernel(const uint16_t* __restrict__ x, int n, int d, int V, int direct,
                        const int32_t* __restrict__ skey, const int32_t* __restrict__ order,
-                       const float2* __restrict__ coef, float* __restrict__ runs) {
+                       const float2* __restrict__ coef, float* __restrict__ runs, int2* __restrict__ words) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -933,6 +942,10 @@ __global__ void __launch_bounds__(128)
   const int left = __shfl_sync(0xffffffffu, before, 0);  // the key before the block
   const bool crosses = (s == 0 && left == key) || (e == 32 && after == key);
   const uint32_t need = __ballot_sync(0xffffffffu, word && (e - s > direct || crosses));
+  if (blockIdx.y == 0 && word) {  // where the word's tokens begin and end
+    if (lane == s && !(s == 0 && left == key)) words[key].x = r;
+    if (lane + 1 == e && !(e == 32 && after == key)) words[key].y = r + 1;
+  }
   const int c = blockIdx.y * kRunCols + lane * 8;
   const uint16_t* col = x + (c < d ? c : 0);
   float acc[8] = {};
@@ -1421,7 +1434,7 @@ struct Layout {
   int64_t ldp;     // row pitch of sums and refs
   int64_t ldv;     // row pitch of the exponentials
   int64_t groups;
-  size_t count, sums, refs, target_logit, coef, skey, order, xs, runs, acc, E, part;
+  size_t count, sums, refs, target_logit, coef, skey, order, words, xs, runs, acc, E, part;
 };
 
 Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
@@ -1446,6 +1459,7 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
     l.coef = take(rows * sizeof(float2));
     l.skey = take(rows * sizeof(int32_t));
     l.order = take(rows * sizeof(int32_t));
+    l.words = take(static_cast<size_t>(V) * sizeof(int2));
     l.xs = take(rows * d * 2);
     l.runs = take(rows * d * sizeof(float));
     // dW of earlier pieces, when it does not fit the output's own type
@@ -1522,6 +1536,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
   float2* coef = reinterpret_cast<float2*>(at(l.coef));
   int32_t* skey = reinterpret_cast<int32_t*>(at(l.skey));
   int32_t* order = reinterpret_cast<int32_t*>(at(l.order));
+  int2* words = reinterpret_cast<int2*>(at(l.words));
   uint16_t* xs = reinterpret_cast<uint16_t*>(at(l.xs));
   float* runs = reinterpret_cast<float*>(at(l.runs));
   float* part = reinterpret_cast<float*>(at(l.part));
@@ -1580,7 +1595,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     if (dw && !few)
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
                                        dim3(128), 0, st, xp, n, d, V, p.direct, static_cast<const int32_t*>(skey),
-                                       static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs));
+                                       static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs, words));
     const int parts = dx ? dx_parts(n, d, V, dw && !few) : 1;
     Grid gx{}, gw{};
     // E as [n, V] with row pitch ldv: the columns past V read as zero
@@ -1597,7 +1612,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     p.coef = coef, p.W = w, p.x = xp;
     p.dx = dx ? dx + t0 * d : nullptr;
     p.dx_part = gx.parts > 1 ? part : nullptr;
-    p.skey = skey, p.order = order, p.runs = runs;
+    p.skey = skey, p.order = order, p.runs = runs, p.words = words;
     const bool last = t0 + n >= T;
     if (dw_f32) {
       p.dw32 = static_cast<float*>(dw);
