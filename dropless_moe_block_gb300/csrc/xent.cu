@@ -94,6 +94,7 @@ constexpr int kPieceMax = 1 << 18;
 // count: with its gradients 3828 / 3814 us.
 constexpr int kNarrowD = 1024;
 
+constexpr int kFewTokens = 8;        // dW of so few tokens has a form of its own
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
 constexpr int kRun = 32;             // positions per partial sum of launch 3
 // Words with at most so many tokens are summed by dW's epilogue itself, token
@@ -170,6 +171,7 @@ struct ParamsX {
   int32_t* err;
   // logits
   uint16_t* E;         // [n][ldv] exponentials (NULL: the loss alone)
+  float* E32;          // the same unrounded, of few tokens (else NULL)
   int64_t ldv;
   float* sums;         // [V / 64][ldp] sums of exponentials, negative where the
   float* refs;         // reference is not 0 but this one
@@ -593,8 +595,14 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
     if (!GRAD && rank == 1 && unit == 0 && p.all) {
       // a warp without other work counts the targets that count
       int c = 0;
-#pragma unroll 8
-      for (int i = lane; i < p.T; i += 32) c += key_of(__ldg(p.all + i), p.V, p.ignore) < p.V;
+#pragma unroll 1
+      for (int i0 = lane; i0 < p.T; i0 += 32 * 16) {
+        int t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = i0 + 32 * i < p.T ? __ldg(p.all + i0 + 32 * i) : p.ignore;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c += key_of(t[i], p.V, p.ignore) < p.V;
+      }
       c = __reduce_add_sync(0xffffffffu, c);
       if (lane == 0) *p.count = c;
     }
@@ -837,6 +845,11 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
             p.sums[at] = shift ? -fabsf(sum) : fabsf(sum);
             if (shift) p.refs[at] = ref;
           }
+          if (p.E32 && row < p.n) {
+            float4* o = reinterpret_cast<float4*>(p.E32 + static_cast<int64_t>(row) * p.ldv + c);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
           if (p.E) {
             if (here) {  // the target's own element is added in fp32 by the gradients
 #pragma unroll
@@ -1011,6 +1024,7 @@ struct ParamsR {
   const uint16_t* x;
   uint16_t* xs;       // s x in bf16 (NULL: no dW)
   uint16_t* E;
+  float* E32;
   int64_t ldv;
   int sorting;        // blocks that sort
   int32_t* skey;
@@ -1180,23 +1194,27 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
       f.x = fix == 2 ? 0.f : f.x * k;
       f.y = fix == 2 ? 0.f : f.y * k;
       *u = __floats2bfloat162_rn(f.x, f.y);
+      if (p.E32) {
+        float2* u32 = reinterpret_cast<float2*>(p.E32 + row * p.ldv + g * kGroup) + lane;
+        *u32 = fix == 2 ? make_float2(0.f, 0.f) : make_float2(u32->x * k, u32->y * k);
+      }
     }
   }
 }
 
 // dW of a few tokens (n <= NT <= kFewTokens): rows of dW are then sums of a few
 // multiples of rows of x, bound by writing them, and need neither the tensor
-// cores nor the sort.  A block takes kFewRows words; their coefficients
+// cores nor the sort, and E can stay in fp32 (with so few terms its rounding
+// would not average out).  A block takes kFewRows words; their coefficients
 // s_t E_tv (c_t at a token's target) meet in shared memory in fp32, every
 // thread holds 8 columns of the n tokens' x.  32000 words, d = 4096: 54 us
 // for 8 tokens beside 59 for dx; with 9 tokens the tensor cores take 115 us
 // for both, and a launch before it.
-constexpr int kFewTokens = 8;
 constexpr int kFewRows = 64;
 constexpr int kFewThreads = 128;
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads)
-    few_dw_kernel(const uint16_t* __restrict__ E, int64_t ldv, const float2* __restrict__ coef,
+    few_dw_kernel(const float* __restrict__ E32, int64_t ldv, const float2* __restrict__ coef,
                   const int32_t* __restrict__ targets, const uint16_t* __restrict__ x, int n, int d, int V,
                   int per_row, uint16_t* dw, float* dw32, const float* add) {
   __shared__ float a[kFewRows][NT];
@@ -1209,7 +1227,7 @@ __global__ void __launch_bounds__(kFewThreads)
     if (t < n && v < V) {
       const float2 cf = __ldg(coef + t);
       if (__ldg(targets + t) == v) k = cf.y;
-      else if (cf.x != 0.f) k = cf.x * __uint_as_float(static_cast<uint32_t>(__ldg(E + t * ldv + v)) << 16);
+      else if (cf.x != 0.f) k = cf.x * __ldg(E32 + t * ldv + v);
     }
     a[r][t] = k;
   }
@@ -1434,7 +1452,7 @@ struct Layout {
   int64_t ldp;     // row pitch of sums and refs
   int64_t ldv;     // row pitch of the exponentials
   int64_t groups;
-  size_t count, sums, refs, target_logit, coef, skey, order, words, xs, runs, acc, E, part;
+  size_t count, sums, refs, target_logit, coef, skey, order, words, xs, runs, acc, E32, E, part;
 };
 
 Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
@@ -1464,6 +1482,7 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
     l.runs = take(rows * d * sizeof(float));
     // dW of earlier pieces, when it does not fit the output's own type
     l.acc = take(dw_bf16 && T > l.piece ? static_cast<size_t>(V) * d * sizeof(float) : 0);
+    l.E32 = take(static_cast<size_t>(kFewTokens * l.ldv) * sizeof(float));
     l.E = take(static_cast<size_t>(l.piece * l.ldv) * 2);
   }
   l.part = at;  // dx's parts come last, see part_bytes()
@@ -1542,6 +1561,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
   float* part = reinterpret_cast<float*>(at(l.part));
   float* acc = reinterpret_cast<float*>(at(l.acc));
   uint16_t* E = reinterpret_cast<uint16_t*>(at(l.E));
+  float* E32 = reinterpret_cast<float*>(at(l.E32));
 
   for (int64_t t0 = 0; t0 < T; t0 += l.piece) {
     const int n = static_cast<int>(std::min<int64_t>(l.piece, T - t0));
@@ -1562,6 +1582,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
         return DMOE_ERR_CUDA;
       if (grad && !dmoe::make_map(&q.map_e, E, n, l.ldv, 64, 32)) return DMOE_ERR_CUDA;
       q.E = E;
+      q.E32 = dw && n <= kFewTokens ? E32 : nullptr;
       q.sums = sums;
       q.refs = refs;
       q.ldp = l.ldp;
@@ -1583,7 +1604,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     r.coef = coef;
     const bool few = n <= kFewTokens;
     r.x = xp, r.xs = dw && !few ? xs : nullptr;
-    r.E = E, r.ldv = l.ldv;
+    r.E = E, r.E32 = dw && few ? E32 : nullptr, r.ldv = l.ldv;
     r.skey = skey, r.order = order;
     r.err = di.err_word;
     r.sorting = dw && !few ? ceil_div(n, kSortTokens) : 0;
@@ -1627,7 +1648,7 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       while (per_row < kFewThreads && per_row * 8 < d) per_row *= 2;
       const dim3 grid(ceil_div(V, kFewRows), ceil_div(d, per_row * 8));
       auto kern = n <= 2 ? few_dw_kernel<2> : n <= 4 ? few_dw_kernel<4> : few_dw_kernel<kFewTokens>;
-      DMOE_TRY_LAUNCH(dmoe::launch_pdl(kern, grid, dim3(kFewThreads), 0, st, static_cast<const uint16_t*>(E), l.ldv,
+      DMOE_TRY_LAUNCH(dmoe::launch_pdl(kern, grid, dim3(kFewThreads), 0, st, static_cast<const float*>(E32), l.ldv,
                                        static_cast<const float2*>(coef), tp, xp, n, d, V, per_row, p.dw, p.dw32,
                                        p.dw_add));
     }
