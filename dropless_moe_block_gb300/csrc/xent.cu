@@ -43,11 +43,15 @@
 //
 // The products are bound by the tensor cores (2 T V d flops each).  They run
 // as persistent CTA pairs (tcgen05 cta_group::2): M = 256 x N = 512 tiles (two
-// sub-tiles of N = 256 that share each K slice's A), a ring of TMA-filled K
-// slices of 64, accumulators in TMEM.  Roles per CTA: warp 0 TMA producer,
-// warp 1 TMEM allocator and (rank 0) MMA issuer, warps 2-9 epilogue.  Every
-// ragged edge is the tensor maps': what lies past a matrix reads as zero,
-// and the epilogue stores nothing there.
+// sub-tiles of N = 256 that share each K slice's A; the logits also N = 256,
+// 128 or 64, see logits_tile()), a ring of TMA-filled K slices of 64,
+// accumulators in TMEM.  Roles per CTA: warp 0 TMA producer, warp 1 TMEM
+// allocator and (rank 0) MMA issuer, warps 2-17 epilogue: sixteen warps,
+// because exponentials, sums and stores of a tile take as long as its product
+// over 512 columns, and eight left that time to latency (8192 x 512 x 32000:
+// logits 231 us with eight, 195 with sixteen).  Every ragged edge is the
+// tensor maps': what lies past a matrix reads as zero, and the epilogue stores
+// nothing there.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -94,12 +98,13 @@ constexpr int kPieceMax = 1 << 18;
 // count: with its gradients 3828 / 3814 us.
 constexpr int kNarrowD = 1024;
 
+constexpr uint64_t kDrainNs = 1000 * 1000;
 constexpr int kFewTokens = 8;        // dW of so few tokens has a form of its own
 constexpr int kUnits = 76;           // CTA pairs of a GB300, for the rule that splits dx
 constexpr int kRun = 32;             // positions per partial sum of launch 3
 // Words with at most so many tokens are summed by dW's epilogue itself, token
 // by token.  From kDirectFrom tokens on that hides behind the tile's product,
-// and keeps launch 3 from writing a row for every token (34 MB at 8192 x 512).
+// and keeps launch 3 from writing a row for every token (17 MB at 8192 x 512).
 // With fewer tokens the product is short, and the epilogue adds launch 3's
 // rows only (1216 x 736 x 41031: gradients 169 us with 4, 162 with 0).
 constexpr int kDirect = 4;
@@ -294,11 +299,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t a_hi, 
       "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
       "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(add)
       : "memory");
-}
-
-__device__ __forceinline__ void mma_pair_add(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
-                                             uint32_t idesc) {
-  mma_pair(d, a, a_hi, b, b_hi, idesc, 1u);
 }
 
 __device__ __forceinline__ void st_shared(uint32_t a, const uint4& q) {
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
         const uint32_t b = b_lo + st * (PL::STAGE >> 4) + s * (B_BYTES >> 4);
         mma_pair(d, a, a_hi, b, b_hi, idesc, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 1; kk < BK / UMMA_K; ++kk) mma_pair_add(d, a + a_step * kk, a_hi, b + B_STEP * kk, b_hi, idesc);
+        for (int kk = 1; kk < BK / UMMA_K; ++kk) mma_pair(d, a + a_step * kk, a_hi, b + B_STEP * kk, b_hi, idesc, 1u);
       };
       Item it;
       for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
@@ -910,6 +910,10 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
   }
 
   __syncwarp();
+  if (*abort_flag) {  // a wait gave up: let copies and products under way land before their memory goes
+    const uint64_t t0 = dmoe::globaltimer_ns();
+    while (dmoe::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+  }
   fence_before_sync();
   // a CTA of a pair leaves only once the other no longer reads or signals
   // its shared memory
@@ -1332,12 +1336,12 @@ Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN
 
 // Columns of a logits tile.  Few tokens and words make few tiles; then narrower
 // ones spread the reading of W over more SMs: the width whose busiest pair is
-// shortest, in 256-wide slices (0.28 us; a narrower one's loads of x and its
-// latency stay).  2 tokens, 4492 words, d = 3296: 18 tiles of 256 34 us, 71 of
+// shortest, in hundredths of a 256-wide slice (0.28 us; a 512-wide one saves
+// operands, of a narrower one the loads of x and the latency stay).  2 tokens, 4492 words, d = 3296: 18 tiles of 256 34 us, 71 of
 // 64 19 us.
 int logits_tile(int n, int d, int V) {
   const int64_t mt = ceil_div(n, 2 * BM);
-  auto cost = [&](int tile, int per_slice) {  // in hundredths
+  auto cost = [&](int tile, int per_slice) {
     return static_cast<int64_t>(ceil_div(mt * ceil_div(V, tile), kUnits)) * per_slice;
   };
   int best = d <= kNarrowD ? BN : 2 * BN;

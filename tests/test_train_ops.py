@@ -408,6 +408,23 @@ def test_loss_of_large_logits(dm, shift):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shift", [150.0, -150.0])
+def test_loss_of_large_logits_of_few_tokens(dm, shift):
+    """The same where dw has its few-token form."""
+    T, V, d = 6, 700, 16
+    x, w = torch.zeros(T, d), torch.zeros(V, d)
+    x[:, 0] = torch.tensor([1.0, -1.0, 0.0, 1.0, 0.5, 1.0])
+    x[:, 1] = 1.0
+    w[:, 0] = shift + torch.randint(-8, 8, (V,), generator=gen(74)).float()
+    w[300, 0] += 90.0
+    w[640:, 0] -= 100.0
+    w[:, 1] = torch.randint(-2, 3, (V,), generator=gen(75)).float()
+    x, w = x.to(torch.bfloat16), w.to(torch.bfloat16)
+    t = torch.tensor([300, 690, 5, -100, 44, 45], dtype=torch.int32)
+    check_loss(run_loss(dm, cuda(x), cuda(w), cuda(t)), x, w, t)
+
+
+@pytest.mark.gpu
 def test_loss_without_targets_that_count(dm):
     T, V, d = 70, 200, 24
     x, w = randn(44, T, d), randn(45, V, d)
