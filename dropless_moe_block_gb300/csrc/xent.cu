@@ -1313,6 +1313,19 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------- host side
 
+// As dmoe::make_map (128-byte swizzle), of a [rows, cols] corner of a matrix
+// whose rows lie ld elements apart: what lies past cols reads as zero.
+bool map_pitched(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_cols,
+                 uint32_t box_rows) {
+  auto fn = dmoe::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, pitch[1] = {ld * 2};
+  const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, pitch, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -1625,12 +1638,12 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
     Grid gx{}, gw{};
     // E as [n, V] with row pitch ldv: the columns past V read as zero
     if (dx) {
-      if (!dmoe::make_map_ld(&p.map_a, E, n, V, l.ldv, BK, p.a_rows) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
+      if (!map_pitched(&p.map_a, E, n, V, l.ldv, BK, p.a_rows) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
         return DMOE_ERR_CUDA;
       gx = make_grid(n, d, V, 16, parts);
     }
     if (dw && !few) {
-      if (!dmoe::make_map_ld(&p.map_a2, E, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b2, xs, n, d, 64, BK))
+      if (!map_pitched(&p.map_a2, E, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b2, xs, n, d, 64, BK))
         return DMOE_ERR_CUDA;
       gw = make_grid(V, d, n, 1);
     }
