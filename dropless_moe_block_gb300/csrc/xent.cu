@@ -147,7 +147,8 @@ struct FastDiv {
 // of `raster` pair rows.
 struct Grid {
   int cols;       // N
-  int width;      // columns of a sub-tile: BN, for the logits also 128 or 64
+  int tile;       // columns of a tile: 512 (two sub-tiles), 256, for the logits also 128 or 64
+  int64_t time;   // of its longest item, for the host: see item_time()
   int mt, nt;     // pair-tile rows, tile columns
   int raster;     // pair-tile rows per raster group
   int slices;     // K slices of 64
@@ -413,7 +414,7 @@ __device__ __forceinline__ void write_rows32(uint32_t slab, int lane, const floa
 // One unit of work: a tile of one product over a range of K slices.
 struct Item {
   int dx;      // gradients: dx's or dW's
-  int m, n;    // pair-tile row, tile column
+  int m, c0;   // pair-tile row, first column
   int k0, k1;  // K slices
   int part;
   bool wide;   // the second sub-tile has columns (else it is left out)
@@ -435,9 +436,10 @@ __device__ __forceinline__ void tile_at(const Grid& g, uint32_t t, Item& it) {
   const uint32_t l = t - q * g.group.d;
   const uint32_t r0 = q * g.raster;
   const bool last = r0 + g.raster > static_cast<uint32_t>(g.mt);
-  it.n = last ? g.rest(l) : g.high(l);
-  it.m = r0 + l - it.n * (last ? g.rest.d : g.high.d);
-  it.wide = (2 * it.n + 1) * BN < g.cols;
+  const uint32_t n = last ? g.rest(l) : g.high(l);
+  it.m = r0 + l - n * (last ? g.rest.d : g.high.d);
+  it.c0 = n * g.tile;
+  it.wide = g.tile > BN && it.c0 + BN < g.cols;
 }
 
 // The j-th item of unit u of U (false: none left).  The items of grid[0],
@@ -538,8 +540,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       Item it;
       for (int j = 0; ok && item_of(p, unit, U, j, it); ++j) {
         const int m0 = it.m * 2 * BM + rank * BM;
-        const int width = GRAD || NS == 2 ? BN : p.grid[0].width;
-        const int n0 = it.n * NS * width + rank * (width / 2);
+        const int width = GRAD || NS == 2 ? BN : p.grid[0].tile;  // of a sub-tile
+        const int n0 = it.c0 + rank * (width / 2);
         const bool a_mn = GRAD && !it.dx;
         // the bytes of both CTAs' A rows, and whether this one has any
         const bool a_none = !a_mn && m0 >= p.n;
@@ -625,8 +627,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
       const uint32_t b_lo = static_cast<uint32_t>(bdesc0);
       uint32_t a_step = K_STEP, idesc = idesc_bf16(2 * BM, BN, false, GRAD);
       if (!GRAD && NS == 1)
-        idesc = p.grid[0].width == BN ? idesc_bf16(2 * BM, BN, false, false)
-                                      : p.grid[0].width == 128 ? idesc_bf16(2 * BM, 128, false, false)
+        idesc = p.grid[0].tile == BN ? idesc_bf16(2 * BM, BN, false, false)
+                                     : p.grid[0].tile == 128 ? idesc_bf16(2 * BM, 128, false, false)
                                                                : idesc_bf16(2 * BM, 64, false, false);
       // one K slice of sub-tile `s` from ring stage st into accumulator d
       auto mmas = [&](uint32_t d, int st, int s, bool first) {
@@ -774,19 +776,19 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
             // two binary searches and no prefetch, 149 so; 126 without the
             // additions, which registers are too few to fetch earlier)
             if (tokens > p.direct) {
-              const float* a = p.runs + static_cast<int64_t>(first) * p.d + it.n * NS * BN + part * 64;
-              const int cols = p.d - (it.n * NS * BN + part * 64);
+              const float* a = p.runs + static_cast<int64_t>(first) * p.d + it.c0 + part * 64;
+              const int cols = p.d - (it.c0 + part * 64);
 #pragma unroll
               for (int i = 0; i < 2 * NS; ++i)
-                if ((i >> 1) * BN + (i & 1) * 32 < cols) prefetch_l1(a + (i >> 1) * BN + (i & 1) * 32);
+                if ((i < 2 || it.wide) && (i >> 1) * BN + (i & 1) * 32 < cols) prefetch_l1(a + (i >> 1) * BN + (i & 1) * 32);
             }
           }
         }
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int width = GRAD || NS == 2 ? BN : p.grid[0].width;
-        const int c = (it.n * NS + s) * width + part * 64;  // this warp's first column
+        const int width = GRAD || NS == 2 ? BN : p.grid[0].tile;
+        const int c = it.c0 + s * BN + part * 64;  // this warp's first column
         if (NS == 1 || s == 0) {
           ok = mbar_wait_cluster(tfull + acc, acc_phase, abort_flag);
           if (!ok) break;
@@ -1329,10 +1331,22 @@ bool map_pitched(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// Time of a gradient item in hundredths of a 512-wide K slice (0.57 us), as
+// measured: the product, of whose operands a 256-wide tile loads a third more
+// a column (8192 x 512 x 32000 all in 256-wide tiles: 0.69 a slice), and the
+// part of the epilogue that the next product does not hide (dW alone, 64 and
+// 19 slices: 10 to 12 slices an item).  alone: no other tile reads the same B,
+// whose 64 KB (or 32) a slice then come from HBM, 0.73 us for 76 pairs
+// together.
+int64_t item_time(int slices, int tile, int cols, bool alone = false) {
+  if (tile > BN && cols > BN) return (alone ? 128 : 100) * static_cast<int64_t>(slices) + 1000;
+  return (alone ? 95 : 69) * static_cast<int64_t>(slices) + 560;
+}
+
 Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN) {
   Grid g{};
   g.cols = N;
-  g.width = std::min(tile, BN);
+  g.tile = tile;
   g.mt = ceil_div(M, 2 * BM);
   g.nt = ceil_div(N, tile);
   g.raster = raster;
@@ -1340,6 +1354,7 @@ Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN
   g.per_part = ceil_div(g.slices, parts);
   g.parts = ceil_div(g.slices, g.per_part);  // none of them empty
   g.items = g.mt * g.nt * g.parts;
+  g.time = item_time(g.per_part, tile, N, g.mt == 1);
   g.tiles.set(static_cast<uint32_t>(g.mt) * g.nt);
   g.group.set(static_cast<uint32_t>(raster) * g.nt);
   g.high.set(raster);
@@ -1367,15 +1382,9 @@ int logits_tile(int n, int d, int V) {
   return best;
 }
 
-// Time of a gradient item in K slices: its product, or, where K is short, its
-// epilogue (256 x 512 outputs take as long as about 9 slices).
-constexpr int kEpilogueSlices = 9;
-int item_time(int slices, int cols) { return std::max(slices, cols > BN ? kEpilogueSlices : kEpilogueSlices / 2 + 1); }
-int item_slices(const Grid& g) { return item_time(g.per_part, g.cols); }
-
 // Deals the items of two grids (the second may have none) to U units: the
 // longer ones into grid[0], and how many of the shorter ones the units with
-// one long item fewer take first (item_of()).  busiest: the slices of the unit
+// one long item fewer take first (item_of()).  busiest: the time of the unit
 // that has most.
 struct Dealt {
   int full, rem, early, extra;
@@ -1396,33 +1405,46 @@ Dealt dealt(int n0, int64_t l0, int n1, int64_t l1, int U) {  // the longer item
 }
 
 void deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
-  p.first_dx = gx.items > 0 && (gw.items == 0 || item_slices(gx) >= item_slices(gw));
+  p.first_dx = gx.items > 0 && (gw.items == 0 || gx.time >= gw.time);
   p.grid[0] = p.first_dx ? gx : gw;
   p.grid[1] = p.first_dx ? gw : gx;
-  const Dealt r = dealt(p.grid[0].items, item_slices(p.grid[0]), p.grid[1].items,
-                        p.grid[1].items > 0 ? item_slices(p.grid[1]) : 1, U);
+  const Dealt r = dealt(p.grid[0].items, p.grid[0].time, p.grid[1].items, std::max<int64_t>(1, p.grid[1].time), U);
   p.full = r.full, p.rem = r.rem, p.early = r.early, p.extra = r.extra;
 }
 
-// Parts of dx's sum over the vocabulary.  dx has few tiles of V / 64 slices
-// each; in one part the last of them can outlast everything else (512
-// tokens: 8 tiles for 76 pairs).  Takes the count whose busiest unit is
-// shortest, charging the fp32 sums that parts write and read back in slices
-// (about 0.5 us each): 12 bytes an element at 6.5 TB/s, and a launch.
-int dx_parts(int n, int d, int V, bool dw) {
-  const int tiles = ceil_div(n, 2 * BM) * ceil_div(d, 2 * BN), slices = ceil_div(V, BK);
-  const int nw = dw ? ceil_div(V, 2 * BM) * ceil_div(d, 2 * BN) : 0;
-  const int64_t lw = item_time(ceil_div(n, BK), d);
-  int best = 1;
-  int64_t best_cost = -1;
-  for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-    if (s > 1 && slices / s < 8) break;
-    const int64_t lx = item_time(ceil_div(slices, s), d);
-    int64_t cost = (nw == 0 || lx >= lw ? dealt(tiles * s, lx, nw, lw, kUnits) : dealt(nw, lw, tiles * s, lx, kUnits)).busiest;
-    if (s > 1) cost += 10 + static_cast<int64_t>(s) * n * d / 270000;
-    if (best_cost < 0 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
+// How the gradients' tiles are cut: the widths of dx's and dW's tiles and the
+// parts of dx's sum over the vocabulary.  512-wide tiles are the faster ones
+// by operands, but few: dx has few tiles of V / 64 slices each, and the last
+// of them can outlast everything else (512 tokens: 8 tiles for 76 pairs).
+// Takes the cut whose busiest unit is shortest, charging the fp32 sums that
+// parts write and read back: 12 bytes an element at 6.5 TB/s, and a launch.
+// 8192 x 512 x 32000: 315 us with 512-wide tiles in one part, 362 with 256-wide
+// ones; 1216 x 736 x 41031: 158 us with 512-wide tiles in six parts, 140 with
+// 256-wide ones of dx in two; 13 x 3984 x 48294: 181 us with dx in three
+// parts, 159 in eight.
+struct Cut {
+  int parts, tile_x, tile_w;
+};
+Cut cut_grads(int n, int d, int V, bool dx, bool dw) {
+  const int mx = ceil_div(n, 2 * BM), mw = ceil_div(V, 2 * BM), slices = ceil_div(V, BK);
+  Cut best{1, 2 * BN, 2 * BN};
+  int64_t least = -1;
+  for (const int tx : {2 * BN, BN}) {
+    for (const int tw : {2 * BN, BN}) {
+      if ((tx == BN && (!dx || d <= BN)) || (tw == BN && (!dw || d <= BN))) continue;
+      const int nw = dw ? mw * ceil_div(d, tw) : 0;
+      const int64_t lw = item_time(ceil_div(n, BK), tw, d, mw == 1);
+      for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        const int nx = dx ? mx * ceil_div(d, tx) * s : 0;
+        if (s > 1 && (!dx || slices / s < 8 || nx > 16 * kUnits)) break;
+        const int64_t lx = item_time(ceil_div(slices, s), tx, d, mx == 1);
+        int64_t time = (nw == 0 || (nx > 0 && lx >= lw) ? dealt(nx, lx, nw, lw, kUnits) : dealt(nw, lw, nx, lx, kUnits)).busiest;
+        if (s > 1) time += 1000 + static_cast<int64_t>(s) * n * d / 2700;
+        if (least < 0 || time < least) {
+          best = Cut{s, tx, tw};
+          least = time;
+        }
+      }
     }
   }
   return best;
@@ -1510,7 +1532,7 @@ Layout layout_of(int T, int d, int V, bool grad, bool dw_bf16, int piece) {
 size_t part_bytes(const Layout& l, int T, int d, int V, bool dw) {
   size_t most = 0;
   for (const int64_t n : {std::min<int64_t>(l.piece, T), T % l.piece}) {
-    const int s = n > 0 ? dx_parts(static_cast<int>(n), d, V, dw && n > kFewTokens) : 1;
+    const int s = n > 0 ? cut_grads(static_cast<int>(n), d, V, true, dw && n > kFewTokens).parts : 1;
     if (s > 1) most = std::max(most, static_cast<size_t>(n) * s * d * sizeof(float));
   }
   return most;
@@ -1634,18 +1656,18 @@ DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t
       DMOE_TRY_LAUNCH(dmoe::launch_pdl(target_runs_kernel, dim3(ceil_div(n, 4 * kRun), ceil_div(d, kRunCols)),
                                        dim3(128), 0, st, xp, n, d, V, p.direct, static_cast<const int32_t*>(skey),
                                        static_cast<const int32_t*>(order), static_cast<const float2*>(coef), runs, words));
-    const int parts = dx ? dx_parts(n, d, V, dw && !few) : 1;
+    const Cut cut = cut_grads(n, d, V, dx != nullptr, dw && !few);
     Grid gx{}, gw{};
     // E as [n, V] with row pitch ldv: the columns past V read as zero
     if (dx) {
       if (!map_pitched(&p.map_a, E, n, V, l.ldv, BK, p.a_rows) || !dmoe::make_map(&p.map_b, w, V, d, 64, BK))
         return DMOE_ERR_CUDA;
-      gx = make_grid(n, d, V, 16, parts);
+      gx = make_grid(n, d, V, 16, cut.parts, cut.tile_x);
     }
     if (dw && !few) {
       if (!map_pitched(&p.map_a2, E, n, V, l.ldv, 64, BK) || !dmoe::make_map(&p.map_b2, xs, n, d, 64, BK))
         return DMOE_ERR_CUDA;
-      gw = make_grid(V, d, n, 1);
+      gw = make_grid(V, d, n, 1, 1, cut.tile_w);
     }
     p.coef = coef, p.W = w, p.x = xp;
     p.dx = dx ? dx + t0 * d : nullptr;
