@@ -772,8 +772,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           if (static_cast<unsigned>(at.x) < static_cast<unsigned>(p.n) && __ldg(p.skey + at.x) == row) {
             first = at.x;
             tokens = at.y - at.x;
-            // the sums it will add (1216 x 736 x 41031: gradients 152 us with
-            // two binary searches and no prefetch, 149 so; 126 without the
+            // the sums it will add (1216 x 736 x 41031 in 512-wide tiles: 152 us
+            // with two binary searches and no prefetch, 149 so; 126 without the
             // additions, which registers are too few to fetch earlier)
             if (tokens > p.direct) {
               const float* a = p.runs + static_cast<int64_t>(first) * p.d + it.c0 + part * 64;
@@ -1418,10 +1418,10 @@ void deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
 // of them can outlast everything else (512 tokens: 8 tiles for 76 pairs).
 // Takes the cut whose busiest unit is shortest, charging the fp32 sums that
 // parts write and read back: 12 bytes an element at 6.5 TB/s, and a launch.
-// 8192 x 512 x 32000: 315 us with 512-wide tiles in one part, 362 with 256-wide
-// ones; 1216 x 736 x 41031: 158 us with 512-wide tiles in six parts, 140 with
-// 256-wide ones of dx in two; 13 x 3984 x 48294: 181 us with dx in three
-// parts, 159 in eight.
+// Gradients with the join of the parts, 512-wide tiles throughout and as cut
+// here: 2000 x 2048 x 32000 341 and 301 us, 1216 x 736 x 41031 167 and 144,
+// 13 x 3984 x 48294 170 and 164; 8192 x 512 x 32000 317 us in the 512-wide
+// tiles that it gets, 362 in 256-wide ones.
 struct Cut {
   int parts, tile_x, tile_w;
 };
