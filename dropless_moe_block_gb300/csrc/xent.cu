@@ -1364,17 +1364,19 @@ Grid make_grid(int M, int N, int K, int raster, int parts = 1, int tile = 2 * BN
 
 // Columns of a logits tile.  Few tokens and words make few tiles; then narrower
 // ones spread the reading of W over more SMs: the width whose busiest pair is
-// shortest, in hundredths of a 256-wide slice (0.28 us; a 512-wide one saves
-// operands, of a narrower one the loads of x and the latency stay).  2 tokens, 4492 words, d = 3296: 18 tiles of 256 34 us, 71 of
-// 64 19 us.
+// shortest, in hundredths of a 256-wide slice.  A 512-wide one saves operands,
+// of a narrower one the loads of x and the latency stay.  The loss, 512-, 256-,
+// 128- and 64-wide: 1 x 4096 x 5000 words 47, 33, 31 and 47 us; 167 x 2640 x
+// 24257 47, 51, 57 and 74; 313 x 3160 x 14191 48, 55, 62 and 96; 1024 x 3160 x
+// 50645 217, 240, 328 and 582; 1024 x 4096 x 32000 168, 158, 256 and 473.
 int logits_tile(int n, int d, int V) {
   const int64_t mt = ceil_div(n, 2 * BM);
   auto cost = [&](int tile, int per_slice) {
     return static_cast<int64_t>(ceil_div(mt * ceil_div(V, tile), kUnits)) * per_slice;
   };
   int best = d <= kNarrowD ? BN : 2 * BN;
-  int64_t least = best == BN ? cost(BN, 100) : cost(2 * BN, 190);
-  for (const auto& w : {std::pair<int, int>{BN, 100}, {128, 60}, {64, 45}})
+  int64_t least = best == BN ? cost(BN, 100) : cost(2 * BN, 180);
+  for (const auto& w : {std::pair<int, int>{BN, 100}, {128, 75}, {64, 60}})
     if (cost(w.first, w.second) < least) {
       best = w.first;
       least = cost(w.first, w.second);
