@@ -1243,7 +1243,12 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float f[8] = {};
-    if (t < n && c < d) unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
+    if (t < n && c < d) {
+      // a token of no weight may hold anything, and 0 times what is not finite is not 0
+      const float2 cf = __ldg(coef + t);
+      if (cf.x != 0.f || cf.y != 0.f)
+        unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[t][j] = make_float2(f[2 * j], f[2 * j + 1]);
   }
