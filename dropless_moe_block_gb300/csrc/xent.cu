@@ -893,7 +893,8 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
               } else {
                 for (int q = 0; q < tokens; ++q) {
                   const int t = __ldg(p.order + first + q);
-                  add_row32(v, p.x + static_cast<int64_t>(t) * p.d + ch, __ldg(&p.coef[t].y), cols);
+                  const float k = __ldg(&p.coef[t].y);
+                  if (k != 0.f) add_row32(v, p.x + static_cast<int64_t>(t) * p.d + ch, k, cols);
                 }
               }
               if (p.dw_add && row < M) add_row32(v, p.dw_add + static_cast<int64_t>(row) * p.d + ch, cols);
@@ -984,8 +985,10 @@ __global__ void __launch_bounds__(128)
       if (!((need >> (b + j)) & 1u)) continue;
       float f[8];
       unpack8x(u[j], f);
+      if (w != 0.f) {  // a token of no weight may hold what is not finite
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      }
       if (b + j + 1 == end) {  // the word's last position here
         if (c < d) {
           float4* o = reinterpret_cast<float4*>(runs + static_cast<int64_t>(base + from) * d + c);

@@ -70,3 +70,25 @@ def test_rows_that_do_not_count_may_hold_anything(dm, T, piece, dtype):
     assert float(out["dx"][rows].float().abs().max()) == 0.0
     if T == 1:
         assert float(out["dw"].float().abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [6, 70, 4100])
+def test_rows_of_no_weight_may_hold_anything(dm, T):
+    """d_loss 0 at a target that is a word.  From 4096 tokens on the words'
+    tokens are added one by one, 70 go by sums of runs."""
+    V, d = 300, 64
+    rows = [1, 3, T - 1]
+    x, w = randn(104, T, d), randn(105, V, d, scale=0.3)
+    t = torch.randint(0, V, (T,), generator=gen(106), dtype=torch.int32)
+    t[3] = t[1]
+    g = randn(107, T, dtype=torch.float32)
+    g[rows] = 0.0
+    if T == 4100:  # a word of one token, which is such a row
+        t[t == 17] = 18
+        t[3] = 17
+    out = run_loss(dm, cuda(hold_anything(x, rows)), cuda(w), cuda(t), dw=torch.float32, d_loss=cuda(g))
+    x[rows] = 0
+    out = replaced(out, "lse", rows, math.log(V))
+    check_loss(replaced(out, "loss", rows, math.log(V)), x, w, t, d_loss=g)
+    assert float(out["dx"][rows].float().abs().max()) == 0.0
