@@ -225,6 +225,14 @@ __device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
   return d;
 }
 
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
 __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -827,13 +835,20 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
           top = max3(top, max3(top2, v[62], v[63]), -INFINITY);
           const bool shift = top > kRefHigh || (top < kRefLow && top != -INFINITY);
           const float ref = shift ? top * p.unbias : 0.f;
+          // The reference leaves before the scaling to powers of two: ref log2 e of a
+          // logit near the type's limits (a mask by its lowest value) is infinite,
+          // and of one of some hundreds loses digits of the difference.
+          if (__any_sync(0xffffffffu, shift)) {
+            const float less = shift ? top : 0.f;
+#pragma unroll
+            for (int q = 0; q < 64; ++q) v[q] -= less;
+          }
           const float2 k2 = make_float2(kLog2e * p.unbias, kLog2e * p.unbias);
-          const float2 bias2 = make_float2(-ref * kLog2e, -ref * kLog2e);
           float2 sum2 = make_float2(0.f, 0.f), sum3 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < 64; q += 4) {
-            float2 a = f2_fma(make_float2(v[q], v[q + 1]), k2, bias2);
-            float2 b = f2_fma(make_float2(v[q + 2], v[q + 3]), k2, bias2);
+            float2 a = f2_mul(make_float2(v[q], v[q + 1]), k2);
+            float2 b = f2_mul(make_float2(v[q + 2], v[q + 3]), k2);
             a = make_float2(ex2(a.x), ex2(a.y));
             b = make_float2(ex2(b.x), ex2(b.y));
             sum2 = f2_add(sum2, a);

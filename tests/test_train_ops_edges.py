@@ -92,3 +92,46 @@ def test_rows_of_no_weight_may_hold_anything(dm, T):
     out = replaced(out, "lse", rows, math.log(V))
     check_loss(replaced(out, "loss", rows, math.log(V)), x, w, t, d_loss=g)
     assert float(out["dx"][rows].float().abs().max()) == 0.0
+
+
+# ---------------------------------------------------------- masked words
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,d", [(5, 700, 16), (40, 700, 16), (300, 38900, 1032)])
+@pytest.mark.parametrize("level", [0.0, -100.0, 100.0])
+def test_words_masked_by_the_lowest_value(dm, T, V, d, level):
+    """A column of x that is 1 and of w that is the type's lowest value takes words out of the softmax: single ones,
+    and whole groups of 64.  The last size has 512-wide tiles."""
+    lowest = torch.finfo(torch.bfloat16).min
+    x, w = randn(111, T, d), randn(112, V, d, scale=0.5 / math.sqrt(d))
+    x[:, 0], w[:, 0] = 1.0, 0.0
+    x[:, 1], w[:, 1] = 1.0, level
+    masked = torch.zeros(V, dtype=torch.bool)
+    masked[64:192] = masked[3] = masked[V - 5:] = masked[400:470] = True
+    keep = ~masked
+    words = keep.nonzero().view(-1)
+    t = words[torch.randint(0, len(words), (T,), generator=gen(113))]
+    w[masked, 0] = lowest
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t.int()))
+    assert dm.get_error() == 0
+    assert float(out["dw"][cuda(masked)].float().abs().max()) == 0.0
+    w, t = w[keep], (keep.cumsum(0) - 1)[t].int()
+    check_loss({**out, "dx": None, "dw": None}, x, w, t)
+    _, dx, dw, tx, tw = bounds(x, w, t, again=1)
+    close(out["dx"], dx, tx, "dx")
+    close(out["dw"][cuda(keep)], dw, tw + U16 * dw.abs(), "dw")
+
+
+@pytest.mark.gpu
+def test_a_word_masked_in_by_the_highest_value(dm):
+    """A logit of 3e38: certain, and the others' loss as large as it."""
+    T, V, d = 9, 200, 16
+    x, w = torch.zeros(T, d, dtype=torch.bfloat16), torch.zeros(V, d, dtype=torch.bfloat16)
+    x[:, 0], w[130, 0] = 1.0, torch.finfo(torch.bfloat16).max
+    t = torch.full((T,), 130, dtype=torch.int32)
+    t[4] = 7
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t), dx=False, dw=None)
+    top = float(w[130, 0])
+    lse, loss = out["lse"].cpu().double(), out["loss"].cpu().double()
+    assert float((lse - top).abs().max()) <= 4 * U32 * top
+    assert abs(float(loss[4]) - top) <= 8 * U32 * top and float(loss[t == 130].abs().max()) == 0.0
