@@ -1244,6 +1244,11 @@ __global__ void __launch_bounds__(kFewThreads)
   __shared__ float a[kFewRows][NT];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
+  // The tokens of some weight: a row of none may hold anything, and 0 times what
+  // is not finite is not 0.
+  const int lane = threadIdx.x & 31;
+  const float2 own = lane < n ? __ldg(coef + lane) : make_float2(0.f, 0.f);
+  const uint32_t weighs = __ballot_sync(0xffffffffu, own.x != 0.f || own.y != 0.f);
   const int v0 = blockIdx.x * kFewRows;
   for (int i = threadIdx.x; i < kFewRows * NT; i += kFewThreads) {
     const int t = i / kFewRows, r = i % kFewRows, v = v0 + r;
@@ -1261,12 +1266,8 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float f[8] = {};
-    if (t < n && c < d) {
-      // a token of no weight may hold anything, and 0 times what is not finite is not 0
-      const float2 cf = __ldg(coef + t);
-      if (cf.x != 0.f || cf.y != 0.f)
-        unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
-    }
+    if ((weighs >> t & 1u) && c < d)
+      unpack8x(__ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * d + c)), f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[t][j] = make_float2(f[2 * j], f[2 * j + 1]);
   }
