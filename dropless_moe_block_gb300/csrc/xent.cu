@@ -1146,6 +1146,7 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
       for (int i = 0; i < 4; ++i) {
         const int g = g0 + i * SLICES;
         if (g >= p.groups) break;
+        if (s[i] == 0.f) continue;  // words that are all masked by minus infinity: no reference either
         const float r = signbit(s[i]) ? __ldg(p.refs + g * p.ldp + t) : 0.f;
         join(R, S, r, fabsf(s[i]));
         low = fminf(low, r);
@@ -1210,8 +1211,9 @@ __global__ void __launch_bounds__(kStatThreads, 2) row_stats_kernel(const Params
     const float top = sh_r[rw];
     uint16_t* e = p.E + static_cast<int64_t>(row) * p.ldv;
     for (int g = sub; g < p.groups; g += WARPS) {
-      const float r = signbit(__ldg(p.sums + g * p.ldp + row)) ? __ldg(p.refs + g * p.ldp + row) : 0.f;
-      if (fix == 1 && r == top) continue;
+      const float s = __ldg(p.sums + g * p.ldp + row);
+      const float r = signbit(s) ? __ldg(p.refs + g * p.ldp + row) : 0.f;
+      if (fix == 1 && (r == top || s == 0.f)) continue;  // nothing to bring there (0 stays 0)
       const float k = fix == 2 ? 0.f : expf(r - top);
       __nv_bfloat162* u = reinterpret_cast<__nv_bfloat162*>(e + g * kGroup) + lane;
       float2 f = __bfloat1622float2(*u);

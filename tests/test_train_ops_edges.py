@@ -135,3 +135,21 @@ def test_a_word_masked_in_by_the_highest_value(dm):
     lse, loss = out["lse"].cpu().double(), out["loss"].cpu().double()
     assert float((lse - top).abs().max()) <= 4 * U32 * top
     assert abs(float(loss[4]) - top) <= 8 * U32 * top and float(loss[t == 130].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("level", [0.0, -100.0, -150.0, 100.0])
+def test_words_masked_by_minus_infinity(dm, level):
+    """The loss alone (dx multiplies what is in w, the infinities too)."""
+    T, V, d = 40, 700, 16
+    x, w = randn(114, T, d), randn(115, V, d, scale=0.1)
+    x[:, 0], w[:, 0] = 1.0, 0.0
+    x[:, 1], w[:, 1] = 1.0, level
+    masked = torch.zeros(V, dtype=torch.bool)
+    masked[64:192] = masked[3] = masked[400:470] = True
+    keep = ~masked
+    words = keep.nonzero().view(-1)
+    t = words[torch.randint(0, len(words), (T,), generator=gen(116))]
+    w[masked, 0] = -math.inf
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t.int()), dx=False, dw=None)
+    check_loss(out, x, w[keep], (keep.cumsum(0) - 1)[t].int())
