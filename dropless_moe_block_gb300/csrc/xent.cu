@@ -1446,6 +1446,9 @@ void deal(ParamsX& p, const Grid& gx, const Grid& gw, int U) {
 // of them can outlast everything else (512 tokens: 8 tiles for 76 pairs).
 // Takes the cut whose busiest unit is shortest, charging the fp32 sums that
 // parts write and read back: 12 bytes an element at 6.5 TB/s, and a launch.
+// Times are compared as whole numbers, without a division: over the n of the
+// same number of K slices only the charge changes, by parts * d each token, so
+// that more tokens never mean more parts there (part_bytes_up_to() counts on it).
 // Gradients with the join of the parts, 512-wide tiles throughout and as cut
 // here: 2000 x 2048 x 32000 341 and 301 us, 1216 x 736 x 41031 167 and 144,
 // 13 x 3984 x 48294 170 and 164; 8192 x 512 x 32000 317 us in the 512-wide
@@ -1466,8 +1469,8 @@ Cut cut_grads(int n, int d, int V, bool dx, bool dw) {
         const int nx = dx ? mx * ceil_div(d, tx) * s : 0;
         if (s > 1 && (!dx || slices / s < 8 || nx > 16 * kUnits)) break;
         const int64_t lx = item_time(ceil_div(slices, s), tx, d, mx == 1);
-        int64_t time = (nw == 0 || (nx > 0 && lx >= lw) ? dealt(nx, lx, nw, lw, kUnits) : dealt(nw, lw, nx, lx, kUnits)).busiest;
-        if (s > 1) time += 1000 + static_cast<int64_t>(s) * n * d / 2700;
+        const int64_t busiest = (nw == 0 || (nx > 0 && lx >= lw) ? dealt(nx, lx, nw, lw, kUnits) : dealt(nw, lw, nx, lx, kUnits)).busiest;
+        const int64_t time = 2700 * (busiest + (s > 1 ? 1000 : 0)) + (s > 1 ? static_cast<int64_t>(s) * n * d : 0);
         if (least < 0 || time < least) {
           best = Cut{s, tx, tw};
           least = time;
@@ -1566,6 +1569,21 @@ size_t part_bytes(const Layout& l, int T, int d, int V, bool dw) {
   return most;
 }
 
+// The most of part_bytes() that T tokens or fewer need, with dw or without: the
+// parts get more as the tokens get fewer, and a workspace for the longest batch
+// has to do for a shorter one.  Counted from the first n of every K slice on, which
+// has the most parts of its slice's, up to 63 tokens too many.
+size_t part_bytes_up_to(const Layout& l, int T, int d, int V) {
+  const int64_t most_n = std::min<int64_t>(l.piece, T);
+  size_t most = 0;
+  for (int64_t n = 0; n < most_n; n += BK)
+    for (const bool dw : {false, true}) {
+      const int s = cut_grads(static_cast<int>(n) + 1, d, V, true, dw).parts;
+      if (s > 1) most = std::max(most, static_cast<size_t>(std::min(n + BK, most_n)) * s * d * sizeof(float));
+    }
+  return most;
+}
+
 bool sizes_ok(int T, int d, int V, int piece) {
   return T >= 0 && d >= 8 && (d & 7) == 0 && V >= 1 && V < (1 << 24) && d <= (1 << 20) && piece >= 0;
 }
@@ -1588,7 +1606,7 @@ bool sizes_ok(int T, int d, int V, int piece) {
 DMOE_API size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, int dw_f32, int piece) {
   if (!sizes_ok(T, d, V, piece)) return 0;
   const Layout l = layout_of(T, d, V, grad != 0, !dw_f32, piece);
-  return l.part + (grad ? std::max(part_bytes(l, T, d, V, false), part_bytes(l, T, d, V, true)) : 0);
+  return l.part + (grad ? part_bytes_up_to(l, T, d, V) : 0);
 }
 
 DMOE_API dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, const int32_t* targets, int T,

@@ -522,10 +522,13 @@ dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy, const u
 
 /* ------------------------------------ vocabulary head + softmax cross entropy */
 
-/* Bytes of scratch dmoe_linear_cross_entropy needs: with gradients (grad != 0)
- * about 2 * piece * V, and 4 * V * d more when T > piece and dw is bf16
- * (dw_f32 == 0).  piece: tokens per piece (0: 8192), rounded up to a multiple
- * of 256; at most 262144. */
+/* Bytes of scratch dmoe_linear_cross_entropy needs for T tokens or fewer: with
+ * gradients (grad != 0) about 2 * piece * V, 4 * V * d more when T > piece and
+ * dw is bf16 (dw_f32 == 0), and room for dx's sum over V in fp32 parts, which
+ * shorter calls cut finer (d = 4096, V = 32000: 193 MB of 953).  It
+ * never falls with T: one made for the longest call serves the shorter ones,
+ * and calls that ask for fewer outputs.  piece: tokens per piece (0: 8192),
+ * rounded up to a multiple of 256; at most 262144. */
 size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, int dw_f32, int piece);
 
 /* Logits l[t, v] = <x[t], w[v]> (bf16 products, fp32 sums on the tensor

@@ -153,3 +153,51 @@ def test_words_masked_by_minus_infinity(dm, level):
     w[masked, 0] = -math.inf
     out = run_loss(dm, cuda(x), cuda(w), cuda(t.int()), dx=False, dw=None)
     check_loss(out, x, w[keep], (keep.cumsum(0) - 1)[t].int())
+
+
+# ------------------------------------------- one workspace, other lengths
+
+SPACES = [(2048, 32000, 0), (4096, 32000, 0), (4096, 128000, 0), (512, 32000, 0), (64, 500, 0), (256, 1009, 0),
+          (1032, 41031, 1024), (8192, 2000, 0)]
+
+
+@pytest.mark.parametrize("d,V,piece", SPACES)
+@pytest.mark.parametrize("grad,f32", [(0, 0), (1, 0), (1, 1)])
+def test_workspace_never_shrinks_with_more_tokens(d, V, piece, grad, f32):
+    size = _dm().lib().dmoe_linear_cross_entropy_workspace_size
+    lengths = sorted(set(range(0, 700)) | set(range(700, 9001, 13)) | {8191, 8192, 8193, 8447, 8448, 16384, 20001})
+    sizes = [size(T, d, V, grad, f32, piece) for T in lengths]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("d,V,piece", SPACES)
+def test_a_longer_batchs_workspace_is_taken(d, V, piece):
+    """Every shorter call gets past the checks of its arguments; a call that asks for fewer outputs does, too."""
+    if torch.cuda.is_available():
+        pytest.skip("without a device: the calls that are taken must not run")
+    L = _dm().lib()
+    p = ctypes.c_void_p(0x1000)
+    longest = 8192 + 4096
+    for f32 in (0, 1):
+        n = L.dmoe_linear_cross_entropy_workspace_size(longest, d, V, 1, f32, piece)
+        for T in [*range(1, 400, 7), *range(400, longest + 1, 97), 238, 2561, 3555, 3584, 6912, 7440, 7921, longest]:
+            for dx, dw in ((p, p), (p, None), (None, p), (None, None)):
+                assert L.dmoe_linear_cross_entropy(p, p, p, T, d, V, -100, None, p, None, dx, dw, f32, 0, piece, p, n,
+                                                   None) in (2, 3), (T, dx, dw)
+
+
+@pytest.mark.gpu
+def test_loss_in_a_longer_batchs_workspace(dm):
+    """The same bits in a workspace made for 1024 tokens as in one of the call's own length."""
+    V, d = 9001, 1032
+    ws = torch.empty(dm.linear_cross_entropy_workspace_size(1024, d, V), dtype=torch.uint8, device="cuda")
+    w = cuda(randn(121, V, d, scale=0.05))
+    for T in (5, 13, 238, 300, 513, 1024):
+        x = cuda(randn(122, T, d))
+        t = cuda(torch.randint(0, V, (T,), generator=gen(123), dtype=torch.int32))
+        own = run_loss(dm, x, w, t)
+        out = {k: torch.empty_like(v) for k, v in own.items()}
+        ws.fill_(255)
+        dm.linear_cross_entropy(x, w, t, out["loss"], out["lse"], ws, dx=out["dx"], dw=out["dw"])
+        for k in out:
+            assert torch.equal(out[k], own[k]), (T, k)
