@@ -35,10 +35,27 @@ constexpr float kE4M3Max = 448.f;
 constexpr int kMaxStages = 4;      // backward: units of rows in flight per block
 constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 
-__device__ __forceinline__ float rcp_approx(float x) {
+// a / b from inv = 1 / b: the product, then one step by what it leaves of a, which
+// the fused multiply-add gives without a rounding (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  1 / b the
+// same way, from an approximation.  4093 rows of 3584 in 8 bits: 19.5
+// us; 18.7 with values times the approximation, which puts some of them one
+// step of e4m3 off; 22.9 with divisions.
+__device__ __forceinline__ float quotient(float a, float inv, float b) {
+  const float q = a * inv;
+  return fmaf(fmaf(-q, b, a), inv, q);
+}
+
+__device__ __forceinline__ float2 quotient(float2 a, float inv, float b) {
+  const float2 i = make_float2(inv, inv);
+  const float2 q = dmoe::f2_mul(a, i);
+  return dmoe::f2_fma(dmoe::f2_fma(q, make_float2(-b, -b), a), i, q);
+}
+
+__device__ __forceinline__ float reciprocal(float b, float back) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+  return fmaf(fmaf(-back, r, 1.f), r, r);
 }
 
 // Copies bytes (a multiple of 16) between 16-byte aligned addresses,
@@ -165,15 +182,19 @@ __global__ void __launch_bounds__(TPR > kFwdThreads ? TPR : kFwdThreads, 1536 / 
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the smallest normal number keeps 1 / scale finite
-      const float s = top > 0.f ? fmaxf(top * (1.f / kE4M3Max), 1.17549435e-38f) : 1.f;
+      // at least the smallest normal number: the scale of a group keeps its digits
+      const float s = top == INFINITY ? top
+                      : top > 0.f     ? fmaxf(quotient(top, 1.f / kE4M3Max, kE4M3Max), 1.17549435e-38f)
+                                      : 1.f;
       if (in) {
-        const float inv = rcp_approx(s);
+        const float back = s < INFINITY ? s : 0.f;  // what is finite over an infinite scale is 0
+        const float inv = reciprocal(s, back);
         uint2 b;
         uint16_t* p = reinterpret_cast<uint16_t*>(&b);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          p[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * inv, f[2 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+          p[j] = __nv_cvt_float2_to_fp8x2(quotient(make_float2(f[2 * j], f[2 * j + 1]), inv, back), __NV_SATFINITE,
+                                          __NV_E4M3);
         *(reinterpret_cast<uint2*>(q + t * d) + v) = b;
         if ((v & 15) == 0) q_scale[t * ((d + kQGroup - 1) / kQGroup) + (v >> 4)] = s;
       }

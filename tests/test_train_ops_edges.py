@@ -201,3 +201,45 @@ def test_loss_in_a_longer_batchs_workspace(dm):
         dm.linear_cross_entropy(x, w, t, out["loss"], out["lse"], ws, dx=out["dx"], dw=out["dw"])
         for k in out:
             assert torch.equal(out[k], own[k]), (T, k)
+
+
+# ------------------------------------------------------- rows in 8 bits
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(64, 512), (33, 1000), (9, 3584), (5, 8200)])
+def test_8_bit_rows_are_the_quotients_rounded_once(dm, T, d):
+    """Given the kernel's own rstd, y in fp32 is two products, the scale one quotient and a value one more: each of
+    them, rounded as IEEE says, gives the bits."""
+    x = randn(131, T, d, scale=3.0)
+    w = randn(132, d, scale=0.3, dtype=torch.float32) + 1
+    rstd = empty(T, dtype=torch.float32)
+    q, s = empty(T, d, dtype=torch.float8_e4m3fn), empty(T, -(-d // 128), dtype=torch.float32)
+    dm.add_rms_norm(cuda(x), None, cuda(w), 1e-5, None, None, rstd=rstd, q=q, q_scale=s)
+    y = x.float() * rstd.cpu()[:, None] * w
+    n = -(-d // 128)
+    pad = torch.zeros(T, n * 128)
+    pad[:, :d] = y
+    scale = pad.view(T, n, 128).abs().amax(2) / 448.0
+    assert torch.equal(s.cpu(), scale)
+    want = (y / scale.repeat_interleave(128, 1)[:, :d]).to(torch.float8_e4m3fn)
+    assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_8_bit_rows_of_a_group_with_an_infinity(dm):
+    """A value past fp32: its group's scale is infinite, the others of the group are 0, other groups as ever."""
+    T, d = 3, 384
+    x = randn(133, T, d).abs() + 0.5
+    w = torch.ones(d)
+    w[140] = 3e38
+    q, s = empty(T, d, dtype=torch.float8_e4m3fn), empty(T, 3, dtype=torch.float32)
+    x[1] = 0
+    x[2, 140] = 50.0
+    x[0, 140] = 50.0
+    dm.add_rms_norm(cuda(x), None, cuda(w), 1e-5, None, None, q=q, q_scale=s)
+    q, s = q.cpu().float(), s.cpu()
+    assert torch.equal(torch.isinf(s), torch.tensor([[False, True, False], [False] * 3, [False, True, False]]))
+    assert torch.equal(s[1], torch.ones(3)) and float(q[1].abs().max()) == 0.0
+    for t in (0, 2):
+        assert math.isnan(float(q[t, 140])) and float(q[t, 128:140].abs().max()) == 0.0
+        assert float(q[t, :128].max()) == 448.0 and float(q[t, 256:].max()) == 448.0
