@@ -243,8 +243,11 @@ __global__ void __launch_bounds__(kClipThreads, kBlocksPerSm)
   const float nrm = static_cast<float>(sqrt(block_sum(v, sh)));
   if (threadIdx.x == 0) {
     *norm = nrm;
-    const float c = max_norm / (nrm + eps);
-    ws->factor = c > 1.f ? 1.f : c;  // a norm that is not a number stays one, and reaches every gradient
+    // 0 / 0 is the factor of zeros, which need none; without a limit no norm
+    // asks for one.  A norm that is not a number stays one, and reaches every
+    // gradient.
+    const float c = nrm + eps == 0.f || (max_norm == INFINITY && nrm == nrm) ? 1.f : max_norm / (nrm + eps);
+    ws->factor = c > 1.f ? 1.f : c;
   }
 }
 

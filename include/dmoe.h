@@ -583,7 +583,8 @@ size_t dmoe_clip_grad_norm_workspace_size(void);
  * c = min(1, max_norm / (norm + eps)); out = c * in for every tensor (a
  * tensor with out == in is left alone when c is 1).  A norm that is not
  * finite is not replaced: an infinite one gives c = 0, NaN reaches every
- * output.  grads [n] is a DEVICE array, chunks the total of its tensors'
+ * output.  c is 1 for an infinite max_norm (no limit) unless the norm is NaN,
+ * and where norm + eps is 0.  grads [n] is a DEVICE array, chunks the total of its tensors'
  * chunks; elements must be aligned to their size; norm [1] fp32 (device,
  * written).  The sums run in a fixed order (squares in fp32, their sums of
  * chunks and blocks in fp64).  Calls sharing a ws must not overlap. */

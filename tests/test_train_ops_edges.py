@@ -243,3 +243,23 @@ def test_8_bit_rows_of_a_group_with_an_infinity(dm):
     for t in (0, 2):
         assert math.isnan(float(q[t, 140])) and float(q[t, 128:140].abs().max()) == 0.0
         assert float(q[t, :128].max()) == 448.0 and float(q[t, 256:].max()) == 448.0
+
+
+# ---------------------------------------------------------------- clipping
+
+@pytest.mark.gpu
+def test_clip_where_the_factor_is_no_quotient(dm):
+    """No limit (an infinite one) never scales; a norm of 0 with eps 0 leaves the zeros alone."""
+    norm = empty(1, dtype=torch.float32)
+    g = torch.zeros(100, device="cuda")
+    dm.clip_grad_norm(dm.GradList([g]), 0.0, norm, eps=0.0)
+    assert float(norm) == 0.0 and float(g.abs().max()) == 0.0
+    g = cuda(randn(141, 1000))
+    before = g.clone()
+    dm.clip_grad_norm(dm.GradList([g]), math.inf, norm)
+    assert torch.equal(g, before) and math.isfinite(float(norm))
+    g[17] = math.inf
+    before = g.clone()
+    out = torch.empty_like(g)
+    dm.clip_grad_norm(dm.GradList([g], [out]), math.inf, norm)
+    assert math.isinf(float(norm)) and torch.equal(out, before)
