@@ -562,20 +562,33 @@ class GradList:
             rows.append([g.data_ptr(), o.data_ptr(), g.numel(), self.chunks, f32])
             self.chunks += int(lib().dmoe_grad_chunks(g.data_ptr(), g.numel(), f32))
         device = self.grads[0].device if self.grads else "cuda"
+        # both copied from the host, which waits: nothing is left to run when the
+        # list is built, so that any stream may use it
         self.table = torch.tensor(rows or [[0] * 5], dtype=torch.int64).to(device)
-        self.ws = torch.zeros(int(lib().dmoe_clip_grad_norm_workspace_size()), dtype=torch.uint8, device=device)
+        self.ws = torch.zeros(int(lib().dmoe_clip_grad_norm_workspace_size()), dtype=torch.uint8).to(device)
+        self._streams = {_stream(None)}  # those that the allocator knows of
 
     def __len__(self):
         return len(self.grads)
+
+    def _used_by(self, handle):
+        """Keeps table and scratch from being given to others while that stream works with them."""
+        if handle not in self._streams:
+            stream = torch.cuda.ExternalStream(handle, device=self.table.device)
+            self.table.record_stream(stream)
+            self.ws.record_stream(stream)
+            self._streams.add(handle)
 
 
 def clip_grad_norm(grads: GradList, max_norm: float, norm, eps: float = 1e-6, stream=None):
     """norm (fp32 [1], written) = the global 2-norm of all gradients; every one
     is scaled by min(1, max_norm / (norm + eps)) into its output."""
     _need(norm, torch.float32, "norm", numel=1)
+    handle = _stream(stream)
+    grads._used_by(handle)
     _check("dmoe_clip_grad_norm", lib().dmoe_clip_grad_norm(
         _ptr(grads.table), len(grads), grads.chunks, max_norm, eps, _ptr(norm), _ptr(grads.ws), grads.ws.numel(),
-        _stream(stream)))
+        handle))
 
 
 # ----------------------------------------------------------------- whole layer

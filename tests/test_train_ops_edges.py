@@ -263,3 +263,48 @@ def test_clip_where_the_factor_is_no_quotient(dm):
     out = torch.empty_like(g)
     dm.clip_grad_norm(dm.GradList([g], [out]), math.inf, norm)
     assert math.isinf(float(norm)) and torch.equal(out, before)
+
+
+@pytest.mark.gpu
+def test_clip_on_another_stream_than_the_lists(dm):
+    """A list is ready when it is built, whatever its stream has still to do: its scratch comes from memory that
+    held something else, its stream is busy, and the clipping goes to a stream that waits for nothing."""
+    sizes = [5000, 70000, 3, 8192]
+    gs = [cuda(randn(151 + i, n)) for i, n in enumerate(sizes)]
+    total = math.sqrt(sum(float((g.double() ** 2).sum()) for g in gs))
+    outs = [torch.empty_like(g) for g in gs]
+    norm = empty(1, dtype=torch.float32)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        dirty = [torch.full((1 << 14,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        del dirty
+        busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.stream(busy):
+            grads = dm.GradList(gs, outs)
+            assert busy.query()  # nothing of the building is left to run
+        norm.fill_(777.0)
+        torch.cuda.synchronize()
+        dm.clip_grad_norm(grads, 1.0, norm, stream=other)
+        other.synchronize()
+        assert abs(float(norm) - total) <= 600 * U32 * total
+
+
+@pytest.mark.gpu
+def test_a_lists_scratch_outlives_its_use_on_another_stream(dm):
+    """The list goes while its clipping still waits in another stream; what is allocated next must not get its memory."""
+    g = cuda(randn(161, 100000))
+    out, norm = torch.empty_like(g), empty(1, dtype=torch.float32)
+    total = math.sqrt(float((g.double() ** 2).sum()))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    grads = dm.GradList([g], [out])
+    places = {grads.table.data_ptr(), grads.ws.data_ptr()}
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+        dm.clip_grad_norm(grads, 1.0, norm)
+    del grads
+    fresh = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (40, 512, 1 << 14, 16400) for _ in range(4)]
+    assert not places & {f.data_ptr() for f in fresh}
+    other.synchronize()
+    assert abs(float(norm) - total) <= 600 * U32 * total
