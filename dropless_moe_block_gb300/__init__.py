@@ -22,6 +22,7 @@ softmax cross entropy and both gradients without the logits in memory) and
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 import threading
@@ -541,11 +542,29 @@ def linear_cross_entropy(x, w, targets, loss, lse, ws, dx=None, dw=None, d_loss=
         _ptr(dw), f32, int(bool(accumulate)), piece, _ptr(ws), ws.numel(), _stream(stream)))
 
 
+def _check_disjoint(ins, outs):
+    """Refuses outputs (address, bytes) that overlap one another or another
+    tensor's gradient: what lies under both would be scaled twice, or read
+    after it was scaled."""
+    written = sorted((p, p + n, i) for i, (p, n) in enumerate(outs) if n)
+    for (_, end, i), (start, _, j) in zip(written, written[1:]):
+        if start < end:
+            raise ValueError(f"outputs {i} and {j} overlap")
+    starts = [w[0] for w in written]
+    for i, (p, n) in enumerate(ins):
+        k = bisect.bisect_left(starts, p + n) if n else 0  # those from k on begin after it
+        while k > 0 and written[k - 1][1] > p:
+            k -= 1
+            if written[k][2] != i or starts[k] != p:
+                raise ValueError(f"gradient {i} and output {written[k][2]} overlap")
+
+
 class GradList:
     """A list of gradients (bf16 or fp32, contiguous, any sizes and places) as
     the device table that ``clip_grad_norm`` walks, with its scratch.  ``outs``
     (same types and sizes) receive the clipped gradients; without them the
-    gradients are clipped in place.  The list keeps its tensors."""
+    gradients are clipped in place.  Outputs may not overlap one another or
+    another tensor's gradient (so in place no gradient is listed twice)."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -561,6 +580,7 @@ class GradList:
             f32 = int(g.dtype == torch.float32)
             rows.append([g.data_ptr(), o.data_ptr(), g.numel(), self.chunks, f32])
             self.chunks += int(lib().dmoe_grad_chunks(g.data_ptr(), g.numel(), f32))
+        _check_disjoint(*([(t.data_ptr(), t.numel() * t.element_size()) for t in ts] for ts in (self.grads, self.outs)))
         device = self.grads[0].device if self.grads else "cuda"
         # both copied from the host, which waits: nothing is left to run when the
         # list is built, so that any stream may use it

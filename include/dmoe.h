@@ -561,7 +561,7 @@ dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, cons
 #define DMOE_GRAD_CHUNK 8192
 
 /* One tensor of a list of gradients: n contiguous elements, bf16, or fp32
- * when f32 != 0; out may be in.  first_chunk: the sum of dmoe_grad_chunks()
+ * when f32 != 0; out may be in, and overlaps nothing else of the list.  first_chunk: the sum of dmoe_grad_chunks()
  * over the tensors before this one. */
 typedef struct dmoe_grad {
   const void* in;

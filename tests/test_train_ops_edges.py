@@ -308,3 +308,32 @@ def test_a_lists_scratch_outlives_its_use_on_another_stream(dm):
     assert not places & {f.data_ptr() for f in fresh}
     other.synchronize()
     assert abs(float(norm) - total) <= 600 * U32 * total
+
+
+def test_gradients_that_overlap_are_refused():
+    """Two outputs in one place, or an output over another tensor's gradient, would be scaled twice or half."""
+    m = _dm()
+    check = m._check_disjoint
+    check([(64, 32), (0, 64), (96, 0), (96, 8)], [(64, 32), (0, 64), (96, 0), (96, 8)])  # in place
+    check([(0, 64), (0, 64), (32, 64)], [(100, 64), (164, 64), (300, 64)])  # read twice, written apart
+    check([(0, 64), (64, 64)], [(128, 64), (192, 64)])
+    for ins, outs in (([(0, 64), (0, 64)], [(0, 64), (0, 64)]),        # the same gradient twice, in place
+                      ([(0, 64), (100, 64)], [(200, 64), (232, 64)]),  # outputs over each other
+                      ([(0, 64), (100, 64)], [(100, 64), (200, 64)]),  # over another's gradient
+                      ([(0, 64)], [(32, 64)]),                         # over its own, moved
+                      ([(0, 64), (256, 8)], [(0, 64), (60, 8)])):
+        with pytest.raises(ValueError, match="overlap"):
+            check(ins, outs)
+
+
+@pytest.mark.gpu
+def test_a_gradient_listed_twice_is_refused(dm):
+    g, h = torch.ones(100, device="cuda"), torch.ones(100, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        dm.GradList([g, h, g])
+    with pytest.raises(ValueError, match="overlap"):
+        dm.GradList([g, h], [h, torch.empty_like(h)])
+    norm = empty(1, dtype=torch.float32)
+    a, b = torch.empty_like(g), torch.empty_like(g)
+    dm.clip_grad_norm(dm.GradList([g, g], [a, b]), 1e9, norm)  # read twice, written apart
+    assert torch.equal(a, g) and torch.equal(b, g) and abs(float(norm) - math.sqrt(200)) <= 8 * U32 * 15
