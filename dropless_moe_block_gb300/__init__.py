@@ -447,6 +447,13 @@ def _rows(t, dtype, name, T, d):
     return t.stride(0)
 
 
+def _apart(a, b, name, other):
+    """Refuses contiguous tensors that share memory."""
+    p, q = a.data_ptr(), b.data_ptr()
+    if p < q + b.numel() * b.element_size() and q < p + a.numel() * a.element_size():
+        raise ValueError(f"{name} must not overlap {other}")
+
+
 def _norm_weight(weight, d):
     if weight is None or weight.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("weight must be torch.bfloat16 or torch.float32")
@@ -459,9 +466,9 @@ def add_rms_norm(x, residual, weight, eps: float, h, y, rstd=None, q=None, q_sca
     (float8_e4m3fn [T, d]) and ``q_scale`` (fp32 [T, ceil(d / 128)]) also, or
     with ``y=None`` only, y in 8 bits with one scale per row and 128 columns.
     ``residual=None`` norms x itself (``h`` may then be None).  ``x`` and
-    ``residual`` may be row slices of wider tensors; ``h`` may be ``x`` or
-    ``residual`` and ``y`` may be ``x``.  ``rstd`` (fp32 [T]) is what the
-    backward reads."""
+    ``residual`` may be row slices of wider tensors; ``h`` and ``y`` may each be
+    one of them that is contiguous, but not the same one.  ``rstd`` (fp32 [T])
+    is what the backward reads."""
     T, d = x.shape
     ldx = _rows(x, torch.bfloat16, "x", T, d)
     ldr = 0 if residual is None else _rows(residual, torch.bfloat16, "residual", T, d)
@@ -475,9 +482,12 @@ def add_rms_norm(x, residual, weight, eps: float, h, y, rstd=None, q=None, q_sca
     if q is not None:
         _need(q, torch.float8_e4m3fn, "q", shape=(T, d))
         _need(q_scale, torch.float32, "q_scale", shape=(T, (d + 127) // 128))
+    hp, yp = _ptr(h), _ptr(y)
+    if hp and hp == yp:
+        raise ValueError("h must not overlap y")
     _check("dmoe_add_rms_norm", lib().dmoe_add_rms_norm(
-        _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), wf, eps, T, d, _ptr(h), _ptr(y), _ptr(rstd), _ptr(q),
-        _ptr(q_scale), _stream(stream)))
+        _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), wf, eps, T, d, hp, yp, _ptr(rstd), _ptr(q), _ptr(q_scale),
+        _stream(stream)))
 
 
 def add_rms_norm_backward_workspace_size(T: int, d: int) -> int:
@@ -517,7 +527,9 @@ def linear_cross_entropy(x, w, targets, loss, lse, ws, dx=None, dw=None, d_loss=
     gradients: of the mean loss over the targets that count, or of
     sum(d_loss * loss) when ``d_loss`` [T] is given.  ``dw`` is bf16 or fp32
     (``accumulate`` adds to an fp32 one).  ``piece`` bounds the workspace: the
-    tokens whose [piece, V] array exists at one time (0: 8192)."""
+    tokens whose [piece, V] array exists at one time (0: 8192).  ``dx`` may be
+    ``x`` where no ``dw`` is asked for; else neither may overlap ``x``, ``w``
+    or the other."""
     T, d = x.shape
     V = w.shape[0]
     _need(x, torch.bfloat16, "x")
@@ -537,6 +549,14 @@ def linear_cross_entropy(x, w, targets, loss, lse, ws, dx=None, dw=None, d_loss=
             raise ValueError(f"dw must be torch.bfloat16 or torch.float32, got {dw.dtype}")
         f32 = int(dw.dtype == torch.float32)
         _need(dw, dw.dtype, "dw", shape=(V, d))
+        _apart(dw, x, "dw", "x")
+        _apart(dw, w, "dw", "w")
+    if dx is not None:
+        _apart(dx, w, "dx", "w")
+        if dw is not None:
+            _apart(dx, dw, "dx", "dw")
+        if dw is not None or dx.data_ptr() != x.data_ptr():
+            _apart(dx, x, "dx", "x")
     _check("dmoe_linear_cross_entropy", lib().dmoe_linear_cross_entropy(
         _ptr(x), _ptr(w), _ptr(targets), T, d, V, ignore_index, _ptr(d_loss), _ptr(loss), _ptr(lse), _ptr(dx),
         _ptr(dw), f32, int(bool(accumulate)), piece, _ptr(ws), ws.numel(), _stream(stream)))

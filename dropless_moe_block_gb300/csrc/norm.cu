@@ -522,6 +522,9 @@ struct Backward {
 
 bool bad_ptr(const void* p) { return !dmoe::aligned16(p); }
 bool bad_ld(int64_t ld, int d) { return ld < d || (ld & 7); }
+// Rows written over rows of another pitch: over some that another block has yet
+// to read.
+bool bad_alias(const void* out, const void* in, int64_t ld, int T, int d) { return out && out == in && T > 1 && ld != d; }
 
 }  // namespace
 
@@ -535,6 +538,9 @@ DMOE_API dmoe_status dmoe_add_rms_norm(const uint16_t* x, int64_t ldx, const uin
   if (bad_ptr(x) || bad_ptr(residual) || bad_ptr(weight) || bad_ptr(h) || bad_ptr(y) ||
       (reinterpret_cast<uintptr_t>(q) & 7) ||
       ((reinterpret_cast<uintptr_t>(rstd) | reinterpret_cast<uintptr_t>(q_scale)) & 3))
+    return DMOE_ERR_INVALID_ARG;
+  if (bad_alias(h, x, ldx, T, d) || bad_alias(y, x, ldx, T, d) || bad_alias(h, residual, ldr, T, d) ||
+      bad_alias(y, residual, ldr, T, d))
     return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;
   dmoe_status s = dmoe::device_info(&di);
@@ -562,6 +568,7 @@ DMOE_API dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy
   if (bad_ptr(dy) || bad_ptr(h) || bad_ptr(weight) || bad_ptr(dh) || bad_ptr(dx) || bad_ptr(ws) ||
       ((reinterpret_cast<uintptr_t>(rstd) | reinterpret_cast<uintptr_t>(dw)) & 3))
     return DMOE_ERR_INVALID_ARG;
+  if (bad_alias(dx, dy, lddy, T, d) || bad_alias(dx, dh, lddh, T, d)) return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;
   dmoe_status s = dmoe::device_info(&di);
   if (s != DMOE_OK) return s;

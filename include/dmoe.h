@@ -488,8 +488,10 @@ dmoe_status dmoe_combine_backward(const uint16_t* dy, const uint16_t* y_perm,
  *   n[t, c] = h[t, c] * r * weight[c]          (fp32)
  * The stream is kept in bf16 and the norm reads the kept value, which is all
  * the backward has.  Outputs (each may be NULL unless stated):
- *   h       [T, d] bf16; required with a residual; may be x or residual
- *   y       [T, d] bf16: n rounded; may be x
+ *   h       [T, d] bf16; required with a residual; may be x or residual, if
+ *           that one's rows lie d apart (else refused)
+ *   y       [T, d] bf16: n rounded; may be x or residual on the same condition;
+ *           must not be h
  *   rstd    [T] fp32: r, what the backward reads
  *   q       [T, d] e4m3 and q_scale [T, ceil(d / 128)] fp32 (both or
  *           neither): n in 8 bits; 128 columns g share the scale
@@ -512,7 +514,7 @@ size_t dmoe_add_rms_norm_backward_workspace_size(int T, int d);
  * dx is the gradient of x and of residual alike.  dh [T, d] (may be NULL) is
  * the gradient that arrives at h from the residual stream.  dy and dh may
  * have rows lddy, lddh elements apart (at least d, multiples of 8); dx
- * [T, d] bf16 may be dy or dh.  dw [d] fp32 may be NULL (then ws too); it is
+ * [T, d] bf16 may be dy or dh, if that one's rows lie d apart (else refused).  dw [d] fp32 may be NULL (then ws too); it is
  * written, not added to, and summed in a fixed order.  T == 0 writes dw = 0.
  * Calls sharing a ws must not overlap. */
 dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, const void* weight,
@@ -543,7 +545,9 @@ size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, i
  *   x [T, d] bf16, w [V, d] bf16, targets [T] int32 (read)
  *   loss [T] fp32, lse [T] fp32 (may be NULL), dx [T, d] bf16,
  *   dw [V, d] bf16, or fp32 when dw_f32 != 0 (written; with accumulate != 0,
- *   fp32 only, added to what dw holds)
+ *   fp32 only, added to what dw holds).  dx may be x where dw is NULL (dW reads
+ *   x while dx is written); otherwise dx and dw must overlap neither one
+ *   another nor x and w
  *   ws: scratch of dmoe_linear_cross_entropy_workspace_size() bytes, 256-byte
  *   aligned; calls sharing one must not overlap.
  * A target outside [0, V) other than ignore_index counts as ignored and sets

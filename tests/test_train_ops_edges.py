@@ -337,3 +337,67 @@ def test_a_gradient_listed_twice_is_refused(dm):
     a, b = torch.empty_like(g), torch.empty_like(g)
     dm.clip_grad_norm(dm.GradList([g, g], [a, b]), 1e9, norm)  # read twice, written apart
     assert torch.equal(a, g) and torch.equal(b, g) and abs(float(norm) - math.sqrt(200)) <= 8 * U32 * 15
+
+
+# ----------------------------------------------------------------- aliases
+
+def test_rows_written_over_rows_of_another_pitch_are_refused():
+    """A block would write over rows that others have not read.  Host-side: an error status, nothing launched."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: not where a device could be given them")
+    L = _dm().lib()
+    x, r, w, h, y, q, s = (ctypes.c_void_p(0x10000 * (i + 1)) for i in range(7))
+
+    def norm(ldx=64, ldr=64, T=4, h=h, y=y):
+        return L.dmoe_add_rms_norm(x, ldx, r, ldr, w, 0, ctypes.c_float(1e-5), T, 64, h, y, None, q, s, None)
+
+    def back(lddy=64, lddh=64, T=4, dx=h):
+        return L.dmoe_add_rms_norm_backward(x, lddy, y, w, 0, q, r, lddh, T, 64, dx, None, None, 0, None)
+
+    bad = [norm(ldx=128, h=x), norm(ldr=128, h=r), norm(ldx=128, y=x), norm(ldr=128, y=r), back(lddy=128, dx=x),
+           back(lddh=128, dx=r)]
+    assert bad == [1] * len(bad), bad
+    # the same pitch, or one row: an error only because there is no device
+    good = [norm(), norm(ldx=128, ldr=72), norm(h=x), norm(h=r), norm(y=x), norm(h=r, y=x), norm(y=r),
+            norm(T=1, ldx=128, h=x), back(dx=x), back(dx=r), back(lddy=128), back(T=1, lddy=128, dx=x)]
+    assert all(g in (2, 3) for g in good), good
+
+
+@pytest.mark.gpu
+def test_outputs_that_overlap_what_is_read_are_refused(dm):
+    T, V, d = 12, 40, 64
+    buf = torch.zeros(4 * T + 2 * V, d, dtype=torch.bfloat16, device="cuda")
+    x, w = buf[:T], buf[T:T + V]
+    t = torch.zeros(T, dtype=torch.int32, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+
+    def loss(**kw):
+        return run_loss_into(dm, x, w, t, **kw)
+
+    for kw in (dict(dx=x, dw=dw), dict(dx=buf[1:T + 1], dw=dw), dict(dx=buf[1:T + 1]), dict(dx=w[:T]), dict(dw=w),
+               dict(dx=dx, dw=buf[:V]), dict(dx=buf[T + V:2 * T + V], dw=buf[T + V + 4:T + 2 * V + 4])):
+        with pytest.raises(ValueError, match="overlap"):
+            loss(**kw)
+    one = randn(165, T, d).cuda()
+    ones = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        dm.add_rms_norm(one, one, ones, 1e-5, dx, dx)
+
+
+def run_loss_into(dm, x, w, t, dx=None, dw=None):
+    loss = torch.empty(len(t), device="cuda")
+    ws = torch.empty(dm.linear_cross_entropy_workspace_size(*x.shape, len(w)), dtype=torch.uint8, device="cuda")
+    dm.linear_cross_entropy(x, w, t, loss, None, ws, dx=dx, dw=dw)
+    return loss
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 300])
+def test_dx_over_x_where_no_dw_is_asked_for(dm, T):
+    V, d = 700, 72
+    x, w = randn(166, T, d), randn(167, V, d, scale=0.3)
+    t = torch.randint(0, V, (T,), generator=gen(168), dtype=torch.int32)
+    own = run_loss(dm, cuda(x), cuda(w), cuda(t), dw=None)
+    xs = cuda(x)
+    loss = run_loss_into(dm, xs, cuda(w), cuda(t), dx=xs)
+    assert torch.equal(xs, own["dx"]) and torch.equal(loss, own["loss"])
