@@ -788,6 +788,7 @@ __global__ void __launch_bounds__(kThreadsX, 1) head_kernel(const __grid_constan
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + part * 64;
         if (!GRAD) {
           float v[64];
+          __syncwarp();  // the first sub-tile left lanes with a target or a reference of their own
           tmem_load64(tb, v);
           release();  // all of this warp's columns are in registers
           const int cols = p.V - c;  // words from here on

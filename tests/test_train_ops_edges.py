@@ -401,3 +401,22 @@ def test_dx_over_x_where_no_dw_is_asked_for(dm, T):
     xs = cuda(x)
     loss = run_loss_into(dm, xs, cuda(w), cuda(t), dx=xs)
     assert torch.equal(xs, own["dx"]) and torch.equal(loss, own["loss"])
+
+
+@pytest.mark.gpu
+def test_lanes_that_differ_in_the_first_half_of_a_wide_tile(dm):
+    """512-wide tiles whose first 256 words hold some rows' targets, and logits past the references' range in some
+    rows only: the second half is loaded by whole warps all the same."""
+    T, V, d = 300, 38900, 1032
+    x, w = randn(201, T, d), randn(202, V, d, scale=0.5 / math.sqrt(d))
+    x[:, 0], w[:, 0] = 0.0, 0.0
+    x[::3, 0] = 1.0
+    w[0:64, 0], w[512 * 20 + 70:512 * 20 + 100, 0] = 90.0, -120.0
+    t = torch.randint(0, V, (T,), generator=gen(203))
+    t[::2] = t[::2] // 512 * 512 + t[::2] % 256
+    t[::2].clamp_(max=V - 1)
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t.int()))
+    check_loss({**out, "dx": None, "dw": None}, x, w, t.int())
+    _, dx, dw, tx, tw = bounds(x, w, t, again=1)
+    close(out["dx"], dx, tx, "dx")
+    close(out["dw"], dw, tw + U16 * dw.abs(), "dw")
