@@ -420,3 +420,96 @@ def test_lanes_that_differ_in_the_first_half_of_a_wide_tile(dm):
     _, dx, dw, tx, tw = bounds(x, w, t, again=1)
     close(out["dx"], dx, tx, "dx")
     close(out["dw"], dw, tw + U16 * dw.abs(), "dw")
+
+
+# ------------------------------------- sizes at which the launches change
+
+def skewed(seed, T, V):
+    """Word frequencies like Zipf's, some runs of one word, and words of exactly 1 to 6, 32, 33 and 64 tokens."""
+    u = torch.rand(T, generator=gen(seed), dtype=torch.float64)
+    t = (torch.exp(u * math.log(V / 2)) - 1.0).long() + V // 2
+    at = 0
+    for i, n in enumerate((1, 2, 3, 4, 5, 6, 32, 33, 64, 4, 4, 4, 5, 5)):
+        t[at:at + n] = i
+        at += n
+    t = t[torch.randperm(T, generator=gen(seed + 1))].clamp(max=V - 1)
+    t[torch.randperm(T, generator=gen(seed + 2))[:T // 10]] = -100
+    return t.int()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,d", [(2048, 300, 64), (2049, 300, 64), (4095, 1009, 72), (4096, 1009, 72), (4500, 5003, 72),
+                                   (4109, 300, 264)])
+def test_loss_of_many_tokens(dm, T, V, d):
+    """Above 2048 tokens the row statistics take 32 rows a block and the targets are sorted in several chunks, from
+    4096 on the words of up to 4 tokens are added one by one, and more than 16 pair rows make two groups of tiles."""
+    x, w, t = randn(171, T, d), randn(172, V, d, scale=2.0 / math.sqrt(d)), skewed(173, T, V)
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t))
+    assert dm.get_error() == 0
+    check_loss(out, x, w, t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,piece", [(700, 256), (517, 256), (8, 0)])
+def test_accumulation_over_pieces(dm, T, piece):
+    V, d = 391, 88
+    x, w = randn(174, T, d), randn(175, V, d, scale=0.3)
+    t = torch.randint(0, V, (T,), generator=gen(176), dtype=torch.int32)
+    t[::6] = -100
+    g, base = randn(177, T, dtype=torch.float32), randn(178, V, d, dtype=torch.float32)
+    n = dm.linear_cross_entropy_workspace_size(T, d, V, dw_dtype=torch.float32, piece=piece)
+    out = dict(loss=empty(T, dtype=torch.float32), lse=empty(T, dtype=torch.float32), dx=empty(T, d, dtype=torch.bfloat16),
+               dw=cuda(base.clone()))
+    dm.linear_cross_entropy(cuda(x), cuda(w), cuda(t), out["loss"], out["lse"],
+                            torch.full((n,), 255, dtype=torch.uint8, device="cuda"), dx=out["dx"], dw=out["dw"],
+                            d_loss=cuda(g), accumulate=True, piece=piece)
+    check_loss(out, x, w, t, d_loss=g, base=base)
+
+
+# ------------------------------------------- where 16 bits are rounded to
+
+def tight_case(T, V, d):
+    x, w = randn(181, T, d), randn(182, V, d, scale=0.5 / math.sqrt(d))
+    t = torch.randint(0, V, (T,), generator=gen(183), dtype=torch.int32)
+    t[::5] = -100
+    return x, w, t
+
+
+def test_the_targets_part_in_16_bits_would_be_seen():
+    """The bound is one that G rounded to bf16 as a whole would break (planted in the reference, no kernel)."""
+    x, w, t = tight_case(60, 1009, 64)
+    G, _, dw, _, tw = bounds(x, w, t)
+    rounded = G.float().to(torch.bfloat16).double().t() @ x.double()
+    assert bool(((rounded - dw).abs() > tw).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,d", [(60, 1009, 64), (7, 1009, 64), (300, 5003, 136), (4100, 5003, 64)])
+def test_the_targets_part_keeps_32_bits(dm, T, V, d):
+    x, w, t = tight_case(T, V, d)
+    _, dx, dw, tx, tw = bounds(x, w, t)
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t), dw=torch.float32)
+    close(out["dx"], dx, tx, "dx")
+    close(out["dw"], dw, tw, "dw")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [512, 4096, 8192])
+def test_logits_of_sparse_rows(dm, d):
+    """Rows of which a few columns are not zero, with logits that are exact in fp32: they come out within the mean
+    that is given back for the tensor cores' truncation, (d / 16) 2^-26 of a logit (and a few roundings)."""
+    T, V = 24, 130
+    x, w = torch.zeros(T, d), torch.zeros(V, d)
+    cols = torch.randperm(d, generator=gen(191))[:3]
+    for i, c in enumerate(cols):
+        x[:, c] = torch.randint(-8, 9, (T,), generator=gen(192 + i)).float()
+        w[:, c] = torch.randint(-8, 9, (V,), generator=gen(195 + i)).float()
+    x, w = x.to(torch.bfloat16), w.to(torch.bfloat16)
+    t = torch.randint(0, V, (T,), generator=gen(198), dtype=torch.int32)
+    loss, lse, _, _, l = ref_loss(x, w, t, -100)
+    out = run_loss(dm, cuda(x), cuda(w), cuda(t), dx=False, dw=None)
+    top = l.abs().amax(1)
+    # besides: exp2's argument (two roundings of up to 1.45 top) and value, the sum and the logarithm
+    e = ((d / 16) * 2.0 ** -26 + 8 * U32) * top + 4e-6
+    close(out["lse"], lse, e, "lse")
+    close(out["loss"], loss, 2 * e, "loss")
