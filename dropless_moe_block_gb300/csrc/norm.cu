@@ -24,11 +24,11 @@
 
 namespace {
 
-// Block sizes while a row takes fewer threads.  Forward: smaller blocks end
-// sooner (rows of 512 columns, 16384 of them: 11.6 us at 256, 11.2 at 128;
-// 4093 rows of 3584 in 8 bits: 19.4 and 18.7 us).
+// Block sizes while a row takes fewer threads (up to 2048 columns): smaller
+// blocks end sooner.  The kernel alone at 256 and 128 threads: forward 16384 x
+// 512 11.3 and 11.0 us, backward 8192 x 512 13.0 and 10.8.
 constexpr int kFwdThreads = 128;
-constexpr int kNormThreads = 128;  // backward (8192 x 512: 15.7 us at 256, 13.9 at 128)
+constexpr int kNormThreads = 128;  // backward
 constexpr int kMaxD = 32768;
 constexpr int kQGroup = 128;       // columns that share a scale in the 8-bit rows
 constexpr float kE4M3Max = 448.f;
@@ -38,9 +38,9 @@ constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 // a / b from inv = 1 / b: the product, then one step by what it leaves of a, which
 // the fused multiply-add gives without a rounding (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990).  1 / b the
-// same way, from an approximation.  4093 rows of 3584 in 8 bits: 19.5
-// us; 18.7 with values times the approximation, which puts some of them one
-// step of e4m3 off; 22.9 with divisions.
+// same way, from an approximation.  4093 rows of 3584 in 8 bits, calls in a
+// row: 19.5 us; 18.7 with values times the approximation, which puts some of
+// them one step of e4m3 off; 22.9 with divisions.
 __device__ __forceinline__ float quotient(float a, float inv, float b) {
   const float q = a * inv;
   return fmaf(fmaf(-q, b, a), inv, q);
@@ -189,12 +189,19 @@ __global__ void __launch_bounds__(TPR > kFwdThreads ? TPR : kFwdThreads, 1536 / 
       if (in) {
         const float back = s < INFINITY ? s : 0.f;  // what is finite over an infinite scale is 0
         const float inv = reciprocal(s, back);
+        // Two values an instruction, except where forty registers must hold four
+        // vectors (4096 x 10240: 76.9 us in pairs, 66.8 one by one; 4093 x 3584,
+        // with two vectors, 19.5 and 19.9).
+        constexpr bool PAIRS = !(TPR == 512 && VPT == 4);
         uint2 b;
         uint16_t* p = reinterpret_cast<uint16_t*>(&b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          p[j] = __nv_cvt_float2_to_fp8x2(quotient(make_float2(f[2 * j], f[2 * j + 1]), inv, back), __NV_SATFINITE,
-                                          __NV_E4M3);
+        for (int j = 0; j < 4; ++j) {
+          const float2 n = make_float2(f[2 * j], f[2 * j + 1]);
+          p[j] = __nv_cvt_float2_to_fp8x2(
+              PAIRS ? quotient(n, inv, back) : make_float2(quotient(n.x, inv, back), quotient(n.y, inv, back)),
+              __NV_SATFINITE, __NV_E4M3);
+        }
         *(reinterpret_cast<uint2*>(q + t * d) + v) = b;
         if ((v & 15) == 0) q_scale[t * ((d + kQGroup - 1) / kQGroup) + (v >> 4)] = s;
       }
@@ -205,10 +212,12 @@ __global__ void __launch_bounds__(TPR > kFwdThreads ? TPR : kFwdThreads, 1536 / 
 // Backward.  A persistent block walks units of RPB rows (BLOCK / TPR), dealt
 // round-robin; a ring of `stages` units of dy, h and dh is filled ahead by bulk
 // copies (one per row and tensor), so that the loads in flight do not depend
-// on registers or on the barrier each row's sum needs (16381 x 4096: 113 us with
-// loads into registers, 85 us, 6.3 TB/s, with the ring).  Every thread keeps its columns of the weight and adds its columns
-// of dw over its rows; a block's row groups meet in shared memory, and the
-// block writes one fp32 row of partial[gridDim.x][d].
+// on registers or on the barrier each row's sum needs.  Between a row's sum and
+// its use it stays packed in registers, 8 values in 4 (16381 x 4096, the kernel
+// alone: 106 us with loads straight into registers, 100 with the ring, 82, 6.5
+// TB/s, with the packed row).  Every thread keeps its columns of the weight and
+// adds its columns of dw over its rows; a block's row groups meet in shared
+// memory, and the block writes one fp32 row of partial[gridDim.x][d].
 template <int TPR, int VPT, bool WF32>
 __global__ void __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, TPR > 256 ? 1 : TPR > kNormThreads ? 2 : 4)
     add_rms_norm_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* h, const void* __restrict__ weight,

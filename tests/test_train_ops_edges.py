@@ -206,7 +206,7 @@ def test_loss_in_a_longer_batchs_workspace(dm):
 # ------------------------------------------------------- rows in 8 bits
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,d", [(64, 512), (33, 1000), (9, 3584), (5, 8200)])
+@pytest.mark.parametrize("T,d", [(64, 512), (33, 1000), (9, 3584), (5, 8200), (2, 16392)])
 def test_8_bit_rows_are_the_quotients_rounded_once(dm, T, d):
     """Given the kernel's own rstd, y in fp32 is two products, the scale one quotient and a value one more: each of
     them, rounded as IEEE says, gives the bits."""
