@@ -32,14 +32,20 @@
 // subtracted, fp32 and bf16 reach from 1e-38 to 3e38, so in the usual case
 // every pair of a row has the reference 0 and E needs no second pass.  A row
 // whose groups disagree is brought to its largest reference by launch 2.
-// What bf16 costs is one rounding of E and one of s x (2^-8 of an element
-// at most, independent from element to element).
+// What bf16 costs is one rounding of E, a second where launch 2 brings a row to
+// one reference, and one of s x (2^-8 of an element at most each, independent
+// from element to element): the products are of tensor-core operands, so a dW
+// in fp32, too, sums terms known to 8 bits, only the target's part to 24.
 //
-// The tensor cores truncate where they add a product to an accumulator: a
-// logit over d columns comes out about (d / 16) 2^-26 of itself too small
-// (measured, d = 512 to 8192: 1.3e-8 to 1.6e-8 per 16 columns).  The
-// epilogue gives that mean back; without it the loss is 1.3e-6 off at d =
-// 4096.
+// The tensor cores truncate where they add products to an accumulator, so a
+// logit comes out too small by an amount that goes by how its sum grows.  In
+// units of (d / 16) 2^-26 of the logit (d = 512 to 8192, measured): none where
+// every partial sum fits (one-hot rows, small integers), 1.0 to 1.1 for Gaussian
+// rows, 1.9 to 4.6 where all products have one sign.  The epilogue gives
+// one unit back, an estimate for rows as a norm leaves them: the loss at d =
+// 4096 is 3e-7 off with it and 1.3e-6 without; sums of one sign stay 0.9 to 3.6
+// units too small, and exact logits come out one unit too large (3.8e-6 of
+// themselves at d = 4096).  An fp32 sum in sequence may be off by 64 units.
 //
 // The products are bound by the tensor cores (2 T V d flops each).  They run
 // as persistent CTA pairs (tcgen05 cta_group::2): M = 256 x N = 512 tiles (two
@@ -89,7 +95,7 @@ constexpr int kGroup = 64;           // columns that share a (ref, sum) pair
 // exponential, reaches the denormals.
 constexpr float kRefHigh = 40.f, kRefLow = -60.f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kTruncation = 1.f / 67108864.f;  // 2^-26 of the sum per 16 products
+constexpr float kTruncation = 1.f / 67108864.f;  // given back: 2^-26 of the sum per 16 products, see above
 constexpr int kPieceDefault = 8192;  // tokens per piece when the caller names none
 constexpr int kPieceMax = 1 << 18;
 // Logits over at most so many columns run 256-wide tiles: their two
@@ -186,7 +192,7 @@ struct ParamsX {
   float* refs;         // reference is not 0 but this one
   int64_t ldp;
   float* target_logit;
-  float unbias;        // 1 + the mean truncation
+  float unbias;        // 1 + the truncation given back
   const int32_t* all;  // the whole call's targets, to be counted (NULL: not here)
   int T, ignore;
   int32_t* count;

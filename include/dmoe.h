@@ -534,20 +534,27 @@ dmoe_status dmoe_add_rms_norm_backward(const uint16_t* dy, int64_t lddy, const u
 size_t dmoe_linear_cross_entropy_workspace_size(int T, int d, int V, int grad, int dw_f32, int piece);
 
 /* Logits l[t, v] = <x[t], w[v]> (bf16 products, fp32 sums on the tensor
- * cores), never stored; for every token t:
+ * cores, which truncate: off by up to some 4 (d / 16) 2^-26 of the largest
+ * partial sum, as measured), never stored; for every token t:
  *   lse[t]  = log sum_v exp(l[t, v])
  *   loss[t] = lse[t] - l[t, targets[t]], or 0 where targets[t] == ignore_index
- * and, with G[t, v] = g[t] * (exp(l[t, v] - lse[t]) - [v == targets[t]])
- * rounded to bf16,
+ * and, with G[t, v] = g[t] * (exp(l[t, v] - lse[t]) - [v == targets[t]]),
  *   dx = G w,  dw = G^T x                       (each may be NULL)
- * where g[t] = d_loss[t], or 1 / (number of targets that count) when d_loss
- * is NULL (the mean loss), and 0 where targets[t] == ignore_index.
+ * summed in fp32.  The exponentials are rounded to bf16 (up to twice in rows
+ * whose logits leave [-60, 40]), for dw also the rows of x with their factors, so
+ * that an fp32 dw, too, sums terms of 8 bits; the targets' part, c[t] w[v] and
+ * c[t] x[t] with c = G[t, targets[t]], is not rounded.  Up to 8 tokens' dw has
+ * all of its terms in fp32.
+ * Here g[t] = d_loss[t], or 1 / (number of targets that count) when d_loss
+ * is NULL (the mean loss), and 0 where targets[t] == ignore_index.  A row of
+ * x with g[t] == 0 may hold anything, what is not finite too: it reaches no
+ * gradient.
  *   x [T, d] bf16, w [V, d] bf16, targets [T] int32 (read)
  *   loss [T] fp32, lse [T] fp32 (may be NULL), dx [T, d] bf16,
  *   dw [V, d] bf16, or fp32 when dw_f32 != 0 (written; with accumulate != 0,
  *   fp32 only, added to what dw holds).  dx may be x where dw is NULL (dW reads
  *   x while dx is written); otherwise dx and dw must overlap neither one
- *   another nor x and w
+ *   another nor x and w.
  *   ws: scratch of dmoe_linear_cross_entropy_workspace_size() bytes, 256-byte
  *   aligned; calls sharing one must not overlap.
  * A target outside [0, V) other than ignore_index counts as ignored and sets
@@ -565,8 +572,9 @@ dmoe_status dmoe_linear_cross_entropy(const uint16_t* x, const uint16_t* w, cons
 #define DMOE_GRAD_CHUNK 8192
 
 /* One tensor of a list of gradients: n contiguous elements, bf16, or fp32
- * when f32 != 0; out may be in, and overlaps nothing else of the list.  first_chunk: the sum of dmoe_grad_chunks()
- * over the tensors before this one. */
+ * when f32 != 0; out may be in, and overlaps nothing else of the list (with
+ * another offset from 16 bytes than in's it is written element by element).
+ * first_chunk: the sum of dmoe_grad_chunks() over the tensors before this one. */
 typedef struct dmoe_grad {
   const void* in;
   void* out;
@@ -588,10 +596,12 @@ size_t dmoe_clip_grad_norm_workspace_size(void);
  * tensor with out == in is left alone when c is 1).  A norm that is not
  * finite is not replaced: an infinite one gives c = 0, NaN reaches every
  * output.  c is 1 for an infinite max_norm (no limit) unless the norm is NaN,
- * and where norm + eps is 0.  grads [n] is a DEVICE array, chunks the total of its tensors'
- * chunks; elements must be aligned to their size; norm [1] fp32 (device,
- * written).  The sums run in a fixed order (squares in fp32, their sums of
- * chunks and blocks in fp64).  Calls sharing a ws must not overlap. */
+ * and where norm + eps is 0.  grads [n] is a DEVICE array, chunks the total of
+ * its tensors' chunks; elements must be aligned to their size; norm [1] fp32
+ * (device, written).  The sums run in a fixed order (squares and a thread's
+ * sum of a chunk in fp32, so that elements above 1.8e19 make the norm
+ * infinite; sums of chunks and blocks in fp64).  Calls sharing a ws must not
+ * overlap. */
 dmoe_status dmoe_clip_grad_norm(const dmoe_grad* grads, int n, int64_t chunks, float max_norm, float eps, float* norm,
                                 void* ws, size_t ws_bytes, dmoe_stream_t stream);
 
