@@ -513,3 +513,23 @@ def test_logits_of_sparse_rows(dm, d):
     e = ((d / 16) * 2.0 ** -26 + 8 * U32) * top + 4e-6
     close(out["lse"], lse, e, "lse")
     close(out["loss"], loss, 2 * e, "loss")
+
+
+@pytest.mark.gpu
+def test_clip_in_a_graph(dm):
+    """Captured on a stream that the list has not seen, replayed with other gradients, and the list dropped."""
+    g = cuda(randn(211, 70000))
+    out, norm = torch.empty_like(g), empty(1, dtype=torch.float32)
+    grads = dm.GradList([g], [out])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        dm.clip_grad_norm(grads, 1.0, norm)
+    for seed in (212, 213):
+        g.copy_(randn(seed, 70000))
+        graph.replay()
+        total = math.sqrt(float((g.double() ** 2).sum()))
+        assert abs(float(norm) - total) <= 600 * U32 * total
+        ref = g.cpu().double() / (total + 1e-6)
+        close(out, ref, (U16 + 600 * U32) * ref.abs(), "clipped")
+    del graph, grads
+    torch.cuda.synchronize()
