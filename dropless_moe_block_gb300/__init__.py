@@ -17,7 +17,12 @@ Beside the layer stand the other operators of a training step:
 ``add_rms_norm`` (residual addition and root-mean-square norm, with its
 backward and rows in 8 bits), ``linear_cross_entropy`` (vocabulary head,
 softmax cross entropy and both gradients without the logits in memory) and
-``clip_grad_norm`` (global norm of a ``GradList`` and its clipping).
+``clip_grad_norm`` (global norm of a ``GradList`` and its clipping).  What
+makes the layer a block of a model stands there, too: ``route_balanced``
+(softmax or sigmoid scores, a bias for balance, groups of experts),
+``sandwich_norm`` (the norm after a block, its gate, the scaled residual
+stream and the norm before the next block) and ``linear`` (dense product with
+bias, activation and residual: a shared expert), each with its backward.
 """
 
 from __future__ import annotations
@@ -36,6 +41,9 @@ __all__ = [
     "dstd", "unpermute_combine", "combine_backward", "DMoELayer", "StepRunner",
     "add_rms_norm", "add_rms_norm_backward", "add_rms_norm_backward_workspace_size", "linear_cross_entropy",
     "linear_cross_entropy_workspace_size", "GradList", "clip_grad_norm",
+    "route_balanced", "route_balanced_backward", "balance_bias",
+    "sandwich_norm", "sandwich_norm_backward", "sandwich_norm_backward_workspace_size",
+    "linear", "linear_workspace_size", "linear_backward", "linear_backward_workspace_size",
     "EPI_STORE", "EPI_GELU_FWD", "EPI_SWIGLU_FWD", "EPI_GELU_BWD", "EPI_SWIGLU_BWD", "BLOCK",
 ]
 
@@ -99,6 +107,18 @@ _SIGS = {
     "dmoe_linear_cross_entropy_workspace_size": (ctypes.c_size_t, [_I] * 6),
     "dmoe_linear_cross_entropy": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P,
                                        ctypes.c_size_t, _P]),
+    "dmoe_route_balanced": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
+    "dmoe_route_balanced_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P]),
+    "dmoe_balance_bias": (_I, [_P, _P, _I, ctypes.c_float, _P]),
+    "dmoe_sandwich_norm": (_I, [_P, _L, _P, _L, _P, _P, _I, _P, _I, ctypes.c_float, ctypes.c_float, _I, _I, _P, _P, _P,
+                                _P, _P]),
+    "dmoe_sandwich_norm_backward_workspace_size": (ctypes.c_size_t, [_I, _I]),
+    "dmoe_sandwich_norm_backward": (_I, [_P, _L, _P, _L, _P, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P, _P, _L, _I, _I,
+                                         _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dmoe_linear_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
+    "dmoe_linear": (_I, [_P, _L, _P, _P, _I, _I, _P, _L, _I, _I, _I, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dmoe_linear_backward_workspace_size": (ctypes.c_size_t, [_I, _I, _I]),
+    "dmoe_linear_backward": (_I, [_P, _L, _P, _P, _L, _P, _P, _I, _I, _I, _P, _P, _I, _P, _P, ctypes.c_size_t, _P]),
     "dmoe_grad_chunks": (_L, [_P, _L, _I]),
     "dmoe_clip_grad_norm_workspace_size": (ctypes.c_size_t, []),
     "dmoe_clip_grad_norm": (_I, [_P, _I, _L, ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
@@ -643,6 +663,253 @@ def clip_grad_norm(grads: GradList, max_norm: float, norm, eps: float = 1e-6, st
     _check("dmoe_clip_grad_norm", lib().dmoe_clip_grad_norm(
         _ptr(grads.table), len(grads), grads.chunks, max_norm, eps, _ptr(norm), _ptr(grads.ws), grads.ws.numel(),
         handle))
+
+
+# ------------------------------------------- what makes the layer a block
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_ACTS = {"none": 0, "gelu": 1, "silu": 2}
+
+
+def _name(table, key, what):
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {key!r}") from None
+
+
+def _apart_from(p, n, name, *others):
+    """Refuses an output of n bytes at p that shares memory with one of others:
+    (address, bytes, name), address None left out."""
+    for q, m, other in others:
+        if q is not None and p < q + m and q < p + n and n and m:
+            raise ValueError(f"{name} must not overlap {other}")
+
+
+def _apart_or_same(p, n, name, *others):
+    """As _apart_from, but an output may begin where another tensor does: it is
+    then that tensor, written behind what is read (the library refuses rows of
+    another pitch)."""
+    for q, m, other in others:
+        if q is not None and p != q and p < q + m and q < p + n and n and m:
+            raise ValueError(f"{name} must not overlap {other}")
+
+
+def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = "softmax", groups: int = 1,
+                   top_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Choice of k experts a token by softmax or sigmoid scores plus ``bias``
+    (fp32 [E]; None: by the logits), among the ``top_groups`` of ``groups``
+    groups of neighbouring experts whose two best choices sum to most.
+    ``gate_w``: the scores of the chosen without the bias, divided by their sum
+    (``renormalize``), times ``scale``.  Ties go to the lower expert; candidates
+    that fp32 cannot tell apart are compared in 64 bits."""
+    T, E = logits.shape
+    _need(logits, torch.float32, "logits")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", shape=(E,))
+    _need(expert_idx, torch.int32, "expert_idx", shape=(T, k))
+    _need(gate_w, torch.float32, "gate_w", shape=(T, k))
+    _check("dmoe_route_balanced", lib().dmoe_route_balanced(
+        _ptr(logits), _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
+        int(bool(renormalize)), scale, _ptr(expert_idx), _ptr(gate_w), _stream(stream)))
+
+
+def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = "softmax", renormalize: bool = True,
+                            scale: float = 1.0, stream=None):
+    """Gradient of ``route_balanced``'s weights with respect to the logits (the
+    bias has none)."""
+    T, E = logits.shape
+    k = expert_idx.shape[1]
+    _need(logits, torch.float32, "logits")
+    _need(expert_idx, torch.int32, "expert_idx", shape=(T, k))
+    _need(d_gate, torch.float32, "d_gate", shape=(T, k))
+    _need(d_logits, torch.float32, "d_logits", shape=(T, E))
+    _check("dmoe_route_balanced_backward", lib().dmoe_route_balanced_backward(
+        _ptr(logits), _ptr(expert_idx), _ptr(d_gate), T, E, k, _name(_SCORES, scores, "scores"),
+        int(bool(renormalize)), scale, _ptr(d_logits), _stream(stream)))
+
+
+def balance_bias(bias, tokens_per_expert, rate: float, stream=None):
+    """bias += rate * sign(mean load - load), in place: after a step, with the
+    loads (int32 [E]) that its permutation counted."""
+    E = bias.shape[0]
+    _need(bias, torch.float32, "bias", shape=(E,))
+    _need(tokens_per_expert, torch.int32, "tokens_per_expert", shape=(E,))
+    _check("dmoe_balance_bias", lib().dmoe_balance_bias(_ptr(bias), _ptr(tokens_per_expert), E, rate, _stream(stream)))
+
+
+def _norm_weights(w_post, w_pre, d):
+    wf = _norm_weight(w_post, d)
+    if _norm_weight(w_pre, d) != wf:
+        raise ValueError("w_post and w_pre must have the same type")
+    return wf
+
+
+def _gate(gate, T):
+    if gate is None:
+        return 0
+    _need(gate, torch.float32, "gate")
+    if gate.shape not in ((T,), (1,)):
+        raise ValueError(f"gate must have shape {(T,)} or (1,), got {tuple(gate.shape)}")
+    return gate.shape[0]
+
+
+def sandwich_norm(u, residual, w_post, w_pre, eps: float, h, y, gate=None, scale: float = 1.0, rstd_u=None,
+                  rstd_h=None, stream=None):
+    """The norm after a block, its gate, the residual stream and the norm before
+    the next block: h = scale * residual + gate * u / rms(u) * w_post (kept in
+    bf16), y = h / rms(h) * w_pre.  ``gate`` is fp32, one a row [T] or one for
+    all [1] (None: 1).  ``u`` and ``residual`` may be row slices of wider
+    tensors; ``h`` and ``y`` may each be one of them that is contiguous, but not
+    the same one.  ``rstd_u`` and ``rstd_h`` (fp32 [T]) are what the backward
+    reads."""
+    T, d = u.shape
+    ldu = _rows(u, torch.bfloat16, "u", T, d)
+    ldr = _rows(residual, torch.bfloat16, "residual", T, d)
+    wf = _norm_weights(w_post, w_pre, d)
+    n = _gate(gate, T)
+    _need(h, torch.bfloat16, "h", shape=(T, d))
+    _need(y, torch.bfloat16, "y", shape=(T, d))
+    if rstd_u is not None:
+        _need(rstd_u, torch.float32, "rstd_u", shape=(T,))
+    if rstd_h is not None:
+        _need(rstd_h, torch.float32, "rstd_h", shape=(T,))
+    up, rp, hp, yp = u.data_ptr(), residual.data_ptr(), h.data_ptr(), y.data_ptr()
+    nb = 2 * T * d
+    reads = (up, 2 * ((T - 1) * ldu + d), "u"), (rp, 2 * ((T - 1) * ldr + d), "residual")
+    _apart_from(hp, nb, "h", (yp, nb, "y"))
+    _apart_or_same(hp, nb, "h", *reads)
+    _apart_or_same(yp, nb, "y", *reads)
+    _check("dmoe_sandwich_norm", lib().dmoe_sandwich_norm(
+        up, ldu, rp, ldr, _ptr(w_post), _ptr(w_pre), wf, _ptr(gate), n, scale, eps, T, d, hp, yp, _ptr(rstd_u),
+        _ptr(rstd_h), _stream(stream)))
+
+
+def sandwich_norm_backward_workspace_size(T: int, d: int) -> int:
+    return int(lib().dmoe_sandwich_norm_backward_workspace_size(T, d))
+
+
+def sandwich_norm_backward(dy, u, h, w_post, w_pre, rstd_u, rstd_h, du, dresidual, dw_post, dw_pre, ws, dh=None,
+                           gate=None, d_gate=None, scale: float = 1.0, stream=None):
+    """Gradient of ``sandwich_norm``: du, dresidual (with the stream's own
+    gradient ``dh`` added before its scale), dw_post and dw_pre (fp32 [d]) and
+    d_gate (fp32, the gate's shape); the last three may be None."""
+    T, d = dy.shape
+    lddy = _rows(dy, torch.bfloat16, "dy", T, d)
+    ldu = _rows(u, torch.bfloat16, "u", T, d)
+    _need(h, torch.bfloat16, "h", shape=(T, d))
+    wf = _norm_weights(w_post, w_pre, d)
+    n = _gate(gate, T)
+    _need(rstd_u, torch.float32, "rstd_u", shape=(T,))
+    _need(rstd_h, torch.float32, "rstd_h", shape=(T,))
+    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", T, d)
+    _need(du, torch.bfloat16, "du", shape=(T, d))
+    _need(dresidual, torch.bfloat16, "dresidual", shape=(T, d))
+    for name, t in (("dw_post", dw_post), ("dw_pre", dw_pre)):
+        if t is not None:
+            _need(t, torch.float32, name, shape=(d,))
+    if d_gate is not None:
+        if gate is None:
+            raise ValueError("d_gate needs a gate")
+        _need(d_gate, torch.float32, "d_gate", shape=gate.shape)
+    nws = 0
+    if dw_post is not None or dw_pre is not None or (d_gate is not None and n == 1):
+        nws = _need(ws, torch.uint8, "ws").numel()
+    dyp, up, hp, dhp, dup, dxp = dy.data_ptr(), u.data_ptr(), h.data_ptr(), _ptr(dh), du.data_ptr(), dresidual.data_ptr()
+    nb = 2 * T * d
+    reads = ((dyp, 2 * ((T - 1) * lddy + d), "dy"), (up, 2 * ((T - 1) * ldu + d), "u"), (hp, nb, "h"),
+             (dhp, 2 * ((T - 1) * lddh + d), "dh"))
+    _apart_from(dup, nb, "du", (dxp, nb, "dresidual"))
+    _apart_or_same(dup, nb, "du", *reads)
+    _apart_or_same(dxp, nb, "dresidual", *reads)
+    _check("dmoe_sandwich_norm_backward", lib().dmoe_sandwich_norm_backward(
+        dyp, lddy, up, ldu, hp, _ptr(w_post), _ptr(w_pre), wf, _ptr(gate), n, scale, _ptr(rstd_u), _ptr(rstd_h), dhp,
+        lddh, T, d, dup, dxp, _ptr(dw_post), _ptr(dw_pre), _ptr(d_gate), _ptr(ws), nws, _stream(stream)))
+
+
+def linear_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().dmoe_linear_workspace_size(M, K, N))
+
+
+def linear(x, w, y, ws, bias=None, act: str = "none", deriv=None, residual=None, stream=None):
+    """y = act(x . w + bias) + residual with w [K, N] as an expert's weights lie;
+    act: "none", "gelu" (exact) or "silu".  ``deriv`` (bf16 [M, N]) receives the
+    activation's derivative, all that the backward needs of the sums.  ``x`` and
+    ``residual`` may be row slices of wider tensors; ``y`` may be ``residual``.
+    ``ws``: uint8, linear_workspace_size() bytes."""
+    M, K = x.shape
+    N = w.shape[1]
+    ldx = _rows(x, torch.bfloat16, "x", M, K)
+    _need(w, torch.bfloat16, "w", shape=(K, N))
+    _need(y, torch.bfloat16, "y", shape=(M, N))
+    _need(ws, torch.uint8, "ws")
+    bf = 0
+    if bias is not None:
+        if bias.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"bias must be torch.bfloat16 or torch.float32, got {bias.dtype}")
+        bf = int(bias.dtype == torch.float32)
+        _need(bias, bias.dtype, "bias", shape=(N,))
+    a = _name(_ACTS, act, "act")
+    if deriv is not None:
+        if a == 0:
+            raise ValueError("deriv needs an activation")
+        _need(deriv, torch.bfloat16, "deriv", shape=(M, N))
+    ldr = 0 if residual is None else _rows(residual, torch.bfloat16, "residual", M, N)
+    xp, wp, rp, yp, fp = x.data_ptr(), w.data_ptr(), _ptr(residual), y.data_ptr(), _ptr(deriv)
+    nb = 2 * M * N
+    reads = (xp, 2 * ((M - 1) * ldx + K), "x"), (wp, 2 * K * N, "w")
+    added = rp, 2 * ((M - 1) * ldr + N), "residual"
+    if fp is not None:
+        _apart_from(fp, nb, "deriv", *reads, added, (yp, nb, "y"))
+    _apart_from(yp, nb, "y", *reads)
+    _apart_or_same(yp, nb, "y", added)
+    _check("dmoe_linear", lib().dmoe_linear(
+        xp, ldx, wp, _ptr(bias), bf, a, rp, ldr, M, K, N, yp, fp, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def linear_backward_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().dmoe_linear_backward_workspace_size(M, K, N))
+
+
+def linear_backward(dy, x, w, dx, dw, ws, deriv=None, dbias=None, factor=None, stream=None):
+    """Gradient of ``linear``: with dz = dy * deriv, dx = (dz . w^T) * factor,
+    dw = x^T . dz (bf16 or fp32) and dbias = the sum of dz's rows (fp32 [N]);
+    each may be None.  The residual's gradient is dy.  ``factor`` (bf16 [M, K])
+    is the ``deriv`` of the layer that made x; dx is then that layer's dz, to be
+    given to its backward as ``dy``, with no deriv.  ``dx`` may be ``factor``."""
+    M, N = dy.shape
+    K = w.shape[0]
+    lddy = _rows(dy, torch.bfloat16, "dy", M, N)
+    _need(w, torch.bfloat16, "w", shape=(K, N))
+    ldx = 0
+    if dw is not None or x is not None:
+        ldx = _rows(x, torch.bfloat16, "x", M, K)
+    nws = _need(ws, torch.uint8, "ws").numel()
+    if deriv is not None:
+        _need(deriv, torch.bfloat16, "deriv", shape=(M, N))
+    if factor is not None:
+        if dx is None:
+            raise ValueError("factor needs dx")
+        _need(factor, torch.bfloat16, "factor", shape=(M, K))
+    dyp, xp, wp, fp, kp, dxp, dwp = (dy.data_ptr(), _ptr(x), w.data_ptr(), _ptr(deriv), _ptr(factor), _ptr(dx), _ptr(dw))
+    reads = ((dyp, 2 * ((M - 1) * lddy + N), "dy"), (xp, 2 * ((M - 1) * ldx + K), "x"), (wp, 2 * K * N, "w"),
+             (fp, 2 * M * N, "deriv"))
+    made = kp, 2 * M * K, "factor"
+    f32 = 0
+    if dw is not None:
+        if dw.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"dw must be torch.bfloat16 or torch.float32, got {dw.dtype}")
+        f32 = int(dw.dtype == torch.float32)
+        _need(dw, dw.dtype, "dw", shape=(K, N))
+        _apart_from(dwp, (4 if f32 else 2) * K * N, "dw", *reads, made)
+    if dx is not None:
+        _need(dx, torch.bfloat16, "dx", shape=(M, K))
+        _apart_from(dxp, 2 * M * K, "dx", *reads, (dwp, (4 if f32 else 2) * K * N, "dw"))
+        _apart_or_same(dxp, 2 * M * K, "dx", made)
+    if dbias is not None:
+        _need(dbias, torch.float32, "dbias", shape=(N,))
+    _check("dmoe_linear_backward", lib().dmoe_linear_backward(
+        dyp, lddy, fp, xp, ldx, wp, kp, M, K, N, dxp, dwp, f32, _ptr(dbias), _ptr(ws), nws, _stream(stream)))
 
 
 # ----------------------------------------------------------------- whole layer

@@ -605,6 +605,138 @@ size_t dmoe_clip_grad_norm_workspace_size(void);
 dmoe_status dmoe_clip_grad_norm(const dmoe_grad* grads, int n, int64_t chunks, float max_norm, float eps, float* norm,
                                 void* ws, size_t ws_bytes, dmoe_stream_t stream);
 
+/* ============================================================================
+ * What makes the layer a block of a model: routing with a bias for balance,
+ * the norms before and after the block, and the dense products of a shared
+ * expert beside the routed ones. */
+
+/* ------------------------------------------------------- balanced routing */
+
+typedef enum dmoe_scores { DMOE_SCORES_SOFTMAX = 0, DMOE_SCORES_SIGMOID = 1 } dmoe_scores;
+
+/* For every token, with z its logits and s = softmax(z) or sigmoid(z):
+ *   c_e  = s_e + bias_e (bias NULL: the experts are ordered by z_e)
+ *   the E experts lie in `groups` groups of E / groups neighbours; a group's
+ *   worth is the sum of its two largest s_e + bias_e (of one, where it has no
+ *   more); the `top_groups` groups of most worth stay
+ *   expert_idx = the k experts of those groups with the largest c, descending
+ *   gate_w     = their s (the bias only chooses), divided by their sum when
+ *                renormalize != 0, times scale
+ * Equal ones go to the lower expert, or group.  The choice is that of the
+ * formulas in 64 bits: where fp32 cannot tell two candidates apart they are
+ * compared in 64.  A logit of NaN counts as minus infinity, plus infinity as
+ * the largest number; an expert whose logit (or bias) is minus infinity adds
+ * nothing to its group's worth, comes after all others and, by its logit, has
+ * the weight 0.  Where every chosen logit is minus infinity the weights are 0.
+ *   logits [T, E] fp32, bias [E] fp32 or NULL (read)
+ *   expert_idx [T, k] int32, gate_w [T, k] fp32 (written)
+ * 1 <= E <= 1024, 1 <= groups <= 32 a divisor of E, 1 <= top_groups <= groups,
+ * 1 <= k <= top_groups * E / groups. */
+dmoe_status dmoe_route_balanced(const float* logits, const float* bias, int T, int E, int k, int scores, int groups,
+                                int top_groups, int renormalize, float scale, int32_t* expert_idx, float* gate_w,
+                                dmoe_stream_t stream);
+
+/* Gradient of dmoe_route_balanced's weights with respect to the logits (the
+ * chosen set is locally constant, and the bias has no gradient).  expert_idx
+ * [T, k] holds distinct experts; an entry outside [0, E) is left out and sets
+ * DMOE_SITE_ROUTE_INDEX | DMOE_ERR_DEVICE.  scores, renormalize and scale as
+ * in the forward call.  d_gate [T, k], d_logits [T, E] fp32 (written). */
+dmoe_status dmoe_route_balanced_backward(const float* logits, const int32_t* expert_idx, const float* d_gate, int T,
+                                         int E, int k, int scores, int renormalize, float scale, float* d_logits,
+                                         dmoe_stream_t stream);
+
+/* bias_e += rate * sign(mean load - load_e), with the loads of one step:
+ * experts that got few tokens get more of the next.  tokens_per_expert [E]
+ * int32 as dmoe_permute_pad writes it, bias [E] fp32 (updated).  E <= 1024. */
+dmoe_status dmoe_balance_bias(float* bias, const int32_t* tokens_per_expert, int E, float rate, dmoe_stream_t stream);
+
+/* ------------------------------ the norms after a block and before the next */
+
+/* For every row t of T, with u the block's output and residual the stream:
+ *   n = u * ru * w_post,   ru = 1 / sqrt(mean_c u^2 + eps)
+ *   h = bf16(scale * residual + gate * n)
+ *   y = h * rh * w_pre,    rh = 1 / sqrt(mean_c h^2 + eps)
+ * The stream is kept in bf16 and its norm reads the kept value.  gate fp32:
+ * one a row (gate_rows == T), one for all (gate_rows == 1), or NULL for 1.
+ *   u, residual [T, d] bf16, rows ldu, ldr elements apart (at least d,
+ *   multiples of 8); w_post, w_pre [d] bf16, or fp32 when weight_f32 != 0
+ *   h, y [T, d] bf16 (written; each may be u or residual if that one's rows
+ *   lie d apart, else refused; not the same one)
+ *   rstd_u, rstd_h [T] fp32: ru and rh, what the backward reads (may be NULL)
+ * d a multiple of 8, 8 <= d <= 16384; eps >= 0. */
+dmoe_status dmoe_sandwich_norm(const uint16_t* u, int64_t ldu, const uint16_t* residual, int64_t ldr,
+                               const void* w_post, const void* w_pre, int weight_f32, const float* gate, int gate_rows,
+                               float scale, float eps, int T, int d, uint16_t* h, uint16_t* y, float* rstd_u,
+                               float* rstd_h, dmoe_stream_t stream);
+
+/* Bytes of scratch dmoe_sandwich_norm_backward needs on the current device
+ * for its sums over the rows, with T rows or fewer. */
+size_t dmoe_sandwich_norm_backward_workspace_size(int T, int d);
+
+/* Backward of dmoe_sandwich_norm: with g = dy * w_pre and
+ *   dH = dh + rh (g - h rh^2 mean(g h))     (dh, the gradient that arrives at h
+ *                                            from further on, may be NULL: 0)
+ *   dx       = scale dH                              (of residual)
+ *   du       = gate ru (w_post dH - u ru^2 mean(w_post dH u))
+ *   d_gate_t = ru sum_c w_post dH u                  (their sum when gate_rows == 1)
+ *   dw_post  = sum_t gate ru dH u,   dw_pre = sum_t rh dy h
+ * dy, u, dh may have rows lddy, ldu, lddh elements apart; du and dx [T, d]
+ * bf16 may each be dy, u, h or dh, if that one's rows lie d apart, but not
+ * the same one.  dw_post, dw_pre [d] and d_gate fp32 may each be NULL (all of
+ * them, or all but a d_gate of T rows: ws too); they are written, not added
+ * to, and summed in a fixed order.  T == 0 writes zeros to them.  Calls
+ * sharing a ws must not overlap. */
+dmoe_status dmoe_sandwich_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* u, int64_t ldu,
+                                        const uint16_t* h, const void* w_post, const void* w_pre, int weight_f32,
+                                        const float* gate, int gate_rows, float scale, const float* rstd_u,
+                                        const float* rstd_h, const uint16_t* dh, int64_t lddh, int T, int d,
+                                        uint16_t* du, uint16_t* dx, float* dw_post, float* dw_pre, float* d_gate,
+                                        void* ws, size_t ws_bytes, dmoe_stream_t stream);
+
+/* ------------------------------------------------------------- dense linear */
+
+typedef enum dmoe_act { DMOE_ACT_NONE = 0, DMOE_ACT_GELU = 1, DMOE_ACT_SILU = 2 } dmoe_act;
+
+/* Bytes of scratch dmoe_linear needs for M rows or fewer: the fp32 sums of
+ * products cut along K, at most 40 MB. */
+size_t dmoe_linear_workspace_size(int M, int K, int N);
+
+/* z = x w + bias,  y = bf16(act(z) + residual),  deriv = bf16(act'(z))
+ * with products of bf16 values summed in fp32 on the tensor cores (which
+ * truncate where they add) and everything up to y in fp32.  gelu is the exact
+ * erf form.
+ *   x [M, K] bf16, rows ldx apart; w [K, N] bf16; bias [N] bf16, or fp32 when
+ *   bias_f32 != 0, or NULL; residual [M, N] bf16, rows ldr apart, or NULL
+ *   y [M, N] bf16 (may be residual, if its rows lie N apart; overlaps nothing
+ *   else); deriv [M, N] bf16: what the backward reads (NULL: not kept; needs
+ *   an activation)
+ * K and N multiples of 8, ldx and ldr too.  Calls sharing a ws must not
+ * overlap. */
+dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t* w, const void* bias, int bias_f32, int act,
+                        const uint16_t* residual, int64_t ldr, int M, int K, int N, uint16_t* y, uint16_t* deriv,
+                        void* ws, size_t ws_bytes, dmoe_stream_t stream);
+
+/* Bytes of scratch dmoe_linear_backward needs for M rows or fewer: M * N * 2 for
+ * dz, and sums of at most 80 MB. */
+size_t dmoe_linear_backward_workspace_size(int M, int K, int N);
+
+/* Backward of dmoe_linear: with dz = bf16(dy * deriv) (dy where deriv is NULL),
+ *   dx = bf16((dz w^T) * factor),  dw = x^T dz,  dbias = sum_t dy * deriv
+ * The residual's gradient is dy itself.  factor [M, K] bf16 (NULL: 1) is the
+ * deriv of the layer that made x: with it dx is that layer's dz already, to be
+ * given to its backward as dy with deriv NULL.
+ *   dy [M, N] bf16, rows lddy apart; deriv [M, N] or NULL; x [M, K], rows ldx
+ *   apart (for dw alone); w [K, N] (for dx alone)
+ *   dx [M, K] bf16, dw [K, N] bf16, or fp32 when dw_f32 != 0, dbias [N] fp32:
+ *   each may be NULL; written, not added to; dx may be factor, otherwise they
+ *   overlap nothing
+ * M == 0 writes zeros to dw and dbias.  Sums run in a fixed order.  Calls
+ * sharing a ws must not overlap. */
+dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, const uint16_t* deriv, const uint16_t* x,
+                                 int64_t ldx, const uint16_t* w, const uint16_t* factor, int M, int K, int N,
+                                 uint16_t* dx, void* dw, int dw_f32, float* dbias, void* ws, size_t ws_bytes,
+                                 dmoe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
