@@ -121,25 +121,73 @@ struct Back {
   int32_t* err;
 };
 
+// Eight bf16 values as four pairs.
+__device__ __forceinline__ void unpack4(const uint4& u, float2* f) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __bfloat1622float2(h[i]);
+}
+
+__device__ __forceinline__ uint4 pack4(const float2* f) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(f[i]);
+  return u;
+}
+
+template <bool WF32>
+__device__ __forceinline__ void load_w4(const void* w, int v, float2* f) {
+  float a[8];
+  load_w<WF32>(w, v, a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(a[2 * i], a[2 * i + 1]);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The sums of s[0..2] over a warp: of s[q] in lanes 8 q .. 8 q + 7.  Lanes
+// that part with half of the sums at a step send fewer numbers than three sums
+// of their own would: 6 exchanges instead of 15.
+__device__ __forceinline__ float three_sums(const float* s, int lane) {
+  const bool high = lane & 16;
+  // the upper half keeps s[2], the lower one s[0] and s[1]
+  const float x = __shfl_xor_sync(0xffffffffu, high ? s[0] : s[2], 16);
+  const float y = __shfl_xor_sync(0xffffffffu, high ? s[1] : 0.f, 16);
+  const float k0 = (high ? s[2] : s[0]) + x, k1 = (high ? 0.f : s[1]) + y;
+  const bool odd = lane & 8;
+  float k = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+  return k;
+}
+
 // A persistent block walks units of RPB rows, dealt round-robin; a ring of
 // `stages` units of dy, u, h and dh is filled ahead by bulk copies, one per
-// row and tensor.  Every thread keeps its columns' sums of both weights'
-// gradients over its rows; a block's row groups meet in shared memory, and the
+// row and tensor, and read twice from there: before the row's sums and after.
+// Every thread keeps its columns of both weights (up to two vectors) and of
+// both weights' gradients; a block's row groups meet in shared memory, and the
 // block writes one fp32 row of `partial`.
+// Instructions come close to being the bound: pairs of values an instruction,
+// and two vectors a thread, so that the sums' meeting costs a quarter of them
+// (8192 x 4096: 99 us with one vector and value by value).
 template <int TPR, int VPT, bool WF32>
 __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackThreads / (TPR > kMinThreads ? TPR : kMinThreads))
-    sandwich_norm_backward_kernel(const Back p) {
+    sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
   using namespace dmoe::tc;
+  using dmoe::f2_fma;
+  using dmoe::f2_mul;
   constexpr int BLOCK = TPR > kMinThreads ? TPR : kMinThreads;
   constexpr int RPB = BLOCK / TPR;
   constexpr int WPR = TPR / 32;
-  constexpr bool KEEP = VPT == 1;  // the row between its sums and their use, and the weights, in registers
-  __shared__ float4 red[2][BLOCK / 32];
+  constexpr bool KEEP = VPT <= 2;  // the weights in registers
+  __shared__ float red[2][BLOCK / 32 * 4];
   __shared__ uint64_t full[kMaxStages];
   __shared__ int gave_up;
   extern __shared__ __align__(16) uint8_t ring[];  // [stages][dy, u, h, dh][RPB][d], then reused for the weights' sums
   const int c = threadIdx.x % TPR;
   const int rg = threadIdx.x / TPR;
+  const int lane = threadIdx.x & 31;
   const int d = p.d, nvec = d >> 3;
   const uint32_t row_bytes = static_cast<uint32_t>(d) * 2;
   const uint32_t part_bytes = RPB * row_bytes;
@@ -152,23 +200,29 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
   __syncthreads();
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  float wa[KEEP ? 8 : 1], wb[KEEP ? 8 : 1];
-  float da[VPT][8] = {}, db[VPT][8] = {};
-  if (KEEP) {
+  float2 wa[KEEP ? VPT : 1][4], wb[KEEP ? VPT : 1][4];
+  float2 da[VPT][4], db[VPT][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wa[j] = wb[j] = 0.f;
-    if (c < nvec) {
-      load_w<WF32>(p.w_post, c, wa);
-      load_w<WF32>(p.w_pre, c, wb);
-    }
-  }
-  auto weights = [&](int v, float* a, float* b) {
+  for (int i = 0; i < VPT; ++i) {
+    const int v = c + i * TPR;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) da[i][j] = db[i][j] = both(0.f);
     if (KEEP) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = wa[j], b[j] = wb[j];
+      for (int j = 0; j < 4; ++j) wa[i][j] = wb[i][j] = both(0.f);
+      if (v < nvec) {
+        load_w4<WF32>(p.w_post, v, wa[i]);
+        load_w4<WF32>(p.w_pre, v, wb[i]);
+      }
+    }
+  }
+  auto weights = [&](int i, float2* a, float2* b) {
+    if (KEEP) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = wa[KEEP ? i : 0][j], b[j] = wb[KEEP ? i : 0][j];
     } else {
-      load_w<WF32>(p.w_post, v, a);
-      load_w<WF32>(p.w_pre, v, b);
+      load_w4<WF32>(p.w_post, c + i * TPR, a);
+      load_w4<WF32>(p.w_pre, c + i * TPR, b);
     }
   };
   // thread 0: the rows of unit n into stage s
@@ -200,90 +254,76 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
     if (!mbar_wait(full + stage, phase, &gave_up)) gave_up = 1;
     const uint4* at = reinterpret_cast<const uint4*>(ring + stage * 4 * part_bytes + rg * row_bytes);
     const int next = RPB * nvec;  // from one tensor's rows to the next one's
-    uint4 q[KEEP ? 4 : 1];        // the row's dy, u, h and dh, kept packed
-    float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
-      if (KEEP) q[0] = q[KEEP ? 1 : 0] = q[KEEP ? 2 : 0] = q[KEEP ? 3 : 0] = make_uint4(0, 0, 0, 0);
       if (!live || v >= nvec) continue;
-      const uint4 q0 = at[v], q1 = at[next + v], q2 = at[2 * next + v];
-      const uint4 q3 = p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0);
-      if (KEEP) q[0] = q0, q[KEEP ? 1 : 0] = q1, q[KEEP ? 2 : 0] = q2, q[KEEP ? 3 : 0] = q3;
-      float f[8], g[8], w[8], o[8], a[8], b[8];
-      unpack8(q0, f);
-      unpack8(q1, g);
-      unpack8(q2, w);
-      unpack8(q3, o);
-      weights(v, a, b);
+      float2 f[4], g[4], w[4], o[4], a[4], b[4];
+      unpack4(at[v], f);
+      unpack4(at[next + v], g);
+      unpack4(at[2 * next + v], w);
+      unpack4(p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0), o);
+      weights(i, a, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gy = f[j] * b[j], au = a[j] * g[j];
-        s1 = fmaf(gy, w[j], s1);
-        s2 = fmaf(au, fmaf(rh, gy, o[j]), s2);
-        s3 = fmaf(au, w[j], s3);
+      for (int j = 0; j < 4; ++j) {
+        const float2 gy = f2_mul(f[j], b[j]), au = f2_mul(a[j], g[j]);
+        s1 = f2_fma(gy, w[j], s1);
+        s2 = f2_fma(au, f2_fma(both(rh), gy, o[j]), s2);
+        s3 = f2_fma(au, w[j], s3);
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-      s3 += __shfl_xor_sync(0xffffffffu, s3, o);
-    }
+    const float part[3] = {s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
+    float sum = three_sums(part, lane);  // of number lane / 8
     if (WPR > 1) {
-      if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = make_float4(s1, s2, s3, 0.f);
+      // sum q of warp w at 4 w + q; each lane brings together those of one q
+      if ((lane & 7) == 0) red[flip][(threadIdx.x >> 5) * 4 + (lane >> 3)] = sum;
       __syncthreads();
-      s1 = s2 = s3 = 0.f;
+      const float* r = red[flip] + rg * WPR * 4;
+      if (WPR >= 8) {
+        sum = r[lane];
 #pragma unroll
-      for (int i = 0; i < WPR; ++i) {
-        const float4 r = red[flip][rg * WPR + i];
-        s1 += r.x, s2 += r.y, s3 += r.z;
+        for (int k = 1; k < WPR / 8; ++k) sum += r[lane + 32 * k];
+      } else {
+        sum = lane < 4 * WPR ? r[lane] : 0.f;
       }
+#pragma unroll
+      for (int o = 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     } else {
       __syncthreads();
     }
+    const int span = WPR > 1 ? 1 : 8;  // lanes from one sum to the next
+    const float t1 = __shfl_sync(0xffffffffu, sum, 0), t2 = __shfl_sync(0xffffffffu, sum, span),
+                t3 = __shfl_sync(0xffffffffu, sum, 2 * span);
     if (gave_up) break;
     // past this barrier every thread is done with the unit before this one
     if (p.stages > 1 && threadIdx.x == 0 && n != static_cast<int64_t>(blockIdx.x))
       fill(n + static_cast<int64_t>(p.stages - 1) * gridDim.x, stage == 0 ? p.stages - 1 : stage - 1);
-    const float m1 = s1 * per * rh * rh;                    // dH = dh + rh (g - h m1)
-    const float along = ru * fmaf(-rh * m1, s3, s2);        // sum a dH u ru
-    const float m2 = along * per * ru;                      // du = gate ru (a dH - u m2)
+    const float m1 = t1 * per * rh * rh;              // dH = dh + rh (g - h m1)
+    const float along = ru * fmaf(-rh * m1, t3, t2);  // sum a dH u ru
+    const float m2 = along * per * ru;                // du = gate ru (a dH - u m2)
     if (live && c == 0 && p.d_gate) p.d_gate[t] = along;
+    const float gr = gt * ru;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
       if (!live || v >= nvec) continue;
-      float f[8], g[8], w[8], o[8], a[8], b[8];
-      if (KEEP) {
-        // unpacked anew (the compiler would carry 32 floats over the barrier instead)
+      float2 f[4], g[4], w[4], o[4], a[4], b[4];
+      unpack4(at[v], f);
+      unpack4(at[next + v], g);
+      unpack4(at[2 * next + v], w);
+      unpack4(p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0), o);
+      weights(i, a, b);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm volatile("" : "+r"(q[KEEP ? k : 0].x), "+r"(q[KEEP ? k : 0].y), "+r"(q[KEEP ? k : 0].z),
-                       "+r"(q[KEEP ? k : 0].w));
-        unpack8(q[0], f);
-        unpack8(q[KEEP ? 1 : 0], g);
-        unpack8(q[KEEP ? 2 : 0], w);
-        unpack8(q[KEEP ? 3 : 0], o);
-      } else {
-        unpack8(at[v], f);
-        unpack8(at[next + v], g);
-        unpack8(at[2 * next + v], w);
-        unpack8(p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0), o);
+      for (int j = 0; j < 4; ++j) {
+        const float2 dH = f2_fma(both(rh), f2_fma(f[j], b[j], f2_mul(w[j], both(-m1))), o[j]);
+        db[i][j] = f2_fma(f2_mul(f[j], both(rh)), w[j], db[i][j]);
+        da[i][j] = f2_fma(f2_mul(dH, both(gr)), g[j], da[i][j]);
+        f[j] = f2_mul(f2_fma(a[j], dH, f2_mul(g[j], both(-m2))), both(gr));
+        o[j] = f2_mul(dH, both(p.scale));
       }
-      weights(v, a, b);
-      const float gr = gt * ru;
-      float du[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dH = fmaf(rh, fmaf(f[j], b[j], -w[j] * m1), o[j]);
-        db[i][j] = fmaf(f[j] * rh, w[j], db[i][j]);
-        da[i][j] = fmaf(dH * gr, g[j], da[i][j]);
-        du[j] = gr * fmaf(a[j], dH, -g[j] * m2);
-        o[j] = p.scale * dH;
-      }
-      *(reinterpret_cast<uint4*>(p.du + t * d) + v) = pack8(du);
-      *(reinterpret_cast<uint4*>(p.dx + t * d) + v) = pack8(o);
+      *(reinterpret_cast<uint4*>(p.du + t * d) + v) = pack4(f);
+      *(reinterpret_cast<uint4*>(p.dx + t * d) + v) = pack4(o);
     }
     if (p.stages == 1) {
       __syncthreads();
@@ -312,14 +352,15 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
   }
   if (!p.partial) return;
   if (RPB > 1) {
-    float* sh = reinterpret_cast<float*>(ring);  // [RPB - 1][2 d]: every unit has been read
+    float2* sh = reinterpret_cast<float2*>(ring);  // [RPB - 1][2 d] floats: every unit has been read
+    if (rg > 0) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = c + i * TPR;
-      if (rg > 0 && v < nvec) {
-        float* o = sh + static_cast<int64_t>(rg - 1) * 2 * d + 8 * v;
+      for (int i = 0; i < VPT; ++i) {
+        const int v = c + i * TPR;
+        if (v >= nvec) continue;
+        float2* o = sh + static_cast<int64_t>(rg - 1) * d + 4 * v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = da[i][j], o[d + j] = db[i][j];
+        for (int j = 0; j < 4; ++j) o[j] = da[i][j], o[d / 2 + j] = db[i][j];
       }
     }
     __syncthreads();
@@ -329,9 +370,12 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
         const int v = c + i * TPR;
         if (v >= nvec) continue;
         for (int g = 1; g < RPB; ++g) {
-          const float* o = sh + static_cast<int64_t>(g - 1) * 2 * d + 8 * v;
+          const float2* o = sh + static_cast<int64_t>(g - 1) * d + 4 * v;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) da[i][j] += o[j], db[i][j] += o[d + j];
+          for (int j = 0; j < 4; ++j) {
+            da[i][j] = dmoe::f2_add(da[i][j], o[j]);
+            db[i][j] = dmoe::f2_add(db[i][j], o[d / 2 + j]);
+          }
         }
       }
     }
@@ -343,9 +387,9 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
       if (v >= nvec) continue;
       float* o = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * d + 8 * v;
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        *reinterpret_cast<float4*>(o + j) = make_float4(da[i][j], da[i][j + 1], da[i][j + 2], da[i][j + 3]);
-        *reinterpret_cast<float4*>(o + d + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+      for (int j = 0; j < 4; j += 2) {
+        *reinterpret_cast<float4*>(o + 2 * j) = make_float4(da[i][j].x, da[i][j].y, da[i][j + 1].x, da[i][j + 1].y);
+        *reinterpret_cast<float4*>(o + d + 2 * j) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
       }
     }
   }
@@ -395,32 +439,27 @@ __global__ void __launch_bounds__(1024) sandwich_sums_kernel(const float* __rest
   }
 }
 
-// Threads per row, forward: the smallest power of two that holds it at two
-// vectors a thread (four above 8192 columns); backward: at one vector, which
-// leaves room for both weights' sums (two and four above 4096 and 8192).
-int threads_per_row(int d, int vectors) {
+// Threads per row: the smallest power of two from 32 on that holds it at two
+// vectors a thread; above 8192 columns at four.
+int threads_per_row(int d) {
   int tpr = 32;
-  while (tpr < 512 && vectors * tpr < (d >> 3)) tpr *= 2;
+  while (tpr < 512 && 2 * tpr < (d >> 3)) tpr *= 2;
   return tpr;
 }
 
 template <typename F>
 cudaError_t by_width(int d, const F& f) {
-  const int nvec = d >> 3;
-  switch (threads_per_row(d, F::kVectors)) {
-    case 32: return f.template operator()<32, F::kVectors>();
-    case 64: return f.template operator()<64, F::kVectors>();
-    case 128: return f.template operator()<128, F::kVectors>();
-    case 256: return f.template operator()<256, F::kVectors>();
-    default:
-      if (nvec <= 512 * F::kVectors) return f.template operator()<512, F::kVectors>();
-      if (nvec <= 1024) return f.template operator()<512, 2>();
-      return f.template operator()<512, 4>();
+  switch (threads_per_row(d)) {
+    case 32: return f.template operator()<32, 2>();
+    case 64: return f.template operator()<64, 2>();
+    case 128: return f.template operator()<128, 2>();
+    case 256: return f.template operator()<256, 2>();
+    default: return (d >> 3) <= 1024 ? f.template operator()<512, 2>() : f.template operator()<512, 4>();
   }
 }
 
-int back_block(int d) { return std::max(kMinThreads, threads_per_row(d, 1)); }
-int back_rows(int d) { return back_block(d) / threads_per_row(d, 1); }
+int back_block(int d) { return std::max(kMinThreads, threads_per_row(d)); }
+int back_rows(int d) { return back_block(d) / threads_per_row(d); }
 size_t unit_bytes(int d) { return static_cast<size_t>(back_rows(d)) * d * 2 * 4; }
 int blocks_per_sm(int d) { return kBackThreads / back_block(d); }
 int ring_stages(int d) {
@@ -435,7 +474,6 @@ int backward_blocks(int T, int d, int sms) {
 }
 
 struct Forward {
-  static constexpr int kVectors = 2;
   const uint16_t* u;
   int64_t ldu;
   const uint16_t* x;
@@ -462,7 +500,6 @@ struct Forward {
 };
 
 struct Backward {
-  static constexpr int kVectors = 1;
   Back p;
   int wf32;
   int blocks;
