@@ -6,26 +6,36 @@
 //   a group's worth: its two largest c summed; the best groups stay
 //   of their experts the k largest c;  w = s (/ their sum) * scale
 //
-// One warp per token, the row of logits in registers (lane l: experts l, l +
-// 32, ...).  A round of the top-k is two integer reductions over the warp:
-// the largest of order-preserving keys, and the lowest expert that has it.
+// One warp per token, lane l with experts l, l + 32, ....  16381 tokens of 256
+// experts are 17 MB, 3 us of HBM: what bounds it are instructions, so the
+// choice works on 31-bit keys, a choice's place in its range and under it the
+// expert's register, such that one integer reduction over the warp finds the
+// best and where it lies.
 //
-// Which experts are chosen must not hang on how fp32 rounds s + bias: c is
-// known to `tol`, and where two neighbours of the descending order (or the
-// last group that stays and the first that goes) are closer than that, the
-// token is decided again by c in 64 bits, of those candidates alone.  With
-// 256 sigmoid scores that is one token in some hundred.  Without a bias the
-// order is that of the logits, which is exact.
+// Which experts are chosen must not hang on how the keys, or fp32, round: a
+// key is known to `tol` steps, and a token where two neighbours of the
+// descending order (or the last group that stays and the first that goes) are
+// closer than that is decided again by c in 64 bits, of those that come into
+// question alone.  With 256 sigmoid scores that is one token in a thousand;
+// what it takes, some microseconds, is the fetching of code that was not run
+// before, so that code is small and one (all of a token's scores in 64 bits,
+// everything inlined: 50 us).
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
+
+#include "act.cuh"
 #include "common.cuh"
 
 namespace {
 
+using namespace dmoe::act;
+
 constexpr int kWarps = 8;  // tokens per block
 constexpr int kMaxGroups = 32;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kLog2e = 1.44269504088896341f;
 
 // Larger key, larger number; 0 is below every number's.
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -53,7 +63,7 @@ __device__ __forceinline__ float warp_max(float v) { return float_of(__reduce_ma
 
 // NaN counts as minus infinity, which no score comes of; plus infinity as the
 // largest number.
-__device__ __forceinline__ float clean(float z) { return isnan(z) ? -INFINITY : fminf(z, FLT_MAX); }
+__device__ __forceinline__ float clean(float z) { return fminf(fmaxf(z, -INFINITY), FLT_MAX); }
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
@@ -79,24 +89,18 @@ struct Choice {
   float* gate_w;
 };
 
-// c in 64 bits; m, total: the softmax's reference and sum.
-__device__ double exact_choice(float z, float b, bool sig, float m, double total) {
-  if (z == -INFINITY) return -INFINITY;
-  const double s = sig ? 1.0 / (1.0 + exp(-static_cast<double>(z))) : exp(static_cast<double>(z) - m) / total;
-  const double c = s + b;
-  return isnan(c) ? -INFINITY : c;
-}
+__device__ __forceinline__ float lower(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ float upper(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double lower(double a, double b) { return a < b ? a : b; }
+__device__ __forceinline__ double upper(double a, double b) { return a > b ? a : b; }
 
 template <class F>
 __device__ __forceinline__ void top_two(F a, F& first, F& second) {
-  if (a > first) {
-    second = first;
-    first = a;
-  } else if (a > second) {
-    second = a;
-  }
+  second = upper(second, lower(first, a));
+  first = upper(first, a);
 }
 
+// Of the lanes that share a group, `lanes` neighbours (a power of two).
 template <class F>
 __device__ __forceinline__ F group_worth(F first, F second, int lanes) {
   for (int o = 1; o < lanes; o <<= 1) {
@@ -108,6 +112,7 @@ __device__ __forceinline__ F group_worth(F first, F second, int lanes) {
 }
 
 // How many of the groups (one every `lanes` lanes) are better than this lane's.
+// Every lane of the warp takes part.
 template <class F>
 __device__ __forceinline__ int group_rank(F worth, int g, int groups, int lanes) {
   int rank = 0;
@@ -118,247 +123,301 @@ __device__ __forceinline__ int group_rank(F worth, int g, int groups, int lanes)
   return rank;
 }
 
-template <int NPL, bool GROUPS>
-__global__ void __launch_bounds__(kWarps * 32) route_balanced_kernel(const Choice p) {
+// c in 64 bits; m and total: the softmax's reference and sum.
+__device__ __noinline__ double exact_choice(float z, float b, int sig, float m, double total) {
+  if (z == -INFINITY) return -INFINITY;
+  const double e = exp(sig ? -static_cast<double>(z) : static_cast<double>(z) - m);
+  const double c = (sig ? 1.0 : e) / (sig ? 1.0 + e : total) + b;
+  return isnan(c) ? -static_cast<double>(INFINITY) : c;
+}
+
+// The softmax's sum in 64 bits.
+__device__ __noinline__ double exact_total(const float* row, int E, int lane, float m) {
+  double sum = 0.0;
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float z = clean(row[e]);
+    if (z > -INFINITY) sum += exp(static_cast<double>(z) - m);
+  }
+  return warp_sum(sum);
+}
+
+// The whole choice by the definition, in 64 bits, where more than a warp's
+// lanes come into question: slot j's expert from lane j mod 32.
+__device__ __noinline__ void choose_exactly(const Choice& p, const float* row, int lane, float m, int32_t* out_i) {
+  const int n = (p.E + 31) >> 5;
+  double c[32];
+  const double total = p.sig ? 1.0 : exact_total(row, p.E, lane, m);
+  for (int i = 0; i < n; ++i) c[i] = i * 32 + lane < p.E ? clean(row[i * 32 + lane]) : -INFINITY;
+  uint32_t left = 0;  // of this lane's experts
+  for (int i = 0; i < n; ++i)
+    if (i * 32 + lane < p.E) left |= 1u << i;
+  const bool groups = p.top_groups < p.groups;
+  auto choice = [&](int i) {
+    return exact_choice(static_cast<float>(c[i]), p.bias ? p.bias[i * 32 + lane] : 0.f, p.sig, m, total);
+  };
+  if (p.bias)  // else the logits order the experts, and the scores the groups
+    for (int i = 0; i < n; ++i)
+      if ((left >> i) & 1u) c[i] = choice(i);
+  if (groups) {
+    double worth = -INFINITY;  // of group `lane`
+    for (int g = 0; g < p.groups; ++g) {
+      double first = -INFINITY, second = -INFINITY;
+      for (int i = 0; i < n; ++i)
+        if (((left >> i) & 1u) && (i * 32 + lane) / p.size == g) top_two(p.bias ? c[i] : choice(i), first, second);
+      const double w = group_worth(first, second, 32);
+      if (lane == g) worth = w;
+    }
+    const int rank = group_rank(worth, lane, p.groups, 1);
+    const uint32_t stay = __ballot_sync(kFull, rank < p.top_groups && lane < p.groups);
+    for (int i = 0; i < n; ++i) {
+      const int e = i * 32 + lane;
+      if (e < p.E && !((stay >> (e / p.size)) & 1u)) left &= ~(1u << i);
+    }
+  }
+  for (int j = 0; j < p.k; ++j) {
+    double top = -INFINITY;
+    int at = 0x7fffffff;
+    for (int i = 0; i < n; ++i)
+      if (((left >> i) & 1u) && (at == 0x7fffffff || c[i] > top)) top = c[i], at = i * 32 + lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double v = __shfl_xor_sync(kFull, top, o);
+      const int q = __shfl_xor_sync(kFull, at, o);
+      if (q != 0x7fffffff && (at == 0x7fffffff || v > top || (v == top && q < at))) top = v, at = q;
+    }
+    if ((at & 31) == lane) left &= ~(1u << (at >> 5));
+    if (lane == (j & 31)) out_i[j] = at;
+  }
+}
+
+// A choice's key: its place v in [1, 2], whose 23 bits of fraction are steps of
+// the range, above the register i that holds it (a lower one is the larger
+// key).  Minus infinity is below all numbers; 0 is no expert.
+constexpr uint32_t kMasked = 1u << 5;
+__device__ __forceinline__ uint32_t pack(float v, int i) {
+  return ((__float_as_uint(v) - 0x3f800000u + 2u) << 5) + (31 - i);
+}
+
+// A warp walks its tokens with the bias in registers.  FULL: E is 32 NPL.
+template <int NPL, bool GROUPS, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
+    route_balanced_kernel(const __grid_constant__ Choice p) {
   extern __shared__ float group_mem[];  // [kWarps][groups * stride]
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const float* row = p.logits + t * p.E;
-  const bool sig = p.sig;
-  float z[NPL];
+  const bool sig = p.sig, biased = p.bias != nullptr;
+  auto there = [&](int i) { return FULL || i * 32 + lane < p.E; };
+  float b[NPL], most = 0.f;  // the largest finite bias, in magnitude
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    z[i] = e < p.E ? __ldg(row + e) : -INFINITY;
+    b[i] = biased && there(i) ? __ldg(p.bias + i * 32 + lane) : 0.f;
+    most = fmaxf(most, fabsf(b[i]) < INFINITY ? fabsf(b[i]) : 0.f);
   }
-  float m = -INFINITY;
+  most = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
+  // Steps that two keys may be off by together.  Without a bias: places by the
+  // logit's distance from the largest, monotone, so only equal ones are open.
+  // With one, in steps of 2^-22 of the range: a sigmoid is off by 1 (its
+  // exponential's argument, ex2 and rcp to 2^-22.5 and 2^-23), the sum and its
+  // place by 0.7, for each of the two; a softmax also by its sum's roundings (a
+  // lane's NPL terms, five more, and its inverse).
+  const float open_steps = sig ? 6.f : 10.f + NPL / 4;
+  const uint32_t tol = (biased ? (sig ? 6u : 10u + NPL / 4) << 5 : 0u) + 31;
+
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
+       t += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const float* row = p.logits + t * p.E;
+    float z[NPL], m = -FLT_MAX;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    z[i] = clean(z[i]);
-    m = fmaxf(m, z[i]);
-  }
-  m = warp_max(m);
-  const bool scored = GROUPS || p.bias || (!sig && !p.renorm);  // else the logits alone decide and weigh
-  float inv = 1.f;  // of the softmax's sum
-  float s[NPL];
-  if (scored) {
-    float sum = 0.f;
+    for (int i = 0; i < NPL; ++i) z[i] = there(i) ? __ldg(row + i * 32 + lane) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      s[i] = z[i] == -INFINITY ? 0.f : sig ? sigmoid(z[i]) : expf(z[i] - m);
-      sum += s[i];
+      z[i] = clean(z[i]);
+      m = fmaxf(m, z[i]);
     }
-    if (!sig) {
-      sum = warp_sum(sum);
-      inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (!sig || !biased) m = warp_max(m);
+    float inv = 1.f;  // of the softmax's sum
+    uint32_t key[NPL];
+    float step = 0.f, s[NPL];
+    if (GROUPS || biased) {
+      if (sig) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) s[i] *= inv;
-    }
-  }
-
-  // choices; how far fp32 may be off between two of them: a score is off by
-  // 2^-22 (expf) and three roundings, a softmax also by its sum's roundings
-  // (in the worst case one for every term a lane adds, and five), s + bias
-  // by 2^-24 of itself; both sides counted
-  float b[NPL];
-  uint32_t key[NPL], alive = 0;
-  float tol = 0.f;
+        for (int i = 0; i < NPL; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
+      } else {
+        float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    b[i] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
-    if (e < p.E) alive |= 1u << i;
-  }
-  if (GROUPS || p.bias) {
-    float size = 0.f;
+        for (int i = 0; i < NPL; ++i) {
+          s[i] = ex2_approx((z[i] - m) * kLog2e);
+          sum += s[i];
+        }
+        sum = warp_sum(sum);
+        inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      size = fmaxf(size, s[i] + (fabsf(b[i]) < INFINITY ? fabsf(b[i]) : 0.f));
-      const float c = z[i] == -INFINITY ? -INFINITY : s[i] + b[i];
-      s[i] = isnan(c) ? -INFINITY : c;  // from here on the choice
-    }
-    tol = warp_max(size) * (8.f + (sig ? 0.f : 2.f * NPL + 10.f)) * 1.1920929e-7f;
-  }
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) key[i] = key_of(p.bias ? s[i] : z[i]);
-
-  double total = -1.0;  // the softmax's sum in 64 bits, once it is needed
-  auto need_total = [&]() {
-    if (sig || total >= 0.0) return;
-    total = 0.0;
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) {
-      const float v = clean(__ldg(row + e));
-      if (v > -INFINITY) total += exp(static_cast<double>(v) - m);
-    }
-    total = warp_sum(total);
-  };
-
-  if (GROUPS) {
-    float* mem = group_mem + (threadIdx.x >> 5) * p.groups * p.stride;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = i * 32 + lane;
-      const int g = static_cast<int>((e * p.inv_size) >> 20);
-      if (e < p.E) mem[g * p.stride + (e - g * p.size)] = s[i];
-    }
-    __syncwarp();
-    const int g = lane / p.lanes, r = lane & (p.lanes - 1);
-    float first = -INFINITY, second = -INFINITY;
-    if (g < p.groups)
-      for (int o = r; o < p.size; o += p.lanes) top_two(mem[g * p.stride + o], first, second);
-    const float worth = group_worth(first, second, p.lanes);
-    // every lane takes part in the ranks' shuffles, those of no group too
-    bool stays = group_rank(worth, g, p.groups, p.lanes) < p.top_groups;
-    stays = stays && g < p.groups;
-    // the worst that stays against the best that goes
-    const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
-    const float high = float_of(__reduce_max_sync(kFull, g < p.groups && !stays ? key_of(worth) : 0u));
-    if (low - high <= 2.f * tol) {
-      // rows whose experts are all alike (padding) need no digits
-      bool alike = true;
+        for (int i = 0; i < NPL; ++i) s[i] *= inv;
+      }
+      const float range = most + (sig ? 1.f : inv);  // a softmax's largest score is its largest exponential's, 1
+      step = range * 2.3841858e-7f;
+      const float half = 0.5f / range;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        const float z0 = __shfl_sync(kFull, z[0], 0), b0 = __shfl_sync(kFull, b[0], 0);
-        alike &= i * 32 + lane >= p.E || (z[i] == z0 && b[i] == b0);
+        s[i] = z[i] == -INFINITY ? -INFINITY : fmaxf(s[i] + b[i], -INFINITY);  // the choice; NaN is minus infinity
+        key[i] = s[i] == -INFINITY ? kMasked + (31 - i) : pack(fminf(fmaf(s[i], half, 1.5f), 2.f), i);
       }
-      if (!__all_sync(kFull, alike)) {
+    }
+    if (!biased) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        key[i] = z[i] == -INFINITY ? kMasked + (31 - i) : pack(fmaxf(fmaf(z[i] - m, 1.f / 32.f, 2.f), 1.f), i);
+    }
+    if (!FULL) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (!there(i)) key[i] = 0;
+    }
+
+    double total = -1.0;  // the softmax's sum in 64 bits, once it is needed
+    // Rows whose experts are all alike (padding) are in order already.
+    auto rows_alike = [&]() {
+      bool alike = true;
+      const float z0 = clean(__ldg(row)), b0 = biased ? __ldg(p.bias) : 0.f;
+#pragma unroll 1
+      for (int e = lane; e < p.E; e += 32) alike &= clean(__ldg(row + e)) == z0 && (!biased || __ldg(p.bias + e) == b0);
+      return __all_sync(kFull, alike) != 0;
+    };
+    auto exactly = [&](int e) {
+      return exact_choice(clean(__ldg(row + e)), biased ? __ldg(p.bias + e) : 0.f, sig, m, total);
+    };
+    auto need_total = [&]() {
+      if (!sig && total < 0.0) total = exact_total(row, p.E, lane, m);
+    };
+    if (GROUPS) {
+      float* mem = group_mem + (threadIdx.x >> 5) * p.groups * p.stride;
+      const int pad = p.stride - p.size;
+      int at[NPL];
+      __syncwarp();  // the last token's have been read
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int e = i * 32 + lane;
+        at[i] = static_cast<int>((e * p.inv_size) >> 20);
+        if (there(i)) mem[e + at[i] * pad] = s[i];
+      }
+      __syncwarp();
+      const int g = lane / p.lanes, r = lane & (p.lanes - 1);
+      const float* mine = mem + g * p.stride;
+      float first = -INFINITY, second = -INFINITY;
+      if (g < p.groups) {
+#pragma unroll 4
+        for (int o = r; o < p.size; o += p.lanes) top_two(mine[o], first, second);
+      }
+      const float worth = group_worth(first, second, p.lanes);
+      int rank = group_rank(worth, g, p.groups, p.lanes);
+      bool stays = rank < p.top_groups && g < p.groups;
+      // the worst that stays against the best that goes
+      const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
+      const float high = float_of(__reduce_max_sync(kFull, g < p.groups && !stays ? key_of(worth) : 0u));
+      const float open = open_steps * step;  // as far as two choices may be off
+      if (low - high <= 2.f * open && !rows_alike()) {
+        // the groups' two best in 64 bits: of those that may be among them
         need_total();
+        const float least = second - open;
         double f = -INFINITY, n = -INFINITY;
-        if (g < p.groups) {
-#pragma unroll 1
-          for (int o = r; o < p.size; o += p.lanes) {
-            const int e = g * p.size + o;
-            top_two(exact_choice(clean(__ldg(row + e)), p.bias ? __ldg(p.bias + e) : 0.f, sig, m, total), f, n);
+        int o = g < p.groups ? r : p.size;
+        for (;;) {
+          while (o < p.size && !(mine[o] >= least)) o += p.lanes;
+          if (!__any_sync(kFull, o < p.size)) break;
+          if (o < p.size) {
+            top_two(exactly(g * p.size + o), f, n);
+            o += p.lanes;
           }
         }
-        const double exact = group_worth(f, n, p.lanes);
-        stays = group_rank(exact, g, p.groups, p.lanes) < p.top_groups;
-        stays = stays && g < p.groups;
+        rank = group_rank(group_worth(f, n, p.lanes), g, p.groups, p.lanes);
+        stays = rank < p.top_groups && g < p.groups;
+      }
+      const uint32_t lanes_in = __ballot_sync(kFull, stays);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (!((lanes_in >> ((at[i] * p.lanes) & 31)) & 1u)) key[i] = 0;  // (past the last expert it is 0 already)
+    }
+
+    int32_t* out_i = p.expert_idx + t * p.k;
+    float* out_w = p.gate_w + t * p.k;
+    uint32_t own = 0;  // this lane's best
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) own = max(own, key[i]);
+    uint32_t last = kFull;
+    int mine = 0;  // slot `lane`'s expert
+    bool near = false;
+    int n = 0;  // slots taken: k, and those behind whose order with the last is open
+    for (;; ++n) {
+      const uint32_t best = __reduce_max_sync(kFull, own);
+      bool open = false;
+      if (last - best <= tol) {  // neighbours: their order is open (masked ones go by their number)
+        open = best >= 2 * kMasked;
+        near |= open;
+      }
+      if (n >= p.k && (!open || n >= 32)) break;
+      last = best;
+      const int src = __ffs(__ballot_sync(kFull, own == best)) - 1;  // equal keys: the lowest lane has the lowest expert
+      const int e = static_cast<int>(31 - (best & 31)) * 32 + src;
+      if (n < 32) mine = lane == n ? e : mine;
+      else if (lane == (n & 31)) out_i[n] = e;
+      if (lane == src) {  // its best below: of the differences that wrap the largest
+        uint32_t next = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
+        own = next & 0x80000000u ? next + best : 0u;
       }
     }
-    const uint32_t lanes_in = __ballot_sync(kFull, stays);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int e = i * 32 + lane;
-      const int ge = static_cast<int>((e * p.inv_size) >> 20);
-      if (e < p.E && !((lanes_in >> (ge * p.lanes)) & 1u)) alive &= ~(1u << i);
-    }
-  }
-
-  int32_t* out_i = p.expert_idx + t * p.k;
-  float* out_w = p.gate_w + t * p.k;
-  // the best of what is left: its key, and the lowest expert that has it
-  auto best_of = [&](uint32_t left, uint32_t& best) {
-    uint32_t own = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = NPL - 1; i >= 0; --i) {
-      const uint32_t v = (left >> i) & 1u ? key[i] : 0u;
-      if (v >= own) own = v, at = i;
-    }
-    best = __reduce_max_sync(kFull, own);
-    return static_cast<int>(__reduce_min_sync(kFull, own == best && own != 0 ? at * 32 + lane : 0x7fffffff));
-  };
-  uint32_t left = alive;
-  bool near = false;
-  float last = INFINITY;
-  int mine = 0;  // slot `lane`'s expert
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t best;
-    const int e = best_of(left, best);
-    if ((e & 31) == lane) left &= ~(1u << (e >> 5));
-    if (lane == (j & 31)) {
-      if (j < 32) mine = e;
-      else out_i[j] = e;
-    }
-    const float c = float_of(best);
-    near |= last - c <= tol;
-    last = c;
-  }
-  if (p.bias) {  // the first that is not chosen
-    uint32_t best;
-    best_of(left, best);
-    near |= best != 0 && last - float_of(best) <= tol;
-    if (near) {
-      left = alive;
+    if (near && !rows_alike()) {
+      if (n < 32) {  // one slot a lane: their order in 64 bits
+        if (biased) need_total();
+        double c = -INFINITY;
+        if (lane < n) c = biased ? exactly(mine) : static_cast<double>(clean(__ldg(row + mine)));
+        int rank = 0;
 #pragma unroll 1
-      for (int j = 0; j < p.k; ++j) {
-        uint32_t best;
-        int e = best_of(left, best);
-        const float least = float_of(best) - tol;
-        uint32_t close = 0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          if (((left >> i) & 1u) && s[i] >= least) close |= 1u << i;
-        const int n = static_cast<int>(__reduce_add_sync(kFull, static_cast<unsigned>(__popc(close))));
-        if (n > 1) {
-          // exactly alike: the lowest, as found
-          float ze = 0.f, be = 0.f;
-#pragma unroll
-          for (int i = 0; i < NPL; ++i)
-            if (i == (e >> 5)) ze = z[i], be = b[i];
-          ze = __shfl_sync(kFull, ze, e & 31);
-          be = __shfl_sync(kFull, be, e & 31);
-          bool alike = true;
-#pragma unroll
-          for (int i = 0; i < NPL; ++i) alike &= !((close >> i) & 1u) || (z[i] == ze && b[i] == be);
-          if (!__all_sync(kFull, alike)) {
-            need_total();
-            double top = -INFINITY;
-            int at = 0x7fffffff;
-#pragma unroll 1
-            for (int i = 0; i < NPL; ++i) {
-              if (!__any_sync(kFull, (close >> i) & 1u)) continue;
-              const int q = i * 32 + lane;
-              if ((close >> i) & 1u) {
-                const double c = exact_choice(clean(__ldg(row + q)), __ldg(p.bias + q), sig, m, total);
-                if (c > top || at == 0x7fffffff) top = c, at = q;
-              }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              const double c = __shfl_xor_sync(kFull, top, o);
-              const int q = __shfl_xor_sync(kFull, at, o);
-              if (q != 0x7fffffff && (at == 0x7fffffff || c > top || (c == top && q < at))) top = c, at = q;
-            }
-            e = at;
-          }
+        for (int j = 0; j < n; ++j) {
+          const double v = __shfl_sync(kFull, c, j);
+          const int e = __shfl_sync(kFull, mine, j);
+          rank += v > c || (v == c && e < mine);
         }
-        if ((e & 31) == lane) left &= ~(1u << (e >> 5));
-        if (lane == (j & 31)) {
-          if (j < 32) mine = e;
-          else out_i[j] = e;
-        }
+        if (lane < n && rank < p.k) out_i[rank] = mine;
+        __syncwarp();
+      } else {
+        choose_exactly(p, row, lane, m, out_i);
       }
+      if (lane < p.k) mine = out_i[lane];
     }
-  }
 
-  // slot j's weight in lane j mod 32, which wrote its expert
-  float top = -INFINITY;
-  if (p.renorm) {
-    for (int j = lane; j < p.k; j += 32) top = fmaxf(top, clean(__ldg(row + (j < 32 ? mine : out_i[j]))));
-    top = warp_max(top);
-  }
-  float sum = 0.f;
-  for (int j = lane; j < p.k; j += 32) {
-    const int e = j < 32 ? mine : out_i[j];
-    if (j < 32) out_i[j] = e;
-    const float v = clean(__ldg(row + e));
-    float w = 0.f;
-    if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) : expf(v - m) * inv;
-    sum += w;
-    if (!p.renorm) out_w[j] = w * p.scale;
-    else if (p.k > 32) out_w[j] = w;
-    else last = w;
-  }
-  if (p.renorm) {
-    sum = warp_sum(sum);
-    const float f = sum > 0.f ? p.scale / sum : 0.f;
-    for (int j = lane; j < p.k; j += 32) out_w[j] = (p.k > 32 ? out_w[j] : last) * f;
+    // slot j's weight in lane j mod 32, which wrote its expert
+    float top = -INFINITY;
+    if (p.renorm) {
+      for (int j = lane; j < p.k; j += 32) top = fmaxf(top, clean(__ldg(row + (j < 32 ? mine : out_i[j]))));
+      top = warp_max(top);
+    } else if (!sig) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) sum += expf(z[i] - m);
+      sum = warp_sum(sum);
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+    }
+    float sum = 0.f, only = 0.f;
+    for (int j = lane; j < p.k; j += 32) {
+      const int e = j < 32 ? mine : out_i[j];
+      if (j < 32) out_i[j] = e;
+      const float v = clean(__ldg(row + e));
+      float w = 0.f;
+      if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) : expf(v - m) * inv;
+      sum += w;
+      if (!p.renorm) out_w[j] = w * p.scale;
+      else if (p.k > 32) out_w[j] = w;
+      else only = w;
+    }
+    if (p.renorm) {
+      sum = warp_sum(sum);
+      const float f = sum > 0.f ? p.scale / sum : 0.f;
+      for (int j = lane; j < p.k; j += 32) out_w[j] = (p.k > 32 ? out_w[j] : only) * f;
+    }
   }
 }
 
@@ -366,7 +425,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_balanced_kernel(const Choic
 // for renormalised weights, r the weights before their scaling:
 //   softmax  dz = scale p (G - sum G p)       renormalised  scale r (G - sum G r)
 //   sigmoid  dz = scale G s (1 - s)           renormalised  scale r (1 - s) (G - sum G r)
-template <int NPL>
+// Only the softmax without renormalisation reaches experts that were not
+// chosen: elsewhere the slots' logits are all that is read, and the row is
+// zeros but for them.  Slot j is lane j mod 32's.
+template <bool ALL>
 __global__ void __launch_bounds__(kWarps * 32)
     route_balanced_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ expert_idx,
                                    const float* __restrict__ d_gate, int T, int E, int k, int sig, int renorm,
@@ -377,69 +439,80 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= T) return;
   const float* row = logits + t * E;
-  float z[NPL], G[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    z[i] = e < E ? __ldg(row + e) : -INFINITY;
-    G[i] = 0.f;
-  }
-  uint32_t on = 0;
-  for (int j0 = 0; j0 < k; j0 += 32) {
-    int ej = -1;
-    float gj = 0.f;
-    if (j0 + lane < k) {
-      ej = __ldg(expert_idx + t * k + j0 + lane);
-      gj = __ldg(d_gate + t * k + j0 + lane);
-      if (ej < 0 || ej >= E) dmoe::raise_error(err, DMOE_SITE_ROUTE_INDEX | DMOE_ERR_DEVICE);
+  float* out = d_logits + t * E;
+  const int32_t* idx = expert_idx + t * k;
+  const float* dg = d_gate + t * k;
+  auto slot = [&](int j, float& z, float& g) {  // a slot's expert, -1 for none
+    const int e = __ldg(idx + j);
+    if (e < 0 || e >= E) {
+      dmoe::raise_error(err, DMOE_SITE_ROUTE_INDEX | DMOE_ERR_DEVICE);
+      return -1;
     }
-    for (int j = 0; j < min(32, k - j0); ++j) {
-      const int e = __shfl_sync(kFull, ej, j);
-      const float g = __shfl_sync(kFull, gj, j);
-      if (e < 0 || e >= E || (e & 31) != lane) continue;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i == (e >> 5)) {
-          G[i] = g;
-          on |= 1u << i;
-        }
+    z = clean(__ldg(row + e));
+    g = __ldg(dg + j);
+    return e;
+  };
+  if (!ALL) {
+    if (((E | static_cast<int>(reinterpret_cast<uintptr_t>(d_logits) >> 2)) & 3) == 0) {
+      for (int e = lane; e < E / 4; e += 32) reinterpret_cast<float4*>(out)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      for (int e = lane; e < E; e += 32) out[e] = 0.f;
     }
   }
-  // what a weight is proportional to, over the experts that share a sum
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    z[i] = clean(z[i]);
-    if (!renorm || ((on >> i) & 1u)) m = fmaxf(m, z[i]);
+  // the first 32 slots stay in registers
+  float z0 = -INFINITY, g0 = 0.f;
+  const int e0 = lane < k ? slot(lane, z0, g0) : -1;
+  float m = -FLT_MAX, sum = 0.f, dot = 0.f;
+  if (ALL) {
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, clean(__ldg(row + e)));
+    m = warp_max(m);
+    for (int e = lane; e < E; e += 32) sum += expf(clean(__ldg(row + e)) - m);
+  } else if (renorm) {
+    m = z0;
+    for (int j = lane + 32; j < k; j += 32) {
+      float z = -INFINITY, g;
+      slot(j, z, g);
+      m = fmaxf(m, z);
+    }
+    m = warp_max(m);
   }
-  m = warp_max(m);
-  float r[NPL], sum = 0.f, dot = 0.f;
-  const bool shared = renorm || !sig;
-  if (shared) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      r[i] = 0.f;
-      if (z[i] > -INFINITY && (!renorm || ((on >> i) & 1u))) r[i] = renorm ? proportion(z[i], m, sig) : expf(z[i] - m);
-      sum += r[i];
-      if ((on >> i) & 1u) dot = fmaf(G[i], r[i], dot);
+  auto weight = [&](float z) { return z == -INFINITY ? 0.f : ALL ? expf(z - m) : proportion(z, m, sig); };
+  float mean = 0.f, inv = 0.f;
+  if (ALL || renorm) {
+    const float w = e0 >= 0 ? weight(z0) : 0.f;
+    dot = g0 * w;
+    if (!ALL) sum = w;
+    for (int j = lane + 32; j < k; j += 32) {
+      float z, g;
+      if (slot(j, z, g) < 0) continue;
+      const float w1 = weight(z);
+      dot = fmaf(g, w1, dot);
+      if (!ALL) sum += w1;
     }
     sum = warp_sum(sum);
     dot = warp_sum(dot);
+    inv = sum > 0.f ? 1.f / sum : 0.f;
+    mean = dot * inv;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const float mean = dot * inv;
-  float* out = d_logits + t * E;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    float d = 0.f;
-    if (shared) d = r[i] == 0.f ? 0.f : scale * (r[i] * inv) * (G[i] - mean);
-    if (sig && ((on >> i) & 1u)) {
-      const float q = expf(-fabsf(z[i])), half = 1.f / (1.f + q);
-      const float rest = z[i] > 0.f ? q * half : half;  // 1 - s
-      d = renorm ? d * rest : scale * G[i] * (q * half) * half;
+  if (ALL) {
+    const float f = -scale * inv * mean;
+    for (int e = lane; e < E; e += 32) out[e] = expf(clean(__ldg(row + e)) - m) * f;
+  }
+  __syncwarp();  // the row is there before its slots
+  for (int j = lane; j < k; j += 32) {
+    float z = z0, g = g0;
+    const int e = j < 32 ? e0 : slot(j, z, g);
+    if (e < 0) continue;
+    float d;
+    const float q = expf(-fabsf(z)), half = 1.f / (1.f + q);
+    if (ALL || renorm) {
+      const float w = weight(z);
+      d = w == 0.f ? 0.f : scale * (w * inv) * (g - mean);
+      if (sig) d *= z > 0.f ? q * half : half;  // 1 - s
+    } else {
+      d = scale * g * (q * half) * half;
     }
-    if (e < E) out[e] = d;
+    out[e] = d;
   }
 }
 
@@ -480,29 +553,19 @@ dim3 grid_of(int T) { return dim3(static_cast<unsigned>((static_cast<int64_t>(T)
 
 struct ForwardCall {
   Choice p;
+  int sms;
   cudaStream_t st;
   template <int NPL>
   cudaError_t operator()() const {
-    const dim3 grid = grid_of(p.T), block(kWarps * 32);
-    if (p.top_groups == p.groups) return dmoe::launch_pdl(route_balanced_kernel<NPL, false>, grid, block, 0, st, p);
-    const size_t smem = sizeof(float) * kWarps * p.groups * p.stride;  // at most (1024 + 32) * 32 bytes
-    return dmoe::launch_pdl(route_balanced_kernel<NPL, true>, grid, block, smem, st, p);
+    return p.E == 32 * NPL ? launch<NPL, true>() : launch<NPL, false>();
   }
-};
-
-struct BackwardCall {
-  const float* logits;
-  const int32_t* ei;
-  const float* dg;
-  int T, E, k, sig, renorm;
-  float scale;
-  float* dl;
-  int32_t* err;
-  cudaStream_t st;
-  template <int NPL>
-  cudaError_t operator()() const {
-    return dmoe::launch_pdl(route_balanced_backward_kernel<NPL>, grid_of(T), dim3(kWarps * 32), 0, st, logits, ei, dg, T,
-                            E, k, sig, renorm, scale, dl, err);
+  template <int NPL, bool FULL>
+  cudaError_t launch() const {
+    const int resident = sms * (NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2);
+    const dim3 grid(std::min<unsigned>(grid_of(p.T).x, static_cast<unsigned>(resident))), block(kWarps * 32);
+    if (p.top_groups == p.groups) return dmoe::launch_pdl(route_balanced_kernel<NPL, false, FULL>, grid, block, 0, st, p);
+    const size_t smem = sizeof(float) * kWarps * p.groups * p.stride;  // at most (1024 + 32) * 32 bytes
+    return dmoe::launch_pdl(route_balanced_kernel<NPL, true, FULL>, grid, block, smem, st, p);
   }
 };
 
@@ -532,7 +595,7 @@ DMOE_API dmoe_status dmoe_route_balanced(const float* logits, const float* bias,
   p.stride = p.size % 8 ? p.size : p.size + p.lanes;
   p.expert_idx = expert_idx;
   p.gate_w = gate_w;
-  const cudaError_t e = by_experts(E, ForwardCall{p, dmoe::as_stream(stream)});
+  const cudaError_t e = by_experts(E, ForwardCall{p, di.sm_count, dmoe::as_stream(stream)});
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
@@ -549,9 +612,10 @@ DMOE_API dmoe_status dmoe_route_balanced_backward(const float* logits, const int
   dmoe::DeviceInfo di;
   dmoe_status st = dmoe::device_info(&di);
   if (st != DMOE_OK) return st;
-  const cudaError_t e =
-      by_experts(E, BackwardCall{logits, expert_idx, d_gate, T, E, k, scores == DMOE_SCORES_SIGMOID,
-                                 renormalize ? 1 : 0, scale, d_logits, di.err_word, dmoe::as_stream(stream)});
+  const int sig = scores == DMOE_SCORES_SIGMOID, renorm = renormalize ? 1 : 0;
+  auto kern = sig || renorm ? route_balanced_backward_kernel<false> : route_balanced_backward_kernel<true>;
+  const cudaError_t e = dmoe::launch_pdl(kern, grid_of(T), dim3(kWarps * 32), 0, dmoe::as_stream(stream), logits,
+                                         expert_idx, d_gate, T, E, k, sig, renorm, scale, d_logits, di.err_word);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
