@@ -111,15 +111,17 @@ __device__ __forceinline__ F group_worth(F first, F second, int lanes) {
   return second == -INFINITY ? first : first + second;
 }
 
-// How many of the groups (one every `lanes` lanes) are better than this lane's.
-// Every lane of the warp takes part.
+// How many of the groups (one every `lanes` lanes, a power of two) are better
+// than this lane's group g.  Every lane of the warp takes part; those of a
+// group share its comparisons.
 template <class F>
-__device__ __forceinline__ int group_rank(F worth, int g, int groups, int lanes) {
+__device__ __forceinline__ int group_rank(F worth, int g, int groups, int lanes, int lane) {
   int rank = 0;
-  for (int h = 0; h < groups; ++h) {
-    const F w = __shfl_sync(kFull, worth, h * lanes);
-    rank += w > worth || (w == worth && h < g);
+  for (int h = lane & (lanes - 1), n = 0; n < groups; h += lanes, n += lanes) {
+    const F w = __shfl_sync(kFull, worth, (h * lanes) & 31);
+    rank += h < groups && (w > worth || (w == worth && h < g));
   }
+  for (int o = 1; o < lanes; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
   return rank;
 }
 
@@ -168,7 +170,7 @@ __device__ __noinline__ void choose_exactly(const Choice& p, const float* row, i
       const double w = group_worth(first, second, 32);
       if (lane == g) worth = w;
     }
-    const int rank = group_rank(worth, lane, p.groups, 1);
+    const int rank = group_rank(worth, lane, p.groups, 1, lane);
     const uint32_t stay = __ballot_sync(kFull, rank < p.top_groups && lane < p.groups);
     for (int i = 0; i < n; ++i) {
       const int e = i * 32 + lane;
@@ -193,8 +195,10 @@ __device__ __noinline__ void choose_exactly(const Choice& p, const float* row, i
 
 // A choice's key: its place v in [1, 2], whose 23 bits of fraction are steps of
 // the range, above the register i that holds it (a lower one is the larger
-// key).  Minus infinity is below all numbers; 0 is no expert.
+// key).  Minus infinity, at the place just below 1, is below all numbers; 0 is
+// no expert.
 constexpr uint32_t kMasked = 1u << 5;
+constexpr float kMaskedPlace = 0.99999994f;
 __device__ __forceinline__ uint32_t pack(float v, int i) {
   return ((__float_as_uint(v) - 0x3f800000u + 2u) << 5) + (31 - i);
 }
@@ -258,17 +262,17 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
       }
       const float range = most + (sig ? 1.f : inv);  // a softmax's largest score is its largest exponential's, 1
       step = range * 2.3841858e-7f;
-      const float half = 0.5f / range;
+      const float half = 0.49999f / range;  // all numbers' places lie above 1
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         s[i] = z[i] == -INFINITY ? -INFINITY : fmaxf(s[i] + b[i], -INFINITY);  // the choice; NaN is minus infinity
-        key[i] = s[i] == -INFINITY ? kMasked + (31 - i) : pack(fminf(fmaf(s[i], half, 1.5f), 2.f), i);
+        key[i] = pack(fmaxf(fminf(fmaf(s[i], half, 1.5f), 2.f), kMaskedPlace), i);
       }
     }
     if (!biased) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        key[i] = z[i] == -INFINITY ? kMasked + (31 - i) : pack(fmaxf(fmaf(z[i] - m, 1.f / 32.f, 2.f), 1.f), i);
+        key[i] = pack(z[i] == -INFINITY ? kMaskedPlace : fmaxf(fmaf(z[i] - m, 1.f / 32.f, 2.f), 1.f), i);
     }
     if (!FULL) {
 #pragma unroll
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
         for (int o = r; o < p.size; o += p.lanes) top_two(mine[o], first, second);
       }
       const float worth = group_worth(first, second, p.lanes);
-      int rank = group_rank(worth, g, p.groups, p.lanes);
+      int rank = group_rank(worth, g, p.groups, p.lanes, lane);
       bool stays = rank < p.top_groups && g < p.groups;
       // the worst that stays against the best that goes
       const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
             o += p.lanes;
           }
         }
-        rank = group_rank(group_worth(f, n, p.lanes), g, p.groups, p.lanes);
+        rank = group_rank(group_worth(f, n, p.lanes), g, p.groups, p.lanes, lane);
         stays = rank < p.top_groups && g < p.groups;
       }
       const uint32_t lanes_in = __ballot_sync(kFull, stays);
@@ -345,30 +349,29 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
     uint32_t own = 0;  // this lane's best
 #pragma unroll
     for (int i = 0; i < NPL; ++i) own = max(own, key[i]);
-    uint32_t last = kFull;
-    int mine = 0;  // slot `lane`'s expert
-    bool near = false;
-    int n = 0;  // slots taken: k, and those behind whose order with the last is open
-    for (;; ++n) {
-      const uint32_t best = __reduce_max_sync(kFull, own);
-      bool open = false;
-      if (last - best <= tol) {  // neighbours: their order is open (masked ones go by their number)
-        open = best >= 2 * kMasked;
-        near |= open;
-      }
-      if (n >= p.k && (!open || n >= 32)) break;
+    uint32_t last = kFull, gap = kFull;  // gap: the smallest between neighbours
+    int mine = 0;                        // slot `lane`'s expert
+    int n = 0;                           // slots taken: k, and those behind whose order with the last is open
+    uint32_t best = __reduce_max_sync(kFull, own);
+    auto take = [&]() {
       last = best;
       const int src = __ffs(__ballot_sync(kFull, own == best)) - 1;  // equal keys: the lowest lane has the lowest expert
       const int e = static_cast<int>(31 - (best & 31)) * 32 + src;
       if (n < 32) mine = lane == n ? e : mine;
       else if (lane == (n & 31)) out_i[n] = e;
-      if (lane == src) {  // its best below: of the differences that wrap the largest
-        uint32_t next = 0;
+      uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
-        own = next & 0x80000000u ? next + best : 0u;
-      }
-    }
+      for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
+      next = next & 0x80000000u ? next + best : 0u;
+      own = lane == src ? next : own;
+      best = __reduce_max_sync(kFull, own);
+      gap = min(gap, last - best);
+      ++n;
+    };
+    while (n < p.k) take();
+    // an order is open between numbers within tol (masked ones go by their place, which the slots below show, too)
+    const bool near = gap <= tol;
+    while (last - best <= tol && best >= 2 * kMasked && n < 32) take();
     if (near && !rows_alike()) {
       if (n < 32) {  // one slot a lane: their order in 64 bits
         if (biased) need_total();
