@@ -451,35 +451,305 @@ __global__ void __launch_bounds__(kThreadsL, 1) linear_kernel(const __grid_const
   }
 }
 
-// Joins the parts of up to two products, eight columns a thread, in the order
-// of the parts.
+// ------------------------------------------------------------- few rows
+// For so few rows W's bytes are all there is to do, and a tile of 256 rows of
+// x is nearly empty: its product takes as long as its loads.  So W takes the
+// place of the first operand, 128 of its columns the rows of a tile, and the
+// rows of x, 16, 32 or 64 of them, are the columns: y^T = W^T x^T, and the
+// product is a tenth of the loads.  One CTA a tile and part of K, a deep ring of
+// 16 KB slices of W; the parts of a tile are a cluster, whose CTAs meet in each
+// other's shared memory, in a fixed order.  One CTA draws some 60 GB/s, so some
+// 110 of them draw all that HBM has.
+// 1 x 14336 x 4096: 26.5 us in tiles of rows of x, with their join; 21.5 here.
+constexpr int kFewRows = 64;
+constexpr int kFewTile = 128;  // columns of W
+constexpr int kFewStages = 11;
+constexpr int kFewThreads = 192;  // TMA producer, MMA issuer, four epilogue warps
+
+struct ParamsF {
+  CUtensorMap map_w, map_x;
+  int box;  // rows of x that are loaded
+  int tiles, parts, slices;
+  Out o;
+  int32_t* err;
+};
+
+template <int ROWS>
+struct PlanF {
+  static constexpr uint32_t W_BYTES = 2 * ATOM;
+  static constexpr uint32_t STAGE = W_BYTES + ROWS * BK * 2;
+  static constexpr int FIT = static_cast<int>((kSmemMax - 2048) / STAGE);
+  static constexpr int STAGES = FIT < kFewStages ? FIT : kFewStages;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE + 512;
+  static_assert(SMEM <= kSmemMax && STAGE % 1024 == 0, "shared-memory plan");
+  static_assert(ROWS * kFewTile * sizeof(float) <= STAGES * STAGE, "the parts' sums take the ring's place");
+};
+
+// 16 consecutive fp32 columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_load16(uint32_t ta, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+__device__ __forceinline__ float float_of_bf16(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+// One sum on its way out.
+template <int ACT>
+__device__ __forceinline__ void finish(const Out& o, int row, int c, float v) {
+  if (o.bias)
+    v += o.bias_f32 ? __ldg(static_cast<const float*>(o.bias) + c)
+                    : float_of_bf16(__ldg(static_cast<const uint16_t*>(o.bias) + c));
+  const int64_t at = static_cast<int64_t>(row) * o.cols + c;
+  if (ACT != DMOE_ACT_NONE) {
+    float2 y, g;
+    if (ACT == DMOE_ACT_GELU) gelu_pair(make_float2(v, v), y, g);
+    else silu_pair(make_float2(v, v), y, g);
+    v = y.x;
+    if (o.deriv) o.deriv[at] = bf16_bits(g.x);
+  }
+  if (o.residual) v += float_of_bf16(o.residual[row * o.ld_res + c]);
+  static_cast<uint16_t*>(o.out)[at] = bf16_bits(v);
+}
+
+template <int ACT, int ROWS>
+__global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_constant__ ParamsF p) {
+  using PL = PlanF<ROWS>;
+  constexpr int STAGES = PL::STAGES;
+  constexpr uint32_t TMEM_COLS = 2 * ROWS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * PL::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&p.map_w);
+    tma_prefetch_map(&p.map_x);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  // one tile a cluster, or where K is whole as many as it takes
+  const int rank = p.parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / p.parts;
+  const int next = p.parts > 1 ? p.tiles : static_cast<int>(gridDim.x);
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.slices) * rank / p.parts);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.slices) * (rank + 1) / p.parts);
+  const int quad = warp & 3;  // epilogue: TMEM lanes, and columns of W, 32 quad .. 32 quad + 31
+  float* sums = reinterpret_cast<float*>(smem);  // parts > 1: [M][kFewTile], once the ring is done with
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = first; ok && tile < p.tiles; tile += next) {
+        for (int i = k0; i < k1; ++i) {
+          ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
+          if (!ok) break;
+          uint8_t* sw = smem + stage * PL::STAGE;
+          mbar_arrive_expect_tx(full + stage, PL::W_BYTES + p.box * BK * 2);
+          tma_load_2d(sw, &p.map_w, full + stage, tile * kFewTile, i * BK);
+          tma_load_2d(sw + ATOM, &p.map_w, full + stage, tile * kFewTile + 64, i * BK);
+          tma_load_2d(sw + PL::W_BYTES, &p.map_x, full + stage, i * BK, 0);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every stage has been consumed before the CTA may leave
+      for (int s = 0; s < STAGES && ok; ++s) {
+        ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc = 0, acc_phase = 0;
+      constexpr uint32_t MN_STEP = (UMMA_K * 128) >> 4, K_STEP = (UMMA_K * 2) >> 4;
+      const uint64_t a0 = sdesc_sw128(smem_u32(smem), ATOM, 1024);
+      const uint64_t b0 = sdesc_sw128(smem_u32(smem) + PL::W_BYTES, 16, 1024);
+      constexpr uint32_t idesc = idesc_bf16(kFewTile, ROWS, true, false);
+      for (int tile = first; ok && tile < p.tiles; tile += next) {
+        ok = mbar_wait(tempty + acc, acc_phase ^ 1u, abort_flag);
+        if (!ok) break;
+        fence_after_sync();
+        for (int i = k0; i < k1; ++i) {
+          ok = mbar_wait(full + stage, phase, abort_flag);
+          if (!ok) break;
+          fence_after_sync();
+          const uint64_t off = static_cast<uint64_t>(stage) * (PL::STAGE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BK / UMMA_K; ++kk)
+            mma_bf16(tmem_base + acc * ROWS, a0 + off + MN_STEP * kk, b0 + off + K_STEP * kk, idesc, i > k0 || kk > 0);
+          mma_commit(empty + stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(tfull + acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    uint32_t acc = 0, acc_phase = 0;
+    for (int tile = first; ok && tile < p.tiles; tile += next) {
+      const int c = tile * kFewTile + quad * 32 + lane;
+      ok = mbar_wait(tfull + acc, acc_phase, abort_flag);
+      if (!ok) break;
+      __syncwarp();
+      fence_after_sync();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * ROWS;
+#pragma unroll 1
+      for (int r = 0; r < ROWS && r < p.o.rows; r += 16) {
+        float v[16];
+        __syncwarp();
+        tmem_load16(tb + r, v);
+        if (p.parts > 1) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (r + q < p.o.rows) sums[(r + q) * kFewTile + quad * 32 + lane] = v[q];
+        } else if (c < p.o.cols) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (r + q < p.o.rows) finish<ACT>(p.o, r + q, c, v[q]);
+        }
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty + acc);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+  if (!ok && (warp > 1 ? lane == 0 : true)) {
+    dmoe::raise_error(p.err, DMOE_SITE_GEMM_WAIT | DMOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  __syncwarp();
+  if (*abort_flag) {  // a wait gave up: let copies and products under way land before their memory goes
+    const uint64_t t0 = dmoe::globaltimer_ns();
+    while (dmoe::globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
+  }
+  if (p.parts > 1) {
+    __syncwarp();
+    cluster_sync();  // every part's sums are there
+    // this CTA's share of the columns, of all rows
+    const int share = kFewTile / p.parts, log_share = __ffs(share) - 1;  // parts is a power of two
+    const int from = rank * share;
+    // four sums at a time, for the way to the other CTAs
+    for (int i0 = threadIdx.x; i0 < p.o.rows * share; i0 += 4 * kFewThreads) {
+      float v[4][8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kFewThreads;
+        const int r = i >> log_share, col = from + (i & (share - 1));
+        if (i >= p.o.rows * share) continue;
+        const uint32_t at = smem_u32(sums + r * kFewTile + col);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[j][q] = q < p.parts ? dsmem_ld_f32(dsmem_addr(at, q)) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kFewThreads;
+        const int r = i >> log_share, c = first * kFewTile + from + (i & (share - 1));
+        if (i >= p.o.rows * share || c >= p.o.cols) continue;
+        float sum = v[j][0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) sum += v[j][q];
+        finish<ACT>(p.o, r, c, sum);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the others have read this one's
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after_sync();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// Joins the parts of up to two products, eight columns a piece.  SHARE
+// neighbouring lanes take every SHARE-th part of a piece and add theirs up, in
+// a fixed order: where pieces are few the parts' loads go side by side.
 struct Join {
   Out o[2];
   int parts[2];
   int64_t vecs[2];  // 8-column pieces (0: nothing to join)
 };
 
-template <int ACT>
-__global__ void __launch_bounds__(256) join_kernel(const Join p) {
+template <int ACT, int SHARE>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Join p) {
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
-  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / SHARE;
+  const int mine = threadIdx.x % SHARE;
   const int kind = i < p.vecs[0] ? 0 : 1;
   if (kind == 1) i -= p.vecs[0];
-  if (i >= p.vecs[kind]) return;
+  const bool live = i < p.vecs[kind];
   const Out& o = p.o[kind];
   const int per_row = o.cols >> 3;
-  const int64_t row = i / per_row;
-  const int c = static_cast<int>(i - row * per_row) * 8;
+  const int64_t row = live ? i / per_row : 0;
+  const int c = live ? static_cast<int>(i - row * per_row) * 8 : 0;
   const int64_t at = row * o.cols + c, step = static_cast<int64_t>(o.rows) * o.cols;
   float v[8] = {};
+  if (live) {
 #pragma unroll 8
-  for (int s = 0; s < p.parts[kind]; ++s) {
-    const float4* a = reinterpret_cast<const float4*>(o.part + s * step + at);
-    const float4 u = __ldg(a), w = __ldg(a + 1);
-    v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
-    v[4] += w.x, v[5] += w.y, v[6] += w.z, v[7] += w.w;
+    for (int s = mine; s < p.parts[kind]; s += SHARE) {
+      const float4* a = reinterpret_cast<const float4*>(o.part + s * step + at);
+      const float4 u = __ldg(a), w = __ldg(a + 1);
+      v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+      v[4] += w.x, v[5] += w.y, v[6] += w.z, v[7] += w.w;
+    }
   }
+#pragma unroll
+  for (int h = SHARE / 2; h > 0; h /= 2) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += __shfl_xor_sync(0xffffffffu, v[q], h);
+  }
+  if (!live || mine != 0) return;
   if (o.bias) {
     float b[8];
     load_bias(o, c, b);
@@ -569,24 +839,34 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ su
 constexpr int kMaxParts = 64;
 constexpr int kMinSlices = 4;  // of a part
 
+// What the times below leave out: launch, first loads, last epilogue.
+constexpr int64_t kTilesNs = 8000, kFewNs = 4500;
+
 // Nanoseconds of an item: `busy` pairs at work, each with this many K slices
-// of a tile.  A slice costs what its product takes or, where no other pair
-// reads the same columns (alone), what its bytes take from HBM at 6.5 TB/s; a
-// tile also its epilogue, of which the next product hides all but the rest
-// here (512-wide tiles fill the TMEM, and hide little).
-int64_t item_ns(int slices, int tile, bool alone, int busy) {
-  const int64_t product = tile == 2 * BN ? 600 : tile == BN ? 370 : 230;
+// of a tile.  A slice costs what its product or its loads from L2 take or,
+// where no other pair reads the same columns (alone), what its bytes take from
+// HBM at 6.5 TB/s.  A 512-wide tile, which fills the TMEM, also waits for part of
+// its epilogue; of a narrower one the next product hides it, unless it is
+// longer, as with an activation and its derivative over a short sum.
+// Measured: 1024 x 2048 x 2048 in tiles of 128, 256 and 512 20, 24 and 41 us, in
+// two parts 22, 19 and -; 8192 x 512 x 2048, gelu 44, 37 and 40; 8192 x 2048 x
+// 512 28, 22 and 33; 8192 x 14336 x 4096 -, 610 and 572.
+int64_t item_ns(int slices, int tile, bool alone, int busy, bool act) {
+  const int64_t product = tile == 2 * BN ? 630 : tile == BN ? 400 : 310;
   const int64_t bytes = alone ? static_cast<int64_t>(tile) * BK * 2 * busy / 6500 : 0;
-  return slices * std::max(product, bytes) + (tile == 2 * BN ? 5500 : tile == BN ? 1500 : 1000);
+  const int64_t sums = slices * std::max(product, bytes);
+  if (tile == 2 * BN) return sums + (act ? 11000 : 5500);
+  return std::max<int64_t>(sums, tile == BN ? (act ? 7000 : 4000) : (act ? 5000 : 2500)) + 500;
 }
 
 // A product [rows, cols] over K slices, and how it is cut.
 struct Want {
   int rows, cols, slices;
+  bool act;  // an activation in the epilogue
   int tile, parts;
   int items() const { return ceil_div(rows, 2 * BM) * ceil_div(cols, tile) * parts; }
   int64_t ns(int busy) const {
-    return item_ns(ceil_div(slices, parts), tile, rows <= 2 * BM, std::min(busy, kUnits));
+    return item_ns(ceil_div(slices, parts), tile, rows <= 2 * BM, std::min(busy, kUnits), act && parts == 1);
   }
   // the join: a launch, and the sums' way to memory and back
   int64_t join_ns() const {
@@ -597,7 +877,7 @@ struct Want {
 // Chooses tiles and parts of up to two products (b.rows == 0: one): the cut
 // whose busiest pair is done first.  Parts only where there are at most two
 // items a pair, which bounds the sums that they leave (part_bytes()).
-void choose(Want& a, Want& b) {
+int64_t choose(Want& a, Want& b) {
   Want best_a = a, best_b = b;
   int64_t least = -1;
   static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
@@ -634,12 +914,14 @@ void choose(Want& a, Want& b) {
       }
     }
   a = best_a, b = best_b;
+  return least + kTilesNs;
 }
 
 // Bytes that the parts of a [rows, cols] product's sums need at most: 2 kUnits
 // items of 256 x 256.  Never falls with rows.
+constexpr int64_t kMostPartSums = static_cast<int64_t>(2 * kUnits) * 2 * BM * BN;
 size_t part_bytes(int64_t rows, int64_t cols) {
-  const int64_t most = std::min<int64_t>(static_cast<int64_t>(2 * kUnits) * 2 * BM * BN, kMaxParts * rows * cols);
+  const int64_t most = std::min<int64_t>(kMostPartSums, kMaxParts * rows * cols);
   return static_cast<size_t>(round_up(most * sizeof(float), 256));
 }
 
@@ -686,6 +968,78 @@ dmoe_status launch_linear(ParamsL& p, const Grid& ga, const Grid& gb, const dmoe
   return DMOE_OK;
 }
 
+template <int ACT>
+dmoe_status join(const Out* o, int parts_a, int parts_b, cudaStream_t st) {
+  Join j{};
+  for (int k = 0; k < 2; ++k) {
+    j.o[k] = o[k];
+    j.parts[k] = k ? parts_b : parts_a;
+    j.vecs[k] = o[k].part ? static_cast<int64_t>(o[k].rows) * (o[k].cols >> 3) : 0;
+  }
+  const int64_t vecs = j.vecs[0] + j.vecs[1];
+  if (vecs == 0) return DMOE_OK;
+  // the parts side by side as long as that leaves no SM more than its threads
+  const bool share = vecs * 8 <= 4 * kUnits * 1024;
+  const int64_t blocks = (vecs * (share ? 8 : 1) + 255) / 256;
+  const cudaError_t e = dmoe::launch_pdl(share ? join_kernel<ACT, 8> : join_kernel<ACT, 1>,
+                                         dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, j);
+  if (e != cudaSuccess) return dmoe::cuda_status(e);
+  dmoe::count_launches(1);
+  return DMOE_OK;
+}
+
+// The parts of few rows' product (a cluster's CTAs: 1, 2, 4 or 8, as many as
+// leave one CTA an SM), and its nanoseconds: slices of 16 KB of W, at what one
+// CTA draws or at its share of 6.5 TB/s.
+struct FewCut {
+  int parts;
+  int64_t ns;
+};
+FewCut cut_few(int K, int N) {
+  const int tiles = ceil_div(N, kFewTile), slices = ceil_div(K, BK);
+  int parts = 8;
+  while (parts > 1 && (tiles * parts > 2 * kUnits || slices < 2 * parts)) parts /= 2;
+  const int busy = std::min(tiles * parts, 2 * kUnits);
+  const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / 6500);
+  return FewCut{parts, static_cast<int64_t>(ceil_div(tiles * parts, 2 * kUnits)) * ceil_div(slices, parts) * slice + kFewNs};
+}
+
+template <int ACT, int ROWS>
+cudaError_t launch_few(const ParamsF& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
+  auto kern = few_rows_kernel<ACT, ROWS>;
+  constexpr size_t smem = PlanF<ROWS>::SMEM;
+  static std::atomic<uint64_t> opted{0};
+  const uint64_t bit = uint64_t(1) << di.device;
+  if (!(opted.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    opted.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  if (p.parts == 1)
+    return dmoe::launch_pdl(kern, dim3(static_cast<unsigned>(std::min(di.sm_count, p.tiles))), dim3(kFewThreads), smem, st, p);
+  return dmoe::launch_pdl_cluster(kern, dim3(static_cast<unsigned>(p.tiles * p.parts)), dim3(kFewThreads), smem, st, p.parts,
+                                  p);
+}
+
+template <int ACT>
+dmoe_status run_few(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const Out& o, int parts,
+                    const dmoe::DeviceInfo& di, cudaStream_t st) {
+  ParamsF p{};
+  p.box = o.rows;
+  p.tiles = ceil_div(o.cols, kFewTile);
+  p.parts = parts;
+  p.slices = ceil_div(K, BK);
+  p.o = o;
+  p.err = di.err_word;
+  if (!map_pitched(&p.map_w, w, K, o.cols, o.cols, 64, BK) || !map_pitched(&p.map_x, x, o.rows, K, ldx, BK, p.box))
+    return DMOE_ERR_CUDA;
+  const cudaError_t e = o.rows <= 16 ? launch_few<ACT, 16>(p, di, st)
+                        : o.rows <= 32 ? launch_few<ACT, 32>(p, di, st) : launch_few<ACT, 64>(p, di, st);
+  if (e != cudaSuccess) return dmoe::cuda_status(e);
+  dmoe::count_launches(1);
+  return DMOE_OK;
+}
+
 // Runs the products a (kind 0) and b (kind 1; b.rows == 0: none) as chosen,
 // and joins what was cut.
 template <int ACT>
@@ -702,18 +1056,7 @@ dmoe_status run_products(ParamsL& p, const Want& a, const Want& b, float* part_a
   if (gb.parts > 1) p.o[1].part = part_b;
   const dmoe_status s = wide ? launch_linear<ACT, 2>(p, ga, gb, di, st) : launch_linear<ACT, 1>(p, ga, gb, di, st);
   if (s != DMOE_OK) return s;
-  Join j{};
-  for (int k = 0; k < 2; ++k) {
-    j.o[k] = p.o[k];
-    j.parts[k] = k ? gb.parts : ga.parts;
-    j.vecs[k] = p.o[k].part ? static_cast<int64_t>(p.o[k].rows) * (p.o[k].cols >> 3) : 0;
-  }
-  if (j.vecs[0] + j.vecs[1] == 0) return DMOE_OK;
-  const int64_t blocks = (j.vecs[0] + j.vecs[1] + 255) / 256;
-  const cudaError_t e = dmoe::launch_pdl(join_kernel<ACT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, j);
-  if (e != cudaSuccess) return dmoe::cuda_status(e);
-  dmoe::count_launches(1);
-  return DMOE_OK;
+  return join<ACT>(p.o, ga.parts, gb.parts, st);
 }
 
 bool sizes_ok(int M, int K, int N) {
@@ -771,9 +1114,19 @@ DMOE_API dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t*
   dmoe::DeviceInfo di;
   const dmoe_status s = dmoe::device_info(&di);
   if (s != DMOE_OK) return s;
-  Want a{M, N, ceil_div(K, BK)}, none{};
-  choose(a, none);
-  if (a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
+  Want a{M, N, ceil_div(K, BK), act != DMOE_ACT_NONE}, none{};
+  const int64_t ns = choose(a, none);
+  const FewCut few = cut_few(K, N);
+  const bool is_few = M <= kFewRows && few.ns < ns;
+  if (!is_few && a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
+  const Out o{M, N, bias, bias_f32, deriv, residual, ldr, nullptr, y, 0, nullptr};
+  float* part = static_cast<float*>(ws);
+  cudaStream_t st = dmoe::as_stream(stream);
+  if (is_few) {
+    if (act == DMOE_ACT_GELU) return run_few<DMOE_ACT_GELU>(x, ldx, w, K, o, few.parts, di, st);
+    if (act == DMOE_ACT_SILU) return run_few<DMOE_ACT_SILU>(x, ldx, w, K, o, few.parts, di, st);
+    return run_few<DMOE_ACT_NONE>(x, ldx, w, K, o, few.parts, di, st);
+  }
   ParamsL p{};
   if (!map_pitched(&p.map_a[0], x, M, K, ldx, BK, box_rows(M)) || !map_pitched(&p.map_b[0], w, K, N, N, 64, BK))
     return DMOE_ERR_CUDA;
@@ -781,10 +1134,8 @@ DMOE_API dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t*
   p.map_b[1] = p.map_b[0];
   p.b_mn = 1;
   p.a_rows = box_rows(M);
-  p.o[0] = Out{M, N, bias, bias_f32, deriv, residual, ldr, nullptr, y, 0, nullptr};
+  p.o[0] = o;
   p.err = di.err_word;
-  float* part = static_cast<float*>(ws);
-  cudaStream_t st = dmoe::as_stream(stream);
   if (act == DMOE_ACT_GELU) return run_products<DMOE_ACT_GELU>(p, a, none, part, nullptr, di, st);
   if (act == DMOE_ACT_SILU) return run_products<DMOE_ACT_SILU>(p, a, none, part, nullptr, di, st);
   return run_products<DMOE_ACT_NONE>(p, a, none, part, nullptr, di, st);
@@ -834,7 +1185,7 @@ DMOE_API dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, cons
     if (out) dz = out, lddz = N;
   }
   if (products) {
-    Want a{dx ? M : 0, K, ceil_div(N, BK)}, b{dw ? K : 0, N, ceil_div(M, BK)};
+    Want a{dx ? M : 0, K, ceil_div(N, BK), false}, b{dw ? K : 0, N, ceil_div(M, BK), false};
     if (dx) {
       choose(a, b);
     } else {

@@ -514,7 +514,8 @@ def check_linear(dm, M, K, N, act, bias, residual, x=None):
     assert bool((guard == 0x5a).all())
 
 
-LINEAR = [(1, 8, 8), (1, 4096, 1024), (7, 72, 136), (16, 2048, 520), (128, 520, 264), (130, 1032, 2056), (257, 64, 1000),
+LINEAR = [(1, 8, 8), (1, 4096, 1024), (7, 72, 136), (16, 2048, 520), (3, 8200, 1000), (17, 4104, 2056), (33, 2048, 1032),
+          (64, 4096, 4096), (65, 4096, 264), (128, 520, 264), (130, 1032, 2056), (257, 64, 1000),
           (600, 264, 8), (1000, 8, 600), (513, 4096, 512), (2560, 512, 4096), (1031, 1000, 5128)]
 
 
