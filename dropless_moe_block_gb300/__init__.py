@@ -44,6 +44,7 @@ __all__ = [
     "route_balanced", "route_balanced_backward", "balance_bias",
     "sandwich_norm", "sandwich_norm_backward", "sandwich_norm_backward_workspace_size",
     "linear", "linear_workspace_size", "linear_backward", "linear_backward_workspace_size",
+    "SharedExpert",
     "EPI_STORE", "EPI_GELU_FWD", "EPI_SWIGLU_FWD", "EPI_GELU_BWD", "EPI_SWIGLU_BWD", "BLOCK",
 ]
 
@@ -923,10 +924,15 @@ class DMoELayer:
     (h_l = act(h_{l-1} W1_l) W2_l), and the weights are lists of L tensors.
     Every intermediate lives in a preallocated device buffer sized for the
     worst-case padding (P_max), so a step never allocates.
+
+    ``balanced`` (a dict of ``scores``, ``groups``, ``top_groups`` and ``scale``
+    of ``route_balanced``, each optional; {} for its defaults) routes with a
+    bias for balance, ``self.route_bias`` (zeros at first), which ``balance()``
+    moves by the loads of the last forward pass.
     """
 
     def __init__(self, T: int, d: int, E: int, F: int, k: int, act: str = "gelu", renormalize: bool = False,
-                 device="cuda", front: str = "separate", depth: int = 1, block: int = BLOCK):
+                 device="cuda", front: str = "separate", depth: int = 1, block: int = BLOCK, balanced=None):
         if act not in ("gelu", "swiglu"):
             raise ValueError(act)
         if depth < 1:
@@ -946,6 +952,14 @@ class DMoELayer:
         if block != BLOCK and front == "route_permute":
             raise ValueError("the route_permute front pads to 128 rows; use separate or fused")
         self.front = front
+        if balanced is not None:
+            if front != "separate":
+                raise ValueError("balanced routing runs the separate front")
+            unknown = set(balanced) - {"scores", "groups", "top_groups", "scale"}
+            if unknown:
+                raise ValueError(f"balanced: unknown {', '.join(sorted(unknown))}")
+            self.route_bias = torch.zeros(E, dtype=torch.float32, device=device)
+        self.balanced = None if balanced is None else dict(balanced)
         self.P_max = padded_rows_max(T, k, E, block)
         self.topo = Topology(E, F, self.P_max, device, block=block)
         nnz_max = self.topo.nnz_max
@@ -1017,11 +1031,20 @@ class DMoELayer:
                 front.append(("build_topology", lambda: build_topology(self.padded_offsets, self.topo,
                                                                        self.tokens_per_expert)))
         else:
-            front = [
-                ("gate_route_topk", lambda: gate_route_topk(x, w_gate, k, self.renormalize, self.gate_logits,
-                                                            self.expert_idx, self.gate_w))
-                if w_gate is not None else
-                ("route_topk", lambda: route_topk(logits, k, self.renormalize, self.expert_idx, self.gate_w)),
+            front = []
+            if w_gate is not None:  # (of a balanced layer it makes the logits alone; its choice is written over)
+                front.append(("gate_route_topk", lambda: gate_route_topk(x, w_gate, k, self.renormalize,
+                                                                         self.gate_logits, self.expert_idx,
+                                                                         self.gate_w)))
+            if self.balanced is not None:
+                front.append(("route_balanced", lambda: route_balanced(logits, k, self.expert_idx, self.gate_w,
+                                                                       bias=self.route_bias,
+                                                                       renormalize=self.renormalize,
+                                                                       **self.balanced)))
+            elif w_gate is None:
+                front.append(("route_topk", lambda: route_topk(logits, k, self.renormalize, self.expert_idx,
+                                                               self.gate_w)))
+            front += [
                 ("permute_pad", lambda: permute_pad(x, self.expert_idx, E, self.P_max, self.tokens_per_expert,
                                                     self.padded_offsets, self.dest_row, self.src_of_row,
                                                     self.x_perm, self.P_dev, self.ws, block=self.block)),
@@ -1048,8 +1071,12 @@ class DMoELayer:
         calls = [
             ("combine_backward", lambda: combine_backward(dy, self.y_perm, self.src_of_row, self.gate_w,
                                                           self.P_dev, k, self.P_max, self.dy_perm, self.d_gate)),
-            ("route_backward", lambda: route_topk_backward(logits, self.expert_idx, self.gate_w, self.d_gate,
-                                                           self.renormalize, self.d_logits)),
+            ("route_backward", (lambda: route_topk_backward(logits, self.expert_idx, self.gate_w, self.d_gate,
+                                                            self.renormalize, self.d_logits))
+             if self.balanced is None else
+             (lambda: route_balanced_backward(logits, self.expert_idx, self.d_gate, self.d_logits,
+                                              scores=self.balanced.get("scores", "softmax"),
+                                              renormalize=self.renormalize, scale=self.balanced.get("scale", 1.0)))),
         ]
         for l in reversed(range(self.depth)):  # g_{l+1} -> dH_l -> g_l, dW*_l
             sfx = self._sfx(l)
@@ -1197,6 +1224,47 @@ class DMoELayer:
     def backward(self, dy, x, w1, w2, w3=None):
         for _, f in self.backward_calls(dy, x, w1, w2, w3):
             f()
+        return self.dx
+
+    def balance(self, rate: float):
+        """Moves ``route_bias`` by the loads of the last forward pass (of a
+        balanced layer)."""
+        if self.balanced is None:
+            raise ValueError("the layer does not route with a bias")
+        balance_bias(self.route_bias, self.tokens_per_expert, rate)
+
+
+class SharedExpert:
+    """Buffers and calls of a dense two-layer MLP that every token passes beside
+    its routed experts: y = act(x . w1 + b1) . w2 + b2 + residual, the residual
+    being what the routed experts gave.  w1 [d, F], w2 [F, d] bf16; b1 [F], b2
+    [d] bf16 or fp32, or None; act: "gelu" or "silu"."""
+
+    def __init__(self, T: int, d: int, F: int, act: str = "gelu", device="cuda"):
+        if act not in ("gelu", "silu"):
+            raise ValueError(act)
+        self.T, self.d, self.F, self.act = T, d, F, act
+        bf = dict(dtype=torch.bfloat16, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        self.a, self.deriv = torch.empty(T, F, **bf), torch.empty(T, F, **bf)
+        self.dz = torch.empty(T, F, **bf)
+        self.y, self.dx = torch.empty(T, d, **bf), torch.empty(T, d, **bf)
+        self.dW1, self.dW2 = torch.empty(d, F, **bf), torch.empty(F, d, **bf)
+        self.db1, self.db2 = torch.empty(F, **f32), torch.empty(d, **f32)
+        n = max(linear_workspace_size(T, d, F), linear_workspace_size(T, F, d),
+                linear_backward_workspace_size(T, d, F), linear_backward_workspace_size(T, F, d))
+        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+
+    def forward(self, x, w1, w2, b1=None, b2=None, residual=None):
+        linear(x, w1, self.a, self.ws, bias=b1, act=self.act, deriv=self.deriv)
+        linear(self.a, w2, self.y, self.ws, bias=b2, residual=residual)
+        return self.y
+
+    def backward(self, dy, x, w1, w2):
+        """dx and, in dW1, dW2, db1 and db2, the weights' gradients (the
+        residual's is dy)."""
+        linear_backward(dy, self.a, w2, self.dz, self.dW2, self.ws, dbias=self.db2, factor=self.deriv)
+        linear_backward(self.dz, x, w1, self.dx, self.dW1, self.ws, dbias=self.db1)
         return self.dx
 
 
