@@ -29,8 +29,8 @@ namespace {
 using namespace dmoe::rows;
 
 constexpr int kMaxD = 16384;
-constexpr int kMinThreads = 128;           // of a block, while a row takes fewer
-constexpr int kMaxStages = 4;              // backward: units of rows in flight per block
+constexpr int kMinThreads = 128;           // forward: of a block, while a row takes fewer
+constexpr int kMaxStages = 4;              // backward: rows in flight per group of threads
 constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 constexpr int kBackThreads = 512;          // backward: threads per SM, 128 registers each
 
@@ -162,39 +162,44 @@ __device__ __forceinline__ float three_sums(const float* s, int lane) {
   return k;
 }
 
-// A persistent block walks units of RPB rows, dealt round-robin; a ring of
-// `stages` units of dy, u, h and dh is filled ahead by bulk copies, one per
-// row and tensor, and read twice from there: before the row's sums and after.
-// Every thread keeps its columns of both weights (up to two vectors) and of
-// both weights' gradients; a block's row groups meet in shared memory, and the
-// block writes one fp32 row of `partial`.
+// One block an SM, in groups of the TPR threads that share a row; the groups
+// walk their rows without meeting one another.  Each fills a ring of `stages`
+// rows ahead by bulk copies, one per tensor, and reads a row twice from there:
+// before its sums and after.  Every thread keeps its columns of both weights (up
+// to two vectors) and of both weights' gradients; the groups' meet in shared
+// memory at the end, and the block writes one fp32 row of `partial`.
 // Instructions come close to being the bound: pairs of values an instruction,
 // and two vectors a thread, so that the sums' meeting costs a quarter of them
-// (8192 x 4096: 99 us with one vector and value by value).
+// (8192 x 4096: 99 us with one vector and value by value, 71 so; 8191 x 512,
+// with blocks of four rows that wait for one another and leave 608 partial
+// rows, 19 us, TBD with groups).
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackThreads / (TPR > kMinThreads ? TPR : kMinThreads))
-    sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
+__global__ void __launch_bounds__(kBackThreads, 1) sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
   using namespace dmoe::tc;
   using dmoe::f2_fma;
   using dmoe::f2_mul;
-  constexpr int BLOCK = TPR > kMinThreads ? TPR : kMinThreads;
-  constexpr int RPB = BLOCK / TPR;
+  constexpr int GROUPS = kBackThreads / TPR;
   constexpr int WPR = TPR / 32;
   constexpr bool KEEP = VPT <= 2;  // the weights in registers
-  __shared__ float red[2][BLOCK / 32 * 4];
-  __shared__ uint64_t full[kMaxStages];
-  __shared__ int gave_up;
-  extern __shared__ __align__(16) uint8_t ring[];  // [stages][dy, u, h, dh][RPB][d], then reused for the weights' sums
+  __shared__ float red[2][kBackThreads / 32 * 4];
+  __shared__ uint64_t full[GROUPS][kMaxStages];
+  __shared__ int gave_up[GROUPS];
+  extern __shared__ __align__(16) uint8_t ring[];  // [GROUPS][stages][dy, u, h, dh][d], then the weights' sums
   const int c = threadIdx.x % TPR;
   const int rg = threadIdx.x / TPR;
   const int lane = threadIdx.x & 31;
   const int d = p.d, nvec = d >> 3;
   const uint32_t row_bytes = static_cast<uint32_t>(d) * 2;
-  const uint32_t part_bytes = RPB * row_bytes;
-  const int64_t units = (static_cast<int64_t>(p.T) + RPB - 1) / RPB;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(full + s, 1);
-    gave_up = 0;
+  const uint32_t stage_bytes = 4 * row_bytes;
+  uint8_t* mine = ring + static_cast<size_t>(rg) * p.stages * stage_bytes;
+  auto meet = [&]() {  // of the group
+    if (TPR == 32) __syncwarp();
+    else if (GROUPS == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(rg + 1), "n"(TPR) : "memory");
+  };
+  if (c == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&full[rg][s], 1);
+    gave_up[rg] = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -225,45 +230,41 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
       load_w4<WF32>(p.w_pre, c + i * TPR, b);
     }
   };
-  // thread 0: the rows of unit n into stage s
-  auto fill = [&](int64_t n, int s) {
-    if (n >= units) return;
-    const int64_t t0 = n * RPB;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(RPB), p.T - t0));
-    uint8_t* at = ring + s * 4 * part_bytes;
-    mbar_arrive_expect_tx(full + s, rows * row_bytes * (p.dh ? 4 : 3));
-    for (int r = 0; r < rows; ++r) {
-      bulk_load(at + r * row_bytes, p.dy + (t0 + r) * p.lddy, row_bytes, full + s);
-      bulk_load(at + part_bytes + r * row_bytes, p.u + (t0 + r) * p.ldu, row_bytes, full + s);
-      bulk_load(at + 2 * part_bytes + r * row_bytes, p.h + (t0 + r) * d, row_bytes, full + s);
-      if (p.dh) bulk_load(at + 3 * part_bytes + r * row_bytes, p.dh + (t0 + r) * p.lddh, row_bytes, full + s);
-    }
+  // the group's first thread: row t into stage s
+  auto fill = [&](int64_t t, int s) {
+    if (t >= p.T) return;
+    uint8_t* at = mine + s * stage_bytes;
+    uint64_t* bar = &full[rg][s];
+    mbar_arrive_expect_tx(bar, row_bytes * (p.dh ? 4 : 3));
+    bulk_load(at, p.dy + t * p.lddy, row_bytes, bar);
+    bulk_load(at + row_bytes, p.u + t * p.ldu, row_bytes, bar);
+    bulk_load(at + 2 * row_bytes, p.h + t * d, row_bytes, bar);
+    if (p.dh) bulk_load(at + 3 * row_bytes, p.dh + t * p.lddh, row_bytes, bar);
   };
-  int64_t n = blockIdx.x;
-  if (threadIdx.x == 0)
-    for (int s = 0; s < p.stages; ++s) fill(n + static_cast<int64_t>(s) * gridDim.x, s);
+  // rows are dealt round the blocks, then the groups: few rows take many SMs
+  const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
+  const int64_t t0 = blockIdx.x + static_cast<int64_t>(gridDim.x) * rg;
+  if (c == 0)
+    for (int s = 0; s < p.stages; ++s) fill(t0 + s * step, s);
   int stage = 0, flip = 0;
   uint32_t phase = 0;
   const float per = 1.f / static_cast<float>(d);
-  for (; n < units; n += gridDim.x) {
-    const int64_t t = n * RPB + rg;
-    const bool live = t < p.T;
-    const float ru = live ? __ldg(p.rstd_u + t) : 0.f;
-    const float rh = live ? __ldg(p.rstd_h + t) : 0.f;
-    const float gt = live && p.gate ? __ldg(p.gate + t * p.gate_step) : 1.f;
-    if (!mbar_wait(full + stage, phase, &gave_up)) gave_up = 1;
-    const uint4* at = reinterpret_cast<const uint4*>(ring + stage * 4 * part_bytes + rg * row_bytes);
-    const int next = RPB * nvec;  // from one tensor's rows to the next one's
+  for (int64_t t = t0; t < p.T; t += step) {
+    const float ru = __ldg(p.rstd_u + t);
+    const float rh = __ldg(p.rstd_h + t);
+    const float gt = p.gate ? __ldg(p.gate + t * p.gate_step) : 1.f;
+    if (!mbar_wait(&full[rg][stage], phase, &gave_up[rg])) gave_up[rg] = 1;
+    const uint4* at = reinterpret_cast<const uint4*>(mine + stage * stage_bytes);
     float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
-      if (!live || v >= nvec) continue;
+      if (v >= nvec) continue;
       float2 f[4], g[4], w[4], o[4], a[4], b[4];
       unpack4(at[v], f);
-      unpack4(at[next + v], g);
-      unpack4(at[2 * next + v], w);
-      unpack4(p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0), o);
+      unpack4(at[nvec + v], g);
+      unpack4(at[2 * nvec + v], w);
+      unpack4(p.dh ? at[3 * nvec + v] : make_uint4(0, 0, 0, 0), o);
       weights(i, a, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -273,12 +274,13 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
         s3 = f2_fma(au, w[j], s3);
       }
     }
+    __syncwarp();
     const float part[3] = {s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
     float sum = three_sums(part, lane);  // of number lane / 8
     if (WPR > 1) {
       // sum q of warp w at 4 w + q; each lane brings together those of one q
       if ((lane & 7) == 0) red[flip][(threadIdx.x >> 5) * 4 + (lane >> 3)] = sum;
-      __syncthreads();
+      meet();
       const float* r = red[flip] + rg * WPR * 4;
       if (WPR >= 8) {
         sum = r[lane];
@@ -289,30 +291,27 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
       }
 #pragma unroll
       for (int o = 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    } else {
-      __syncthreads();
     }
     const int span = WPR > 1 ? 1 : 8;  // lanes from one sum to the next
     const float t1 = __shfl_sync(0xffffffffu, sum, 0), t2 = __shfl_sync(0xffffffffu, sum, span),
                 t3 = __shfl_sync(0xffffffffu, sum, 2 * span);
-    if (gave_up) break;
-    // past this barrier every thread is done with the unit before this one
-    if (p.stages > 1 && threadIdx.x == 0 && n != static_cast<int64_t>(blockIdx.x))
-      fill(n + static_cast<int64_t>(p.stages - 1) * gridDim.x, stage == 0 ? p.stages - 1 : stage - 1);
+    if (*reinterpret_cast<volatile int*>(&gave_up[rg])) break;
+    // past this meeting every thread of the group is done with the row before this one
+    if (p.stages > 1 && c == 0 && t != t0) fill(t + (p.stages - 1) * step, stage == 0 ? p.stages - 1 : stage - 1);
     const float m1 = t1 * per * rh * rh;              // dH = dh + rh (g - h m1)
     const float along = ru * fmaf(-rh * m1, t3, t2);  // sum a dH u ru
     const float m2 = along * per * ru;                // du = gate ru (a dH - u m2)
-    if (live && c == 0 && p.d_gate) p.d_gate[t] = along;
+    if (c == 0 && p.d_gate) p.d_gate[t] = along;
     const float gr = gt * ru;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = c + i * TPR;
-      if (!live || v >= nvec) continue;
+      if (v >= nvec) continue;
       float2 f[4], g[4], w[4], o[4], a[4], b[4];
       unpack4(at[v], f);
-      unpack4(at[next + v], g);
-      unpack4(at[2 * next + v], w);
-      unpack4(p.dh ? at[3 * next + v] : make_uint4(0, 0, 0, 0), o);
+      unpack4(at[nvec + v], g);
+      unpack4(at[2 * nvec + v], w);
+      unpack4(p.dh ? at[3 * nvec + v] : make_uint4(0, 0, 0, 0), o);
       weights(i, a, b);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -326,8 +325,8 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
       *(reinterpret_cast<uint4*>(p.dx + t * d) + v) = pack4(o);
     }
     if (p.stages == 1) {
-      __syncthreads();
-      if (threadIdx.x == 0) fill(n + gridDim.x, 0);
+      meet();
+      if (c == 0) fill(t + step, 0);
     }
     flip ^= 1;
     if (++stage == p.stages) {
@@ -335,63 +334,42 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, kBackTh
       phase ^= 1u;
     }
   }
-  __syncthreads();
-  if (gave_up) {  // a copy that did not arrive: nothing more is written
-    if (threadIdx.x == 0) {
-      dmoe::raise_error(p.err, DMOE_SITE_NORM_WAIT | DMOE_ERR_TIMEOUT);
-      volatile int go_on = 0;
-      for (int i = 0; i < p.stages; ++i) {  // the copies still on their way, as far as they come
-        mbar_wait(full + stage, phase, &go_on);
-        if (++stage == p.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+  __syncwarp();
+  if (gave_up[rg] && c == 0) {  // a copy that did not arrive
+    dmoe::raise_error(p.err, DMOE_SITE_NORM_WAIT | DMOE_ERR_TIMEOUT);
+    volatile int go_on = 0;
+    for (int i = 0; i < p.stages; ++i) {  // the copies still on their way, as far as they come
+      mbar_wait(&full[rg][stage], phase, &go_on);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
-    return;
   }
   if (!p.partial) return;
-  if (RPB > 1) {
-    float2* sh = reinterpret_cast<float2*>(ring);  // [RPB - 1][2 d] floats: every unit has been read
-    if (rg > 0) {
+  __syncthreads();  // every row has been read
+  float* sums = reinterpret_cast<float*>(ring);  // [GROUPS][2 d]
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = c + i * TPR;
-        if (v >= nvec) continue;
-        float2* o = sh + static_cast<int64_t>(rg - 1) * d + 4 * v;
+  for (int i = 0; i < VPT; ++i) {
+    const int v = c + i * TPR;
+    if (v >= nvec) continue;
+    float* o = sums + static_cast<size_t>(rg) * 2 * d + 8 * v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = da[i][j], o[d / 2 + j] = db[i][j];
-      }
-    }
-    __syncthreads();
-    if (rg == 0) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = c + i * TPR;
-        if (v >= nvec) continue;
-        for (int g = 1; g < RPB; ++g) {
-          const float2* o = sh + static_cast<int64_t>(g - 1) * d + 4 * v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            da[i][j] = dmoe::f2_add(da[i][j], o[j]);
-            db[i][j] = dmoe::f2_add(db[i][j], o[d / 2 + j]);
-          }
-        }
-      }
+    for (int j = 0; j < 4; j += 2) {
+      *reinterpret_cast<float4*>(o + 2 * j) = make_float4(da[i][j].x, da[i][j].y, da[i][j + 1].x, da[i][j + 1].y);
+      *reinterpret_cast<float4*>(o + d + 2 * j) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
     }
   }
-  if (rg == 0) {
+  __syncthreads();
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * d;
+  for (int i = threadIdx.x; i < d / 2; i += kBackThreads) {  // four columns of 2 d
+    float4 a = reinterpret_cast<const float4*>(sums)[i];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = c + i * TPR;
-      if (v >= nvec) continue;
-      float* o = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * d + 8 * v;
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        *reinterpret_cast<float4*>(o + 2 * j) = make_float4(da[i][j].x, da[i][j].y, da[i][j + 1].x, da[i][j + 1].y);
-        *reinterpret_cast<float4*>(o + d + 2 * j) = make_float4(db[i][j].x, db[i][j].y, db[i][j + 1].x, db[i][j + 1].y);
-      }
+    for (int g = 1; g < GROUPS; ++g) {
+      const float4 q = reinterpret_cast<const float4*>(sums + static_cast<size_t>(g) * 2 * d)[i];
+      a.x += q.x, a.y += q.y, a.z += q.z, a.w += q.w;
     }
+    reinterpret_cast<float4*>(out)[i] = a;
   }
 }
 
@@ -458,20 +436,11 @@ cudaError_t by_width(int d, const F& f) {
   }
 }
 
-int back_block(int d) { return std::max(kMinThreads, threads_per_row(d)); }
-int back_rows(int d) { return back_block(d) / threads_per_row(d); }
-size_t unit_bytes(int d) { return static_cast<size_t>(back_rows(d)) * d * 2 * 4; }
-int blocks_per_sm(int d) { return kBackThreads / back_block(d); }
-int ring_stages(int d) {
-  return static_cast<int>(std::clamp<size_t>(kRingBytes / blocks_per_sm(d) / unit_bytes(d), 1, kMaxStages));
-}
+size_t back_stage_bytes(int d) { return static_cast<size_t>(kBackThreads / threads_per_row(d)) * d * 2 * 4; }
+int ring_stages(int d) { return static_cast<int>(std::clamp<size_t>(kRingBytes / back_stage_bytes(d), 1, kMaxStages)); }
 
-// Blocks of the backward: what is resident, each leaving one partial row.
-int backward_blocks(int T, int d, int sms) {
-  const int rpb = back_rows(d);
-  const int64_t need = (static_cast<int64_t>(T) + rpb - 1) / rpb;
-  return static_cast<int>(std::min<int64_t>(need, static_cast<int64_t>(sms) * blocks_per_sm(d)));
-}
+// Blocks of the backward: one an SM, each leaving one partial row.
+int backward_blocks(int T, int sms) { return std::min(T, sms); }
 
 struct Forward {
   const uint16_t* u;
@@ -508,9 +477,8 @@ struct Backward {
 
   template <int TPR, int VPT, bool WF32>
   cudaError_t launch() const {
-    constexpr int block = TPR > kMinThreads ? TPR : kMinThreads;
     auto kern = sandwich_norm_backward_kernel<TPR, VPT, WF32>;
-    // the ring also holds the row groups' sums: (RPB - 1) x 2 fp32 rows in 4 RPB bf16 ones
+    // the ring also holds the groups' sums: two fp32 rows each where four bf16 ones were
     static std::atomic<uint64_t> opted{0};
     const uint64_t bit = uint64_t(1) << device;
     if (!(opted.load(std::memory_order_acquire) & bit)) {
@@ -519,7 +487,7 @@ struct Backward {
       if (e != cudaSuccess) return e;
       opted.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return dmoe::launch_pdl(kern, dim3(blocks), dim3(block), p.stages * unit_bytes(p.d), st, p);
+    return dmoe::launch_pdl(kern, dim3(blocks), dim3(kBackThreads), p.stages * back_stage_bytes(p.d), st, p);
   }
 
   template <int TPR, int VPT>
@@ -561,7 +529,7 @@ DMOE_API dmoe_status dmoe_sandwich_norm(const uint16_t* u, int64_t ldu, const ui
 DMOE_API size_t dmoe_sandwich_norm_backward_workspace_size(int T, int d) {
   dmoe::DeviceInfo di;
   if (T < 0 || d < 8 || (d & 7) || d > kMaxD || dmoe::device_info(&di) != DMOE_OK) return 0;
-  return (static_cast<size_t>(backward_blocks(T, d, di.sm_count)) * 2 * d + T) * sizeof(float);
+  return (static_cast<size_t>(backward_blocks(T, di.sm_count)) * 2 * d + T) * sizeof(float);
 }
 
 DMOE_API dmoe_status dmoe_sandwich_norm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* u, int64_t ldu,
@@ -597,7 +565,7 @@ DMOE_API dmoe_status dmoe_sandwich_norm_backward(const uint16_t* dy, int64_t ldd
     if (e == cudaSuccess && shared) e = cudaMemsetAsync(d_gate, 0, sizeof(float), st);
     return dmoe::cuda_status(e);
   }
-  const int blocks = backward_blocks(T, d, di.sm_count);
+  const int blocks = backward_blocks(T, di.sm_count);
   const size_t part = static_cast<size_t>(blocks) * 2 * d;
   const bool sums = dw_post || dw_pre;
   if ((sums || shared) && (!ws || ws_bytes < (part + T) * sizeof(float))) return DMOE_ERR_INVALID_ARG;
