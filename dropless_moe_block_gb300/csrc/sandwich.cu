@@ -172,7 +172,7 @@ __device__ __forceinline__ float three_sums(const float* s, int lane) {
 // and two vectors a thread, so that the sums' meeting costs a quarter of them
 // (8192 x 4096: 99 us with one vector and value by value, 71 so; 8191 x 512,
 // with blocks of four rows that wait for one another and leave 608 partial
-// rows, 19 us, TBD with groups).
+// rows, 19 us, 17.7 with groups).
 template <int TPR, int VPT, bool WF32>
 __global__ void __launch_bounds__(kBackThreads, 1) sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
   using namespace dmoe::tc;
