@@ -7,8 +7,10 @@
 //   of their experts the k largest c;  w = s (/ their sum) * scale
 //
 // One warp per token, lane l with experts l, l + 32, ....  16381 tokens of 256
-// experts are 17 MB, 3 us of HBM: what bounds it are instructions, so the
-// choice works on 31-bit keys, a choice's place in its range and under it the
+// experts are 17 MB, 3 us of HBM, and take 25: what bounds it are some 1080
+// instructions a token (70% of the issue slots while an SM is busy; 21 us), and
+// behind them the last of the tokens decided twice.  So the choice works on
+// 31-bit keys, a choice's place in its range and under it the
 // expert's register, such that one integer reduction over the warp finds the
 // best and where it lies.
 //
@@ -241,10 +243,18 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
       m = fmaxf(m, z[i]);
     }
     if (!sig || !biased) m = warp_max(m);
-    float inv = 1.f;  // of the softmax's sum
+    float weigh = 0.f;  // what exponentials become weights by, where the whole softmax does
+    if (!sig && !p.renorm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) sum += expf(z[i] - m);
+      sum = warp_sum(sum);
+      weigh = sum > 0.f ? p.scale / sum : 0.f;
+    }
     uint32_t key[NPL];
     float step = 0.f, s[NPL];
     if (GROUPS || biased) {
+      float inv = 1.f;  // of the softmax's sum
       if (sig) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
@@ -260,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
 #pragma unroll
         for (int i = 0; i < NPL; ++i) s[i] *= inv;
       }
-      const float range = most + (sig ? 1.f : inv);  // a softmax's largest score is its largest exponential's, 1
+      const float range = most + inv;  // a softmax's largest score is its largest exponential's, 1
       step = range * 2.3841858e-7f;
       const float half = 0.49999f / range;  // all numbers' places lie above 1
 #pragma unroll
@@ -346,9 +356,13 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
 
     int32_t* out_i = p.expert_idx + t * p.k;
     float* out_w = p.gate_w + t * p.k;
-    uint32_t own = 0;  // this lane's best
+    uint32_t own = 0, second = 0;  // this lane's best two
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) own = max(own, key[i]);
+    for (int i = 0; i < NPL; ++i) {
+      second = max(second, min(own, key[i]));
+      own = max(own, key[i]);
+    }
+    uint32_t used = 0;  // lanes whose second one has come up: behind it they look again
     uint32_t last = kFull, gap = kFull;  // gap: the smallest between neighbours
     int mine = 0;                        // slot `lane`'s expert
     int n = 0;                           // slots taken: k, and those behind whose order with the last is open
@@ -359,11 +373,16 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
       const int e = static_cast<int>(31 - (best & 31)) * 32 + src;
       if (n < 32) mine = lane == n ? e : mine;
       else if (lane == (n & 31)) out_i[n] = e;
-      uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
+      if ((used >> src) & 1u) {
+        uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
-      next = next & 0x80000000u ? next + best : 0u;
-      own = lane == src ? next : own;
+        for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
+        next = next & 0x80000000u ? next + best : 0u;
+        own = lane == src ? next : own;
+      } else {
+        own = lane == src ? second : own;
+        used |= 1u << src;
+      }
       best = __reduce_max_sync(kFull, own);
       gap = min(gap, last - best);
       ++n;
@@ -397,12 +416,6 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
     if (p.renorm) {
       for (int j = lane; j < p.k; j += 32) top = fmaxf(top, clean(__ldg(row + (j < 32 ? mine : out_i[j]))));
       top = warp_max(top);
-    } else if (!sig) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) sum += expf(z[i] - m);
-      sum = warp_sum(sum);
-      inv = sum > 0.f ? 1.f / sum : 0.f;
     }
     float sum = 0.f, only = 0.f;
     for (int j = lane; j < p.k; j += 32) {
@@ -410,9 +423,9 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
       if (j < 32) out_i[j] = e;
       const float v = clean(__ldg(row + e));
       float w = 0.f;
-      if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) : expf(v - m) * inv;
+      if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) * p.scale : expf(v - m) * weigh;
       sum += w;
-      if (!p.renorm) out_w[j] = w * p.scale;
+      if (!p.renorm) out_w[j] = w;
       else if (p.k > 32) out_w[j] = w;
       else only = w;
     }
@@ -564,8 +577,8 @@ struct ForwardCall {
   }
   template <int NPL, bool FULL>
   cudaError_t launch() const {
-    const int resident = sms * (NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2);
-    const dim3 grid(std::min<unsigned>(grid_of(p.T).x, static_cast<unsigned>(resident))), block(kWarps * 32);
+    const unsigned resident = static_cast<unsigned>(sms * (NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2));
+    const dim3 grid(std::min(grid_of(p.T).x, resident)), block(kWarps * 32);
     if (p.top_groups == p.groups) return dmoe::launch_pdl(route_balanced_kernel<NPL, false, FULL>, grid, block, 0, st, p);
     const size_t smem = sizeof(float) * kWarps * p.groups * p.stride;  // at most (1024 + 32) * 32 bytes
     return dmoe::launch_pdl(route_balanced_kernel<NPL, true, FULL>, grid, block, smem, st, p);
