@@ -696,6 +696,49 @@ def _apart_or_same(p, n, name, *others):
             raise ValueError(f"{name} must not overlap {other}")
 
 
+def _device(t, name):
+    """The current device, which has to be the tensor's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} lies on device {dev}, the current one is {torch.cuda.current_device()}")
+    return dev
+
+
+def _is(t, dev, dtype, name, shape):
+    """Refuses what is not a contiguous tensor of that type and shape there."""
+    if (t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return
+    _need(t, dtype, name, shape=shape)
+    raise ValueError(f"{name} lies on device {t.get_device()}, the current one is {dev}")
+
+
+def _pitch(t, dev, dtype, name, shape):
+    """Row pitch of a matrix whose rows may lie apart."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return shape[1]
+    ld = _rows(t, dtype, name, *shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on device {t.get_device()}, the current one is {dev}")
+    return ld
+
+
+def _workspace(ws, dev):
+    _need(ws, torch.uint8, "ws")
+    if ws.get_device() != dev:
+        raise ValueError(f"ws lies on device {ws.get_device()}, the current one is {dev}")
+    return ws.numel()
+
+
+def _bf16_or_f32(t, dev, name, shape):
+    """Whether a tensor is fp32; bf16 otherwise."""
+    if t is None or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32" + ("" if t is None else f", got {t.dtype}"))
+    _is(t, dev, t.dtype, name, shape)
+    return int(t.dtype is torch.float32)
+
+
 def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = "softmax", groups: int = 1,
                    top_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
     """Choice of k experts a token by softmax or sigmoid scores plus ``bias``
@@ -705,54 +748,58 @@ def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = 
     (``renormalize``), times ``scale``.  Ties go to the lower expert; candidates
     that fp32 cannot tell apart are compared in 64 bits."""
     T, E = logits.shape
-    _need(logits, torch.float32, "logits")
+    dev = _device(logits, "logits")
+    _is(logits, dev, torch.float32, "logits", (T, E))
     if bias is not None:
-        _need(bias, torch.float32, "bias", shape=(E,))
-    _need(expert_idx, torch.int32, "expert_idx", shape=(T, k))
-    _need(gate_w, torch.float32, "gate_w", shape=(T, k))
+        _is(bias, dev, torch.float32, "bias", (E,))
+    _is(expert_idx, dev, torch.int32, "expert_idx", (T, k))
+    _is(gate_w, dev, torch.float32, "gate_w", (T, k))
     _check("dmoe_route_balanced", lib().dmoe_route_balanced(
-        _ptr(logits), _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
-        int(bool(renormalize)), scale, _ptr(expert_idx), _ptr(gate_w), _stream(stream)))
+        logits.data_ptr(), _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
+        int(bool(renormalize)), scale, expert_idx.data_ptr(), gate_w.data_ptr(), _stream(stream)))
 
 
 def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = "softmax", renormalize: bool = True,
                             scale: float = 1.0, stream=None):
     """Gradient of ``route_balanced``'s weights with respect to the logits (the
-    bias has none)."""
+    bias has none).  ``expert_idx`` holds distinct experts for each token."""
     T, E = logits.shape
     k = expert_idx.shape[1]
-    _need(logits, torch.float32, "logits")
-    _need(expert_idx, torch.int32, "expert_idx", shape=(T, k))
-    _need(d_gate, torch.float32, "d_gate", shape=(T, k))
-    _need(d_logits, torch.float32, "d_logits", shape=(T, E))
+    dev = _device(logits, "logits")
+    _is(logits, dev, torch.float32, "logits", (T, E))
+    _is(expert_idx, dev, torch.int32, "expert_idx", (T, k))
+    _is(d_gate, dev, torch.float32, "d_gate", (T, k))
+    _is(d_logits, dev, torch.float32, "d_logits", (T, E))
+    lp, op, n = logits.data_ptr(), d_logits.data_ptr(), 4 * T * E
+    _apart_from(op, n, "d_logits", (lp, n, "logits"))
     _check("dmoe_route_balanced_backward", lib().dmoe_route_balanced_backward(
-        _ptr(logits), _ptr(expert_idx), _ptr(d_gate), T, E, k, _name(_SCORES, scores, "scores"),
-        int(bool(renormalize)), scale, _ptr(d_logits), _stream(stream)))
+        lp, expert_idx.data_ptr(), d_gate.data_ptr(), T, E, k, _name(_SCORES, scores, "scores"), int(bool(renormalize)),
+        scale, op, _stream(stream)))
 
 
 def balance_bias(bias, tokens_per_expert, rate: float, stream=None):
     """bias += rate * sign(mean load - load), in place: after a step, with the
     loads (int32 [E]) that its permutation counted."""
     E = bias.shape[0]
-    _need(bias, torch.float32, "bias", shape=(E,))
-    _need(tokens_per_expert, torch.int32, "tokens_per_expert", shape=(E,))
+    dev = _device(bias, "bias")
+    _is(bias, dev, torch.float32, "bias", (E,))
+    _is(tokens_per_expert, dev, torch.int32, "tokens_per_expert", (E,))
     _check("dmoe_balance_bias", lib().dmoe_balance_bias(_ptr(bias), _ptr(tokens_per_expert), E, rate, _stream(stream)))
 
 
-def _norm_weights(w_post, w_pre, d):
-    wf = _norm_weight(w_post, d)
-    if _norm_weight(w_pre, d) != wf:
+def _norm_weights(w_post, w_pre, dev, d):
+    wf = _bf16_or_f32(w_post, dev, "w_post", (d,))
+    if _bf16_or_f32(w_pre, dev, "w_pre", (d,)) != wf:
         raise ValueError("w_post and w_pre must have the same type")
     return wf
 
 
-def _gate(gate, T):
+def _gate(gate, dev, T):
     if gate is None:
         return 0
-    _need(gate, torch.float32, "gate")
-    if gate.shape not in ((T,), (1,)):
-        raise ValueError(f"gate must have shape {(T,)} or (1,), got {tuple(gate.shape)}")
-    return gate.shape[0]
+    n = 1 if gate.shape == (1,) else T
+    _is(gate, dev, torch.float32, "gate", (n,))
+    return n
 
 
 def sandwich_norm(u, residual, w_post, w_pre, eps: float, h, y, gate=None, scale: float = 1.0, rstd_u=None,
@@ -764,17 +811,19 @@ def sandwich_norm(u, residual, w_post, w_pre, eps: float, h, y, gate=None, scale
     tensors; ``h`` and ``y`` may each be one of them that is contiguous, but not
     the same one.  ``rstd_u`` and ``rstd_h`` (fp32 [T]) are what the backward
     reads."""
-    T, d = u.shape
-    ldu = _rows(u, torch.bfloat16, "u", T, d)
-    ldr = _rows(residual, torch.bfloat16, "residual", T, d)
-    wf = _norm_weights(w_post, w_pre, d)
-    n = _gate(gate, T)
-    _need(h, torch.bfloat16, "h", shape=(T, d))
-    _need(y, torch.bfloat16, "y", shape=(T, d))
+    shape = T, d = u.shape
+    bf = torch.bfloat16
+    dev = _device(u, "u")
+    ldu = _pitch(u, dev, bf, "u", shape)
+    ldr = _pitch(residual, dev, bf, "residual", shape)
+    wf = _norm_weights(w_post, w_pre, dev, d)
+    n = _gate(gate, dev, T)
+    _is(h, dev, bf, "h", shape)
+    _is(y, dev, bf, "y", shape)
     if rstd_u is not None:
-        _need(rstd_u, torch.float32, "rstd_u", shape=(T,))
+        _is(rstd_u, dev, torch.float32, "rstd_u", (T,))
     if rstd_h is not None:
-        _need(rstd_h, torch.float32, "rstd_h", shape=(T,))
+        _is(rstd_h, dev, torch.float32, "rstd_h", (T,))
     up, rp, hp, yp = u.data_ptr(), residual.data_ptr(), h.data_ptr(), y.data_ptr()
     nb = 2 * T * d
     reads = (up, 2 * ((T - 1) * ldu + d), "u"), (rp, 2 * ((T - 1) * ldr + d), "residual")
@@ -782,7 +831,7 @@ def sandwich_norm(u, residual, w_post, w_pre, eps: float, h, y, gate=None, scale
     _apart_or_same(hp, nb, "h", *reads)
     _apart_or_same(yp, nb, "y", *reads)
     _check("dmoe_sandwich_norm", lib().dmoe_sandwich_norm(
-        up, ldu, rp, ldr, _ptr(w_post), _ptr(w_pre), wf, _ptr(gate), n, scale, eps, T, d, hp, yp, _ptr(rstd_u),
+        up, ldu, rp, ldr, w_post.data_ptr(), w_pre.data_ptr(), wf, _ptr(gate), n, scale, eps, T, d, hp, yp, _ptr(rstd_u),
         _ptr(rstd_h), _stream(stream)))
 
 
@@ -794,28 +843,33 @@ def sandwich_norm_backward(dy, u, h, w_post, w_pre, rstd_u, rstd_h, du, dresidua
                            gate=None, d_gate=None, scale: float = 1.0, stream=None):
     """Gradient of ``sandwich_norm``: du, dresidual (with the stream's own
     gradient ``dh`` added before its scale), dw_post and dw_pre (fp32 [d]) and
-    d_gate (fp32, the gate's shape); the last three may be None."""
-    T, d = dy.shape
-    lddy = _rows(dy, torch.bfloat16, "dy", T, d)
-    ldu = _rows(u, torch.bfloat16, "u", T, d)
-    _need(h, torch.bfloat16, "h", shape=(T, d))
-    wf = _norm_weights(w_post, w_pre, d)
-    n = _gate(gate, T)
-    _need(rstd_u, torch.float32, "rstd_u", shape=(T,))
-    _need(rstd_h, torch.float32, "rstd_h", shape=(T,))
-    lddh = 0 if dh is None else _rows(dh, torch.bfloat16, "dh", T, d)
-    _need(du, torch.bfloat16, "du", shape=(T, d))
-    _need(dresidual, torch.bfloat16, "dresidual", shape=(T, d))
-    for name, t in (("dw_post", dw_post), ("dw_pre", dw_pre)):
-        if t is not None:
-            _need(t, torch.float32, name, shape=(d,))
+    d_gate (fp32, the gate's shape); the last three may be None.  ``du`` and
+    ``dresidual`` may each be dy, u, h or dh, if that is contiguous, but not the
+    same one."""
+    shape = T, d = dy.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = _device(dy, "dy")
+    lddy = _pitch(dy, dev, bf, "dy", shape)
+    ldu = _pitch(u, dev, bf, "u", shape)
+    lddh = 0 if dh is None else _pitch(dh, dev, bf, "dh", shape)
+    _is(h, dev, bf, "h", shape)
+    wf = _norm_weights(w_post, w_pre, dev, d)
+    n = _gate(gate, dev, T)
+    _is(rstd_u, dev, f32, "rstd_u", (T,))
+    _is(rstd_h, dev, f32, "rstd_h", (T,))
+    _is(du, dev, bf, "du", shape)
+    _is(dresidual, dev, bf, "dresidual", shape)
+    if dw_post is not None:
+        _is(dw_post, dev, f32, "dw_post", (d,))
+    if dw_pre is not None:
+        _is(dw_pre, dev, f32, "dw_pre", (d,))
     if d_gate is not None:
         if gate is None:
             raise ValueError("d_gate needs a gate")
-        _need(d_gate, torch.float32, "d_gate", shape=gate.shape)
+        _is(d_gate, dev, f32, "d_gate", (n,))
     nws = 0
     if dw_post is not None or dw_pre is not None or (d_gate is not None and n == 1):
-        nws = _need(ws, torch.uint8, "ws").numel()
+        nws = _workspace(ws, dev)
     dyp, up, hp, dhp, dup, dxp = dy.data_ptr(), u.data_ptr(), h.data_ptr(), _ptr(dh), du.data_ptr(), dresidual.data_ptr()
     nb = 2 * T * d
     reads = ((dyp, 2 * ((T - 1) * lddy + d), "dy"), (up, 2 * ((T - 1) * ldu + d), "u"), (hp, nb, "h"),
@@ -824,8 +878,9 @@ def sandwich_norm_backward(dy, u, h, w_post, w_pre, rstd_u, rstd_h, du, dresidua
     _apart_or_same(dup, nb, "du", *reads)
     _apart_or_same(dxp, nb, "dresidual", *reads)
     _check("dmoe_sandwich_norm_backward", lib().dmoe_sandwich_norm_backward(
-        dyp, lddy, up, ldu, hp, _ptr(w_post), _ptr(w_pre), wf, _ptr(gate), n, scale, _ptr(rstd_u), _ptr(rstd_h), dhp,
-        lddh, T, d, dup, dxp, _ptr(dw_post), _ptr(dw_pre), _ptr(d_gate), _ptr(ws), nws, _stream(stream)))
+        dyp, lddy, up, ldu, hp, w_post.data_ptr(), w_pre.data_ptr(), wf, _ptr(gate), n, scale, rstd_u.data_ptr(),
+        rstd_h.data_ptr(), dhp, lddh, T, d, dup, dxp, _ptr(dw_post), _ptr(dw_pre), _ptr(d_gate), _ptr(ws), nws,
+        _stream(stream)))
 
 
 def linear_workspace_size(M: int, K: int, N: int) -> int:
@@ -840,22 +895,19 @@ def linear(x, w, y, ws, bias=None, act: str = "none", deriv=None, residual=None,
     ``ws``: uint8, linear_workspace_size() bytes."""
     M, K = x.shape
     N = w.shape[1]
-    ldx = _rows(x, torch.bfloat16, "x", M, K)
-    _need(w, torch.bfloat16, "w", shape=(K, N))
-    _need(y, torch.bfloat16, "y", shape=(M, N))
-    _need(ws, torch.uint8, "ws")
-    bf = 0
-    if bias is not None:
-        if bias.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"bias must be torch.bfloat16 or torch.float32, got {bias.dtype}")
-        bf = int(bias.dtype == torch.float32)
-        _need(bias, bias.dtype, "bias", shape=(N,))
+    bf = torch.bfloat16
+    dev = _device(x, "x")
+    ldx = _pitch(x, dev, bf, "x", (M, K))
+    _is(w, dev, bf, "w", (K, N))
+    _is(y, dev, bf, "y", (M, N))
+    nws = _workspace(ws, dev)
+    b32 = 0 if bias is None else _bf16_or_f32(bias, dev, "bias", (N,))
     a = _name(_ACTS, act, "act")
     if deriv is not None:
         if a == 0:
             raise ValueError("deriv needs an activation")
-        _need(deriv, torch.bfloat16, "deriv", shape=(M, N))
-    ldr = 0 if residual is None else _rows(residual, torch.bfloat16, "residual", M, N)
+        _is(deriv, dev, bf, "deriv", (M, N))
+    ldr = 0 if residual is None else _pitch(residual, dev, bf, "residual", (M, N))
     xp, wp, rp, yp, fp = x.data_ptr(), w.data_ptr(), _ptr(residual), y.data_ptr(), _ptr(deriv)
     nb = 2 * M * N
     reads = (xp, 2 * ((M - 1) * ldx + K), "x"), (wp, 2 * K * N, "w")
@@ -865,7 +917,7 @@ def linear(x, w, y, ws, bias=None, act: str = "none", deriv=None, residual=None,
     _apart_from(yp, nb, "y", *reads)
     _apart_or_same(yp, nb, "y", added)
     _check("dmoe_linear", lib().dmoe_linear(
-        xp, ldx, wp, _ptr(bias), bf, a, rp, ldr, M, K, N, yp, fp, _ptr(ws), ws.numel(), _stream(stream)))
+        xp, ldx, wp, _ptr(bias), b32, a, rp, ldr, M, K, N, yp, fp, ws.data_ptr(), nws, _stream(stream)))
 
 
 def linear_backward_workspace_size(M: int, K: int, N: int) -> int:
@@ -875,42 +927,43 @@ def linear_backward_workspace_size(M: int, K: int, N: int) -> int:
 def linear_backward(dy, x, w, dx, dw, ws, deriv=None, dbias=None, factor=None, stream=None):
     """Gradient of ``linear``: with dz = dy * deriv, dx = (dz . w^T) * factor,
     dw = x^T . dz (bf16 or fp32) and dbias = the sum of dz's rows (fp32 [N]);
-    each may be None.  The residual's gradient is dy.  ``factor`` (bf16 [M, K])
-    is the ``deriv`` of the layer that made x; dx is then that layer's dz, to be
-    given to its backward as ``dy``, with no deriv.  ``dx`` may be ``factor``."""
+    each may be None (``x`` too where no dw is asked for).  The residual's
+    gradient is dy.  ``factor`` (bf16 [M, K]) is the ``deriv`` of the layer that
+    made x; dx is then that layer's dz, to be given to its backward as ``dy``,
+    with no deriv.  ``dx`` may be ``factor``."""
     M, N = dy.shape
     K = w.shape[0]
-    lddy = _rows(dy, torch.bfloat16, "dy", M, N)
-    _need(w, torch.bfloat16, "w", shape=(K, N))
-    ldx = 0
+    bf = torch.bfloat16
+    dev = _device(dy, "dy")
+    lddy = _pitch(dy, dev, bf, "dy", (M, N))
+    _is(w, dev, bf, "w", (K, N))
+    ldx = K
     if dw is not None or x is not None:
-        ldx = _rows(x, torch.bfloat16, "x", M, K)
-    nws = _need(ws, torch.uint8, "ws").numel()
+        ldx = _pitch(x, dev, bf, "x", (M, K))
+    nws = _workspace(ws, dev)
     if deriv is not None:
-        _need(deriv, torch.bfloat16, "deriv", shape=(M, N))
+        _is(deriv, dev, bf, "deriv", (M, N))
     if factor is not None:
         if dx is None:
             raise ValueError("factor needs dx")
-        _need(factor, torch.bfloat16, "factor", shape=(M, K))
+        _is(factor, dev, bf, "factor", (M, K))
     dyp, xp, wp, fp, kp, dxp, dwp = (dy.data_ptr(), _ptr(x), w.data_ptr(), _ptr(deriv), _ptr(factor), _ptr(dx), _ptr(dw))
     reads = ((dyp, 2 * ((M - 1) * lddy + N), "dy"), (xp, 2 * ((M - 1) * ldx + K), "x"), (wp, 2 * K * N, "w"),
              (fp, 2 * M * N, "deriv"))
     made = kp, 2 * M * K, "factor"
-    f32 = 0
+    f32, nw = 0, 0
     if dw is not None:
-        if dw.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"dw must be torch.bfloat16 or torch.float32, got {dw.dtype}")
-        f32 = int(dw.dtype == torch.float32)
-        _need(dw, dw.dtype, "dw", shape=(K, N))
-        _apart_from(dwp, (4 if f32 else 2) * K * N, "dw", *reads, made)
+        f32 = _bf16_or_f32(dw, dev, "dw", (K, N))
+        nw = (4 if f32 else 2) * K * N
+        _apart_from(dwp, nw, "dw", *reads, made)
     if dx is not None:
-        _need(dx, torch.bfloat16, "dx", shape=(M, K))
-        _apart_from(dxp, 2 * M * K, "dx", *reads, (dwp, (4 if f32 else 2) * K * N, "dw"))
+        _is(dx, dev, bf, "dx", (M, K))
+        _apart_from(dxp, 2 * M * K, "dx", *reads, (dwp, nw, "dw"))
         _apart_or_same(dxp, 2 * M * K, "dx", made)
     if dbias is not None:
-        _need(dbias, torch.float32, "dbias", shape=(N,))
+        _is(dbias, dev, torch.float32, "dbias", (N,))
     _check("dmoe_linear_backward", lib().dmoe_linear_backward(
-        dyp, lddy, fp, xp, ldx, wp, kp, M, K, N, dxp, dwp, f32, _ptr(dbias), _ptr(ws), nws, _stream(stream)))
+        dyp, lddy, fp, xp, ldx, wp, kp, M, K, N, dxp, dwp, f32, _ptr(dbias), ws.data_ptr(), nws, _stream(stream)))
 
 
 # ----------------------------------------------------------------- whole layer

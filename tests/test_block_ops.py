@@ -199,6 +199,7 @@ def test_route_masked_and_extreme_logits(dm, scores, renorm, biased, groups, top
     E, k = 16, 6
     top = torch.finfo(F32).max
     inf = math.inf
+    # (a bias of plus infinity forces its expert, one of minus infinity or NaN rules it out)
     rows = [[-inf] * E, [float("nan")] * E, [0.0] + [-inf] * 15, [-inf] * 14 + [1.0, 2.0], [-top] * E,
             [top] * 3 + [-top] * 13, [inf] + [1.0] * 15, [float("nan"), 3.0] * 8, [-200.0 - i for i in range(E)],
             [-100.0 + 3 * i for i in range(E)], [300.0 - i for i in range(E)], [-0.0, 0.0] * 8,
@@ -206,7 +207,7 @@ def test_route_masked_and_extreme_logits(dm, scores, renorm, biased, groups, top
     logits = torch.tensor(rows, device="cuda")
     bias = torch.tensor([0.01 * (i % 5) for i in range(E)], device="cuda") if biased else None
     if biased:
-        bias[3] = -inf
+        bias[3], bias[7], bias[9] = -inf, float("nan"), inf
     idx, w = route(dm, logits, k, bias=bias, scores=scores, groups=groups, top_groups=top_groups, renormalize=renorm)
     ri, rw = ref_route(logits, bias, k, scores, groups, top_groups, renorm, 1.0)
     assert torch.equal(idx.long(), ri)
