@@ -733,10 +733,11 @@ def _workspace(ws, dev):
 
 def _bf16_or_f32(t, dev, name, shape):
     """Whether a tensor is fp32; bf16 otherwise."""
-    if t is None or t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32" + ("" if t is None else f", got {t.dtype}"))
-    _is(t, dev, t.dtype, name, shape)
-    return int(t.dtype is torch.float32)
+    dtype = None if t is None else t.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+    _is(t, dev, dtype, name, shape)
+    return int(dtype is torch.float32)
 
 
 def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = "softmax", groups: int = 1,

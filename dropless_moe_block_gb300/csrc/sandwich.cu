@@ -34,8 +34,13 @@ constexpr int kMaxStages = 4;              // backward: rows in flight per group
 constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 constexpr int kBackThreads = 512;          // backward: threads per SM, 128 registers each
 
+// Five blocks of 256 threads an SM (48 registers) where a row takes that many:
+// 8192 x 4096 42.2 us, 45.4 with four, 48.2 with six; narrower rows are
+// better off with registers (8192 x 512: 7.8 us with 1024 threads an SM, 8.7 with
+// 1280).
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads, 1024 / (TPR > kMinThreads ? TPR : kMinThreads))
+__global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads,
+                                  TPR == 256 ? 5 : 1024 / (TPR > kMinThreads ? TPR : kMinThreads))
     sandwich_norm_kernel(const uint16_t* u, int64_t ldu, const uint16_t* x, int64_t ldx,
                          const void* __restrict__ w_post, const void* __restrict__ w_pre,
                          const float* __restrict__ gate, int gate_step, float scale, float eps, int T, int d,
