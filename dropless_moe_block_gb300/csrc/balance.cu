@@ -36,6 +36,14 @@ using namespace dmoe::act;
 
 constexpr int kWarps = 8;  // tokens per block
 constexpr int kMaxGroups = 32;
+// Four tokens go to a warp from so many tokens on, or where each takes one
+// expert: then few orders are open.  What is left to the whole warp costs its
+// 6 us however few they are (us, whole warps and four tokens: 64 experts, top-1
+// softmax, 1024 tokens 2.7 and 2.5, 8192 5.5 and 3.5, 32768 17.0 and 7.5; top-8
+// sigmoid, 4096 6.5 and 7.9, 8192 9.1 and 8.2, 32768 24.8 and 12.3; 256 experts
+// in 8 groups, 4096 9.7 and 13.6, 8192 15.3 and 15.2, 16381 24.5 and 22.4, 32768
+// 42.8 and 31.3).
+constexpr int kEighthsFrom = 8192;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -205,23 +213,13 @@ __device__ __forceinline__ uint32_t pack(float v, int i) {
   return ((__float_as_uint(v) - 0x3f800000u + 2u) << 5) + (31 - i);
 }
 
-// A warp walks its tokens with the bias in registers.  FULL: E is 32 NPL.
+// One token by one warp; b: the bias of the lane's experts, most: the largest
+// finite one in magnitude, mem: room for the groups' scores.  FULL: E is 32 NPL.
 template <int NPL, bool GROUPS, bool FULL>
-__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
-    route_balanced_kernel(const __grid_constant__ Choice p) {
-  extern __shared__ float group_mem[];  // [kWarps][groups * stride]
-  dmoe::pdl_wait();
-  dmoe::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void route_by_warp(const Choice& p, int64_t t, const float (&b)[NPL], float most, float* mem,
+                                              int lane) {
   const bool sig = p.sig, biased = p.bias != nullptr;
   auto there = [&](int i) { return FULL || i * 32 + lane < p.E; };
-  float b[NPL], most = 0.f;  // the largest finite bias, in magnitude
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    b[i] = biased && there(i) ? __ldg(p.bias + i * 32 + lane) : 0.f;
-    most = fmaxf(most, fabsf(b[i]) < INFINITY ? fabsf(b[i]) : 0.f);
-  }
-  most = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
   // Steps that two keys may be off by together.  Without a bias: places by the
   // logit's distance from the largest, monotone, so only equal ones are open.
   // With one, in steps of 2^-22 of the range: a sigmoid is off by 1 (its
@@ -230,210 +228,466 @@ __global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
   // lane's NPL terms, five more, and its inverse).
   const float open_steps = sig ? 6.f : 10.f + NPL / 4;
   const uint32_t tol = (biased ? (sig ? 6u : 10u + NPL / 4) << 5 : 0u) + 31;
-
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const float* row = p.logits + t * p.E;
-    float z[NPL], m = -FLT_MAX;
+  const float* row = p.logits + t * p.E;
+  float z[NPL], m = -FLT_MAX;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) z[i] = there(i) ? __ldg(row + i * 32 + lane) : -INFINITY;
+  for (int i = 0; i < NPL; ++i) z[i] = there(i) ? __ldg(row + i * 32 + lane) : -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      z[i] = clean(z[i]);
-      m = fmaxf(m, z[i]);
-    }
-    if (!sig || !biased) m = warp_max(m);
-    float weigh = 0.f;  // what exponentials become weights by, where the whole softmax does
-    if (!sig && !p.renorm) {
+  for (int i = 0; i < NPL; ++i) {
+    z[i] = clean(z[i]);
+    m = fmaxf(m, z[i]);
+  }
+  if (!sig || !biased) m = warp_max(m);
+  float weigh = 0.f;  // what exponentials become weights by, where the whole softmax does
+  if (!sig && !p.renorm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) sum += expf(z[i] - m);
+    sum = warp_sum(sum);
+    weigh = sum > 0.f ? p.scale / sum : 0.f;
+  }
+  uint32_t key[NPL];
+  float step = 0.f, s[NPL];
+  if (GROUPS || biased) {
+    float inv = 1.f;  // of the softmax's sum
+    if (sig) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
+    } else {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) sum += expf(z[i] - m);
+      for (int i = 0; i < NPL; ++i) {
+        s[i] = ex2_approx((z[i] - m) * kLog2e);
+        sum += s[i];
+      }
       sum = warp_sum(sum);
-      weigh = sum > 0.f ? p.scale / sum : 0.f;
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) s[i] *= inv;
     }
-    uint32_t key[NPL];
-    float step = 0.f, s[NPL];
-    if (GROUPS || biased) {
-      float inv = 1.f;  // of the softmax's sum
-      if (sig) {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = rcp_approx(1.f + ex2_approx(z[i] * -kLog2e));
-      } else {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-          s[i] = ex2_approx((z[i] - m) * kLog2e);
-          sum += s[i];
-        }
-        sum = warp_sum(sum);
-        inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] *= inv;
-      }
-      const float range = most + inv;  // a softmax's largest score is its largest exponential's, 1
-      step = range * 2.3841858e-7f;
-      const float half = 0.49999f / range;  // all numbers' places lie above 1
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        s[i] = z[i] == -INFINITY ? -INFINITY : fmaxf(s[i] + b[i], -INFINITY);  // the choice; NaN is minus infinity
-        key[i] = pack(fmaxf(fminf(fmaf(s[i], half, 1.5f), 2.f), kMaskedPlace), i);
-      }
-    }
-    if (!biased) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        key[i] = pack(z[i] == -INFINITY ? kMaskedPlace : fmaxf(fmaf(z[i] - m, 1.f / 32.f, 2.f), 1.f), i);
-    }
-    if (!FULL) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (!there(i)) key[i] = 0;
-    }
-
-    double total = -1.0;  // the softmax's sum in 64 bits, once it is needed
-    // Rows whose experts are all alike (padding) are in order already.
-    auto rows_alike = [&]() {
-      bool alike = true;
-      const float z0 = clean(__ldg(row)), b0 = biased ? __ldg(p.bias) : 0.f;
-#pragma unroll 1
-      for (int e = lane; e < p.E; e += 32) alike &= clean(__ldg(row + e)) == z0 && (!biased || __ldg(p.bias + e) == b0);
-      return __all_sync(kFull, alike) != 0;
-    };
-    auto exactly = [&](int e) {
-      return exact_choice(clean(__ldg(row + e)), biased ? __ldg(p.bias + e) : 0.f, sig, m, total);
-    };
-    auto need_total = [&]() {
-      if (!sig && total < 0.0) total = exact_total(row, p.E, lane, m);
-    };
-    if (GROUPS) {
-      float* mem = group_mem + (threadIdx.x >> 5) * p.groups * p.stride;
-      const int pad = p.stride - p.size;
-      int at[NPL];
-      __syncwarp();  // the last token's have been read
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        at[i] = static_cast<int>((e * p.inv_size) >> 20);
-        if (there(i)) mem[e + at[i] * pad] = s[i];
-      }
-      __syncwarp();
-      const int g = lane / p.lanes, r = lane & (p.lanes - 1);
-      const float* mine = mem + g * p.stride;
-      float first = -INFINITY, second = -INFINITY;
-      if (g < p.groups) {
-#pragma unroll 4
-        for (int o = r; o < p.size; o += p.lanes) top_two(mine[o], first, second);
-      }
-      const float worth = group_worth(first, second, p.lanes);
-      int rank = group_rank(worth, g, p.groups, p.lanes, lane);
-      bool stays = rank < p.top_groups && g < p.groups;
-      // the worst that stays against the best that goes
-      const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
-      const float high = float_of(__reduce_max_sync(kFull, g < p.groups && !stays ? key_of(worth) : 0u));
-      const float open = open_steps * step;  // as far as two choices may be off
-      if (low - high <= 2.f * open && !rows_alike()) {
-        // the groups' two best in 64 bits: of those that may be among them
-        need_total();
-        const float least = second - open;
-        double f = -INFINITY, n = -INFINITY;
-        int o = g < p.groups ? r : p.size;
-        for (;;) {
-          while (o < p.size && !(mine[o] >= least)) o += p.lanes;
-          if (!__any_sync(kFull, o < p.size)) break;
-          if (o < p.size) {
-            top_two(exactly(g * p.size + o), f, n);
-            o += p.lanes;
-          }
-        }
-        rank = group_rank(group_worth(f, n, p.lanes), g, p.groups, p.lanes, lane);
-        stays = rank < p.top_groups && g < p.groups;
-      }
-      const uint32_t lanes_in = __ballot_sync(kFull, stays);
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (!((lanes_in >> ((at[i] * p.lanes) & 31)) & 1u)) key[i] = 0;  // (past the last expert it is 0 already)
-    }
-
-    int32_t* out_i = p.expert_idx + t * p.k;
-    float* out_w = p.gate_w + t * p.k;
-    uint32_t own = 0, second = 0;  // this lane's best two
+    const float range = most + inv;  // a softmax's largest score is its largest exponential's, 1
+    step = range * 2.3841858e-7f;
+    const float half = 0.49999f / range;  // all numbers' places lie above 1
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      second = max(second, min(own, key[i]));
-      own = max(own, key[i]);
+      s[i] = z[i] == -INFINITY ? -INFINITY : fmaxf(s[i] + b[i], -INFINITY);  // the choice; NaN is minus infinity
+      key[i] = pack(fmaxf(fminf(fmaf(s[i], half, 1.5f), 2.f), kMaskedPlace), i);
     }
-    uint32_t used = 0;  // lanes whose second one has come up: behind it they look again
-    uint32_t last = kFull, gap = kFull;  // gap: the smallest between neighbours
-    int mine = 0;                        // slot `lane`'s expert
-    int n = 0;                           // slots taken: k, and those behind whose order with the last is open
-    uint32_t best = __reduce_max_sync(kFull, own);
-    auto take = [&]() {
-      last = best;
-      const int src = __ffs(__ballot_sync(kFull, own == best)) - 1;  // equal keys: the lowest lane has the lowest expert
-      const int e = static_cast<int>(31 - (best & 31)) * 32 + src;
-      if (n < 32) mine = lane == n ? e : mine;
-      else if (lane == (n & 31)) out_i[n] = e;
-      if ((used >> src) & 1u) {
-        uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
+  }
+  if (!biased) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
-        next = next & 0x80000000u ? next + best : 0u;
-        own = lane == src ? next : own;
-      } else {
-        own = lane == src ? second : own;
-        used |= 1u << src;
-      }
-      best = __reduce_max_sync(kFull, own);
-      gap = min(gap, last - best);
-      ++n;
-    };
-    while (n < p.k) take();
-    // an order is open between numbers within tol (masked ones go by their place, which the slots below show, too)
-    const bool near = gap <= tol;
-    while (last - best <= tol && best >= 2 * kMasked && n < 32) take();
-    if (near && !rows_alike()) {
-      if (n < 32) {  // one slot a lane: their order in 64 bits
-        if (biased) need_total();
-        double c = -INFINITY;
-        if (lane < n) c = biased ? exactly(mine) : static_cast<double>(clean(__ldg(row + mine)));
-        int rank = 0;
-#pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const double v = __shfl_sync(kFull, c, j);
-          const int e = __shfl_sync(kFull, mine, j);
-          rank += v > c || (v == c && e < mine);
-        }
-        if (lane < n && rank < p.k) out_i[rank] = mine;
-        __syncwarp();
-      } else {
-        choose_exactly(p, row, lane, m, out_i);
-      }
-      if (lane < p.k) mine = out_i[lane];
-    }
+    for (int i = 0; i < NPL; ++i)
+      key[i] = pack(z[i] == -INFINITY ? kMaskedPlace : fmaxf(fmaf(z[i] - m, 1.f / 32.f, 2.f), 1.f), i);
+  }
+  if (!FULL) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (!there(i)) key[i] = 0;
+  }
 
-    // slot j's weight in lane j mod 32, which wrote its expert
-    float top = -INFINITY;
-    if (p.renorm) {
-      for (int j = lane; j < p.k; j += 32) top = fmaxf(top, clean(__ldg(row + (j < 32 ? mine : out_i[j]))));
-      top = warp_max(top);
+  double total = -1.0;  // the softmax's sum in 64 bits, once it is needed
+  // Rows whose experts are all alike (padding) are in order already.
+  auto rows_alike = [&]() {
+    bool alike = true;
+    const float z0 = clean(__ldg(row)), b0 = biased ? __ldg(p.bias) : 0.f;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) alike &= clean(__ldg(row + e)) == z0 && (!biased || __ldg(p.bias + e) == b0);
+    return __all_sync(kFull, alike) != 0;
+  };
+  auto exactly = [&](int e) {
+    return exact_choice(clean(__ldg(row + e)), biased ? __ldg(p.bias + e) : 0.f, sig, m, total);
+  };
+  auto need_total = [&]() {
+    if (!sig && total < 0.0) total = exact_total(row, p.E, lane, m);
+  };
+  if (GROUPS) {
+    const int pad = p.stride - p.size;
+    int at[NPL];
+    __syncwarp();  // the last token's have been read
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = i * 32 + lane;
+      at[i] = static_cast<int>((e * p.inv_size) >> 20);
+      if (there(i)) mem[e + at[i] * pad] = s[i];
     }
-    float sum = 0.f, only = 0.f;
-    for (int j = lane; j < p.k; j += 32) {
-      const int e = j < 32 ? mine : out_i[j];
-      if (j < 32) out_i[j] = e;
-      const float v = clean(__ldg(row + e));
-      float w = 0.f;
-      if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) * p.scale : expf(v - m) * weigh;
-      sum += w;
-      if (!p.renorm) out_w[j] = w;
-      else if (p.k > 32) out_w[j] = w;
-      else only = w;
+    __syncwarp();
+    const int g = lane / p.lanes, r = lane & (p.lanes - 1);
+    const float* mine = mem + g * p.stride;
+    float first = -INFINITY, second = -INFINITY;
+    if (g < p.groups) {
+#pragma unroll 4
+      for (int o = r; o < p.size; o += p.lanes) top_two(mine[o], first, second);
     }
-    if (p.renorm) {
-      sum = warp_sum(sum);
-      const float f = sum > 0.f ? p.scale / sum : 0.f;
-      for (int j = lane; j < p.k; j += 32) out_w[j] = (p.k > 32 ? out_w[j] : only) * f;
+    const float worth = group_worth(first, second, p.lanes);
+    int rank = group_rank(worth, g, p.groups, p.lanes, lane);
+    bool stays = rank < p.top_groups && g < p.groups;
+    // the worst that stays against the best that goes
+    const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
+    const float high = float_of(__reduce_max_sync(kFull, g < p.groups && !stays ? key_of(worth) : 0u));
+    const float open = open_steps * step;  // as far as two choices may be off
+    if (low - high <= 2.f * open && !rows_alike()) {
+      // the groups' two best in 64 bits: of those that may be among them
+      need_total();
+      const float least = second - open;
+      double f = -INFINITY, n = -INFINITY;
+      int o = g < p.groups ? r : p.size;
+      for (;;) {
+        while (o < p.size && !(mine[o] >= least)) o += p.lanes;
+        if (!__any_sync(kFull, o < p.size)) break;
+        if (o < p.size) {
+          top_two(exactly(g * p.size + o), f, n);
+          o += p.lanes;
+        }
+      }
+      rank = group_rank(group_worth(f, n, p.lanes), g, p.groups, p.lanes, lane);
+      stays = rank < p.top_groups && g < p.groups;
     }
+    const uint32_t lanes_in = __ballot_sync(kFull, stays);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (!((lanes_in >> ((at[i] * p.lanes) & 31)) & 1u)) key[i] = 0;  // (past the last expert it is 0 already)
+  }
+
+  int32_t* out_i = p.expert_idx + t * p.k;
+  float* out_w = p.gate_w + t * p.k;
+  uint32_t own = 0, second = 0;  // this lane's best two
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    second = max(second, min(own, key[i]));
+    own = max(own, key[i]);
+  }
+  uint32_t used = 0;  // lanes whose second one has come up: behind it they look again
+  uint32_t last = kFull, gap = kFull;  // gap: the smallest between neighbours
+  int mine = 0;                        // slot `lane`'s expert
+  int n = 0;                           // slots taken: k, and those behind whose order with the last is open
+  uint32_t best = __reduce_max_sync(kFull, own);
+  auto take = [&]() {
+    last = best;
+    const int src = __ffs(__ballot_sync(kFull, own == best)) - 1;  // equal keys: the lowest lane has the lowest expert
+    const int e = static_cast<int>(31 - (best & 31)) * 32 + src;
+    if (n < 32) mine = lane == n ? e : mine;
+    else if (lane == (n & 31)) out_i[n] = e;
+    if ((used >> src) & 1u) {
+      uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) next = max(next, key[i] - best);
+      next = next & 0x80000000u ? next + best : 0u;
+      own = lane == src ? next : own;
+    } else {
+      own = lane == src ? second : own;
+      used |= 1u << src;
+    }
+    best = __reduce_max_sync(kFull, own);
+    gap = min(gap, last - best);
+    ++n;
+  };
+  while (n < p.k) take();
+  // an order is open between numbers within tol (masked ones go by their place, which the slots below show, too)
+  const bool near = gap <= tol;
+  while (last - best <= tol && best >= 2 * kMasked && n < 32) take();
+  if (near && !rows_alike()) {
+    if (n < 32) {  // one slot a lane: their order in 64 bits
+      if (biased) need_total();
+      double c = -INFINITY;
+      if (lane < n) c = biased ? exactly(mine) : static_cast<double>(clean(__ldg(row + mine)));
+      int rank = 0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const double v = __shfl_sync(kFull, c, j);
+        const int e = __shfl_sync(kFull, mine, j);
+        rank += v > c || (v == c && e < mine);
+      }
+      if (lane < n && rank < p.k) out_i[rank] = mine;
+      __syncwarp();
+    } else {
+      choose_exactly(p, row, lane, m, out_i);
+    }
+    if (lane < p.k) mine = out_i[lane];
+  }
+
+  // slot j's weight in lane j mod 32, which wrote its expert
+  float top = -INFINITY;
+  if (p.renorm) {
+    for (int j = lane; j < p.k; j += 32) top = fmaxf(top, clean(__ldg(row + (j < 32 ? mine : out_i[j]))));
+    top = warp_max(top);
+  }
+  float sum = 0.f, only = 0.f;
+  for (int j = lane; j < p.k; j += 32) {
+    const int e = j < 32 ? mine : out_i[j];
+    if (j < 32) out_i[j] = e;
+    const float v = clean(__ldg(row + e));
+    float w = 0.f;
+    if (v > -INFINITY) w = p.renorm ? proportion(v, top, sig) : sig ? sigmoid(v) * p.scale : expf(v - m) * weigh;
+    sum += w;
+    if (!p.renorm) out_w[j] = w;
+    else if (p.k > 32) out_w[j] = w;
+    else only = w;
+  }
+  if (p.renorm) {
+    sum = warp_sum(sum);
+    const float f = sum > 0.f ? p.scale / sum : 0.f;
+    for (int j = lane; j < p.k; j += 32) out_w[j] = (p.k > 32 ? out_w[j] : only) * f;
+  }
+}
+
+template <int NPL, bool FULL>
+__device__ __forceinline__ float load_bias(const Choice& p, float (&b)[NPL], int lane) {
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    b[i] = p.bias && (FULL || i * 32 + lane < p.E) ? __ldg(p.bias + i * 32 + lane) : 0.f;
+    most = fmaxf(most, fabsf(b[i]) < INFINITY ? fabsf(b[i]) : 0.f);
+  }
+  return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
+}
+
+// A warp walks its tokens with the bias in registers.
+template <int NPL, bool GROUPS, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 4 : NPL <= 16 ? 3 : 2)
+    route_balanced_kernel(const __grid_constant__ Choice p) {
+  extern __shared__ float group_mem[];  // [kWarps][groups * stride]
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  float b[NPL];
+  const float most = load_bias<NPL, FULL>(p, b, lane);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < p.T;
+       t += static_cast<int64_t>(gridDim.x) * kWarps)
+    route_by_warp<NPL, GROUPS, FULL>(p, t, b, most, group_mem + (threadIdx.x >> 5) * p.groups * p.stride, lane);
+}
+
+// Four tokens a warp, eight lanes each: what is done once a token, the groups'
+// merging, the slots and their weights, then serves four.  For E = 32 NI up to
+// 256, k up to 8 and groups of whole 32s (G of them, 1: none), rows 16 bytes
+// apart; lane q of a token has experts 32 i + 4 q + r.  Keys hold the expert's
+// number itself, under a place of 22 bits, and a token whose order is open, or
+// with experts ruled out among its best, is left to the whole warp.  (Settling
+// it among the eight lanes took longer, 15 us against 11 at 1024 x 256: it is
+// more code that was not run before.)
+template <int NI, int G>
+__device__ __noinline__ void route_again(const Choice& p, int64_t t, float* mem, int lane) {
+  float b[NI];
+  const float most = load_bias<NI, true>(p, b, lane);
+  route_by_warp<NI, (G > 1), true>(p, t, b, most, mem, lane);
+}
+
+// The segment's largest: of eight neighbouring lanes.
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+constexpr uint32_t kLive8 = 2u << 8;  // the lowest key of a number
+__device__ __forceinline__ uint32_t pack8(float place, int e) {
+  return ((__float_as_uint(place) - 0x3f800000u + 2u) << 8) + (255 - e);
+}
+
+template <int NI, int G>
+__global__ void __launch_bounds__(kWarps * 32, NI == 8 ? 2 : 4) route_eighths_kernel(const __grid_constant__ Choice p) {
+  extern __shared__ float group_mem[];  // [kWarps][groups * stride], for route_again()
+  dmoe::pdl_wait();
+  dmoe::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, q = lane & 7, seg = lane >> 3;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * 4;
+  if (t0 >= p.T) return;
+  const bool there = t0 + seg < p.T;
+  const int64_t t = there ? t0 + seg : p.T - 1;  // (the last token again, and written by none)
+  const float* row = p.logits + t * p.E;
+  const bool sig = p.sig, biased = p.bias != nullptr;
+  float s[NI][4];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(row) + 8 * i + q);
+    s[i][0] = clean(v.x), s[i][1] = clean(v.y), s[i][2] = clean(v.z), s[i][3] = clean(v.w);
+  }
+  float m = -FLT_MAX;
+  if (!sig || !biased) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) m = fmaxf(m, fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3])));
+    m = max8(m);
+  }
+  float weigh = 0.f;  // what exponentials become weights by, where the whole softmax does
+  if (!sig && !p.renorm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum += expf(s[i][r] - m);
+    sum = sum8(sum);
+    weigh = sum > 0.f ? p.scale / sum : 0.f;
+  }
+  uint32_t key[NI][4];
+  if (!biased) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float z = s[i][r];
+        key[i][r] = pack8(z == -INFINITY ? kMaskedPlace : fmaxf(fmaf(z - m, 1.f / 64.f, 1.5f), 1.f), 32 * i + 4 * q + r);
+      }
+  }
+  // In steps of 2^-21 of the range, half as many as the whole warp's, and one
+  // for the coarser places; a lane adds 4 NI terms of a softmax's sum, and three
+  // more.
+  uint32_t tol = 255;
+  float open = 0.f;
+  bool near = false;
+  if (G > 1 || biased) {
+    float inv = 1.f;
+    if (!sig) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum += ex2_approx((s[i][r] - m) * kLog2e);
+      sum = sum8(sum);
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+    }
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (biased) b = __ldg(reinterpret_cast<const float4*>(p.bias) + 8 * i + q);
+      const float bb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        most = fmaxf(most, fabsf(bb[r]));
+        const float z = s[i][r];
+        const float v = sig ? rcp_approx(1.f + ex2_approx(z * -kLog2e)) : ex2_approx((z - m) * kLog2e) * inv;
+        s[i][r] = z == -INFINITY ? -INFINITY : fmaxf(v + bb[r], -INFINITY);  // the choice; NaN is minus infinity
+      }
+    }
+    most = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
+    near = most == INFINITY;  // experts that a bias rules out, or forces
+    const float range = most + inv;
+    open = (sig ? 5.f : 12.f) * 4.7683716e-7f * range;
+    if (biased) {
+      tol += (sig ? 5u : 12u) << 8;
+      const float quarter = 0.24999f / range;  // all numbers' places lie above 1
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          key[i][r] = pack8(fminf(fmaxf(fmaf(s[i][r], quarter, 1.25f), kMaskedPlace), 1.5f), 32 * i + 4 * q + r);
+    }
+  }
+  if (G > 1) {
+    constexpr int PER = NI / G;  // rows of 32 experts of a group
+    float f[G], g[G];            // the best two of each group: the lane's, then of more and more lanes
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      f[h] = g[h] = -INFINITY;
+#pragma unroll
+      for (int i = h * PER; i < (h + 1) * PER; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top_two(s[i][r], f[h], g[h]);
+    }
+    // lanes that part with half of the groups at a step: lane q ends with group q G / 8
+#pragma unroll
+    for (int o = 4, n = G; o > 0; o >>= 1) {
+      const bool high = (q & o) != 0;
+      if (n > 1) {
+        n /= 2;
+#pragma unroll
+        for (int h = 0; h < n; ++h) {
+          const float f2 = __shfl_xor_sync(kFull, high ? f[h] : f[h + n], o);
+          const float g2 = __shfl_xor_sync(kFull, high ? g[h] : g[h + n], o);
+          const float f1 = high ? f[h + n] : f[h], g1 = high ? g[h + n] : g[h];
+          f[h] = fmaxf(f1, f2);
+          g[h] = fmaxf(fminf(f1, f2), fmaxf(g1, g2));
+        }
+      } else {
+        const float f2 = __shfl_xor_sync(kFull, f[0], o), g2 = __shfl_xor_sync(kFull, g[0], o);
+        const float f1 = f[0];
+        f[0] = fmaxf(f1, f2);
+        g[0] = fmaxf(fminf(f1, f2), fmaxf(g[0], g2));
+      }
+    }
+    const float worth = g[0] == -INFINITY ? f[0] : f[0] + g[0];
+    const int mine = q / (8 / G);
+    int rank = 0;
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      const float w = __shfl_sync(kFull, worth, (lane & 24) + h * (8 / G));
+      rank += w > worth || (w == worth && h < mine);
+    }
+    const bool stays = rank < p.top_groups;
+    const float low = -max8(stays ? -worth : -INFINITY), high = max8(stays ? -INFINITY : worth);
+    near |= low - high <= 2.f * open;
+    const uint32_t in = __ballot_sync(kFull, stays) >> (lane & 24);
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      if ((in >> (h * (8 / G))) & 1u) continue;
+#pragma unroll
+      for (int i = h * PER; i < (h + 1) * PER; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) key[i][r] = 0;
+    }
+  }
+  uint32_t own = 0, second = 0;  // the lane's best two
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      second = max(second, min(own, key[i][r]));
+      own = max(own, key[i][r]);
+    }
+  bool used = false;  // the second one has come up: behind it the lane looks again
+  uint32_t slot = 0, gap = kFull;
+  uint32_t best = max8(own);
+  for (int j = 0; j < p.k; ++j) {
+    slot = q == j ? best : slot;
+    const uint32_t last = best;
+    const bool owner = own == best;  // keys are all different
+    if (__any_sync(kFull, owner && used)) {
+      uint32_t next = 0;  // the lane's best below: of the differences that wrap the largest
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) next = max(next, key[i][r] - best);
+      second = owner && used ? (next & 0x80000000u ? next + best : 0u) : second;
+    }
+    own = owner ? second : own;
+    used |= owner;
+    best = max8(own);
+    gap = min(gap, last - best);
+    near |= last < kLive8;
+  }
+  near |= gap <= tol;
+  // the slots' weights, one a lane
+  const int e = static_cast<int>(255 - (slot & 255));
+  const bool mine = q < p.k && slot != 0;
+  const float v = mine ? clean(__ldg(row + e)) : -INFINITY;
+  float w = 0.f;
+  if (p.renorm) {
+    const float top = max8(v);
+    if (v > -INFINITY) w = proportion(v, top, sig);
+    const float sum = sum8(w);
+    w *= sum > 0.f ? p.scale / sum : 0.f;
+  } else if (v > -INFINITY) {
+    w = sig ? sigmoid(v) * p.scale : expf(v - m) * weigh;
+  }
+  if (mine && there && !near) {
+    p.expert_idx[t * p.k + q] = e;
+    p.gate_w[t * p.k + q] = w;
+  }
+  uint32_t again = __ballot_sync(kFull, near && there && q == 0);
+  float* mem = group_mem + (threadIdx.x >> 5) * p.groups * p.stride;
+  while (again) {
+    const int at = __ffs(again) - 1;
+    again &= again - 1;
+    route_again<NI, G>(p, t0 + (at >> 3), mem, lane);
   }
 }
 
@@ -573,7 +827,26 @@ struct ForwardCall {
   cudaStream_t st;
   template <int NPL>
   cudaError_t operator()() const {
+    if constexpr (NPL >= 2 && NPL <= 8) {
+      // four tokens a warp where it has that many
+      const bool even = p.E == 32 * NPL && p.k <= 8 && dmoe::aligned16(p.logits) && dmoe::aligned16(p.bias);
+      const int groups = p.top_groups == p.groups ? 1 : p.groups;
+      if (even && (p.k == 1 || p.T >= kEighthsFrom)) {
+        if (groups == 1) return eighths<NPL, 1>();
+        if (groups == 2) return eighths<NPL, 2>();
+        if constexpr (NPL >= 4)
+          if (groups == 4) return eighths<NPL, 4>();
+        if constexpr (NPL >= 8)
+          if (groups == 8) return eighths<NPL, 8>();
+      }
+    }
     return p.E == 32 * NPL ? launch<NPL, true>() : launch<NPL, false>();
+  }
+  template <int NI, int G>
+  cudaError_t eighths() const {
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.T) + 4 * kWarps - 1) / (4 * kWarps)));
+    const size_t smem = G > 1 ? sizeof(float) * kWarps * p.groups * p.stride : 0;
+    return dmoe::launch_pdl(route_eighths_kernel<NI, G>, grid, dim3(kWarps * 32), smem, st, p);
   }
   template <int NPL, bool FULL>
   cudaError_t launch() const {

@@ -124,7 +124,10 @@ def route(dm, logits, k, **kw):
 ROUTES = [  # T, E, k, groups, top_groups
     (1, 1, 1, 1, 1), (1, 256, 8, 8, 4), (5, 8, 2, 1, 1), (9, 31, 31, 1, 1), (130, 64, 1, 1, 1), (77, 66, 5, 3, 2),
     (1000, 256, 8, 8, 4), (513, 96, 6, 32, 5), (64, 40, 12, 20, 7), (33, 160, 6, 5, 1), (257, 512, 40, 16, 3),
-    (17, 1024, 9, 1, 1), (12, 1024, 64, 32, 2), (11, 24, 3, 24, 5), (2049, 128, 8, 2, 1), (6, 7, 7, 7, 7)]
+    (17, 1024, 9, 1, 1), (12, 1024, 64, 32, 2), (11, 24, 3, 24, 5), (2049, 128, 8, 2, 1), (6, 7, 7, 7, 7),
+    # four tokens a warp: one expert each, or many tokens
+    (1, 64, 1, 1, 1), (7, 128, 1, 4, 2), (130, 256, 1, 8, 8), (33, 128, 1, 2, 1), (50, 256, 1, 2, 1), (8193, 64, 8, 2, 1),
+    (8195, 128, 5, 4, 3), (9001, 256, 8, 8, 4), (8192, 256, 7, 4, 1), (8194, 256, 8, 1, 1), (8200, 64, 6, 1, 1)]
 
 
 @pytest.mark.gpu
@@ -173,6 +176,34 @@ def test_route_where_32_bits_cannot_tell(dm, scores, groups, top_groups):
     if groups == 1:
         assert float((got - want).abs().max()) < 1e-14
     assert float((idx.long() != ri).any(1).double().mean()) < 0.02
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top_groups,biased", [(1, 1, False), (1, 1, True), (8, 3, True), (8, 3, False)])
+def test_route_of_many_tokens_with_open_orders(dm, scores, groups, top_groups, biased):
+    """A batch large enough for four tokens a warp, in which rows with ties, masks and extremes lie between usual ones."""
+    T, E, k = 8300, 256, 8
+    logits = randn(1, T, E, dtype=F32)
+    bias = randn(2, E, scale=0.02, dtype=F32) if biased else None
+    logits[::7] = 0.0                                             # padding
+    logits[3::11] = (torch.arange(E, device="cuda") % 5).float()  # ties all over
+    logits[5::13, 9:] = -math.inf                                 # few experts left, one of them twice
+    logits[6::17, ::2] = -math.inf
+    logits[8::19] = math.nan
+    logits[9::23] *= 1e20
+    if biased:
+        logits[2::29] = torch.logit(((0.5 - bias).double()).clamp(1e-3, 1 - 1e-3)).to(F32)  # sigmoids level with the bias
+    idx, w = route(dm, logits, k, bias=bias, scores=scores, groups=groups, top_groups=top_groups)
+    ri, rw = ref_route(logits, bias, k, scores, groups, top_groups, True, 1.0)
+    same = (idx.long() == ri).all(1)
+    level = torch.zeros(T, dtype=torch.bool, device="cuda")
+    if biased:
+        level[2::29] = True
+    # everywhere but in the levelled rows, whose 64-bit values differ by their own roundings
+    assert bool(same[~level].all())
+    assert float(same[level].double().mean()) > 0.9 if biased else True
+    close(w[same], rw[same], 400 * U32 * rw[same] + 2.0 ** -126, "gate_w")
 
 
 @pytest.mark.gpu
