@@ -41,8 +41,8 @@ constexpr int kMaxGroups = 32;
 // 6 us however few they are (us, whole warps and four tokens: 64 experts, top-1
 // softmax, 1024 tokens 2.7 and 2.5, 8192 5.5 and 3.5, 32768 17.0 and 7.5; top-8
 // sigmoid, 4096 6.5 and 7.9, 8192 9.1 and 8.2, 32768 24.8 and 12.3; 256 experts
-// in 8 groups, 4096 9.7 and 13.6, 8192 15.3 and 15.2, 16381 24.5 and 22.4, 32768
-// 42.8 and 31.3).
+// in 8 groups, 4096 9.7 and 14.1, 8192 15.3 and 15.5, 16381 24.5 and 21.6, 32768
+// 42.8 and 29.7).
 constexpr int kEighthsFrom = 8192;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -494,7 +494,7 @@ __device__ __forceinline__ uint32_t pack8(float place, int e) {
 }
 
 template <int NI, int G>
-__global__ void __launch_bounds__(kWarps * 32, NI == 8 ? 2 : 4) route_eighths_kernel(const __grid_constant__ Choice p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) route_eighths_kernel(const __grid_constant__ Choice p) {
   extern __shared__ float group_mem[];  // [kWarps][groups * stride], for route_again()
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
@@ -527,21 +527,11 @@ __global__ void __launch_bounds__(kWarps * 32, NI == 8 ? 2 : 4) route_eighths_ke
     sum = sum8(sum);
     weigh = sum > 0.f ? p.scale / sum : 0.f;
   }
-  uint32_t key[NI][4];
-  if (!biased) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float z = s[i][r];
-        key[i][r] = pack8(z == -INFINITY ? kMaskedPlace : fmaxf(fmaf(z - m, 1.f / 64.f, 1.5f), 1.f), 32 * i + 4 * q + r);
-      }
-  }
   // In steps of 2^-21 of the range, half as many as the whole warp's, and one
   // for the coarser places; a lane adds 4 NI terms of a softmax's sum, and three
   // more.
   uint32_t tol = 255;
-  float open = 0.f;
+  float open = 0.f, quarter = 0.f;
   bool near = false;
   if (G > 1 || biased) {
     float inv = 1.f;
@@ -572,16 +562,10 @@ __global__ void __launch_bounds__(kWarps * 32, NI == 8 ? 2 : 4) route_eighths_ke
     near = most == INFINITY;  // experts that a bias rules out, or forces
     const float range = most + inv;
     open = (sig ? 5.f : 12.f) * 4.7683716e-7f * range;
-    if (biased) {
-      tol += (sig ? 5u : 12u) << 8;
-      const float quarter = 0.24999f / range;  // all numbers' places lie above 1
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          key[i][r] = pack8(fminf(fmaxf(fmaf(s[i][r], quarter, 1.25f), kMaskedPlace), 1.5f), 32 * i + 4 * q + r);
-    }
+    quarter = 0.24999f / range;  // all numbers' places lie above 1
+    if (biased) tol += (sig ? 5u : 12u) << 8;
   }
+  uint32_t in = 255;  // the groups that stay, a bit at lane h 8 / G
   if (G > 1) {
     constexpr int PER = NI / G;  // rows of 32 experts of a group
     float f[G], g[G];            // the best two of each group: the lane's, then of more and more lanes
@@ -625,14 +609,22 @@ __global__ void __launch_bounds__(kWarps * 32, NI == 8 ? 2 : 4) route_eighths_ke
     const bool stays = rank < p.top_groups;
     const float low = -max8(stays ? -worth : -INFINITY), high = max8(stays ? -INFINITY : worth);
     near |= low - high <= 2.f * open;
-    const uint32_t in = __ballot_sync(kFull, stays) >> (lane & 24);
+    in = __ballot_sync(kFull, stays) >> (lane & 24);
+  }
+  uint32_t key[NI][4];
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      if ((in >> (h * (8 / G))) & 1u) continue;
+  for (int i = 0; i < NI; ++i) {
+    const bool here = G == 1 || ((in >> (i / (NI / G) * (8 / G))) & 1u);
+    if (G > 1 && !biased) {  // the logits, whose place the groups' scores have taken
+      const float4 v = __ldg(reinterpret_cast<const float4*>(row) + 8 * i + q);
+      s[i][0] = clean(v.x), s[i][1] = clean(v.y), s[i][2] = clean(v.z), s[i][3] = clean(v.w);
+    }
 #pragma unroll
-      for (int i = h * PER; i < (h + 1) * PER; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) key[i][r] = 0;
+    for (int r = 0; r < 4; ++r) {
+      const float c = s[i][r];
+      const float place = biased ? fminf(fmaxf(fmaf(c, quarter, 1.25f), kMaskedPlace), 1.5f)
+                          : c == -INFINITY ? kMaskedPlace : fmaxf(fmaf(c - m, 1.f / 64.f, 1.5f), 1.f);
+      key[i][r] = here ? pack8(place, 32 * i + 4 * q + r) : 0u;
     }
   }
   uint32_t own = 0, second = 0;  // the lane's best two
