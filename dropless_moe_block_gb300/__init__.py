@@ -696,14 +696,24 @@ def _apart_or_same(p, n, name, *others):
             raise ValueError(f"{name} must not overlap {other}")
 
 
+# the index of the current device without the checks of torch.cuda.current_device() (0.3 us)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _device(t, name):
     """The current device, which has to be the tensor's."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} lies on device {dev}, the current one is {torch.cuda.current_device()}")
+    now = torch.cuda.current_device() if _current_device is None else _current_device()
+    if dev != now:
+        raise ValueError(f"{name} lies on device {dev}, the current one is {now}")
     return dev
+
+
+def _stream_on(stream, dev):
+    """The handle of that stream, or of the device's current one."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _is(t, dev, dtype, name, shape):
@@ -757,7 +767,7 @@ def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = 
     _is(gate_w, dev, torch.float32, "gate_w", (T, k))
     _check("dmoe_route_balanced", lib().dmoe_route_balanced(
         logits.data_ptr(), _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
-        int(bool(renormalize)), scale, expert_idx.data_ptr(), gate_w.data_ptr(), _stream(stream)))
+        int(bool(renormalize)), scale, expert_idx.data_ptr(), gate_w.data_ptr(), _stream_on(stream, dev)))
 
 
 def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = "softmax", renormalize: bool = True,
@@ -775,7 +785,7 @@ def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = 
     _apart_from(op, n, "d_logits", (lp, n, "logits"))
     _check("dmoe_route_balanced_backward", lib().dmoe_route_balanced_backward(
         lp, expert_idx.data_ptr(), d_gate.data_ptr(), T, E, k, _name(_SCORES, scores, "scores"), int(bool(renormalize)),
-        scale, op, _stream(stream)))
+        scale, op, _stream_on(stream, dev)))
 
 
 def balance_bias(bias, tokens_per_expert, rate: float, stream=None):
@@ -785,12 +795,18 @@ def balance_bias(bias, tokens_per_expert, rate: float, stream=None):
     dev = _device(bias, "bias")
     _is(bias, dev, torch.float32, "bias", (E,))
     _is(tokens_per_expert, dev, torch.int32, "tokens_per_expert", (E,))
-    _check("dmoe_balance_bias", lib().dmoe_balance_bias(_ptr(bias), _ptr(tokens_per_expert), E, rate, _stream(stream)))
+    _check("dmoe_balance_bias", lib().dmoe_balance_bias(_ptr(bias), _ptr(tokens_per_expert), E, rate, _stream_on(stream, dev)))
 
 
 def _norm_weights(w_post, w_pre, dev, d):
-    wf = _bf16_or_f32(w_post, dev, "w_post", (d,))
-    if _bf16_or_f32(w_pre, dev, "w_pre", (d,)) != wf:
+    bf = torch.bfloat16
+    shape = (d,)
+    if (w_post is not None and w_pre is not None and w_post.dtype is bf and w_pre.dtype is bf
+            and w_post.get_device() == dev and w_pre.get_device() == dev and w_post.shape == shape
+            and w_pre.shape == shape and w_post.is_contiguous() and w_pre.is_contiguous()):
+        return 0  # the usual case
+    wf = _bf16_or_f32(w_post, dev, "w_post", shape)
+    if _bf16_or_f32(w_pre, dev, "w_pre", shape) != wf:
         raise ValueError("w_post and w_pre must have the same type")
     return wf
 
@@ -827,13 +843,16 @@ def sandwich_norm(u, residual, w_post, w_pre, eps: float, h, y, gate=None, scale
         _is(rstd_h, dev, torch.float32, "rstd_h", (T,))
     up, rp, hp, yp = u.data_ptr(), residual.data_ptr(), h.data_ptr(), y.data_ptr()
     nb = 2 * T * d
-    reads = (up, 2 * ((T - 1) * ldu + d), "u"), (rp, 2 * ((T - 1) * ldr + d), "residual")
-    _apart_from(hp, nb, "h", (yp, nb, "y"))
-    _apart_or_same(hp, nb, "h", *reads)
-    _apart_or_same(yp, nb, "y", *reads)
+    nu, nr = 2 * ((T - 1) * ldu + d), 2 * ((T - 1) * ldr + d)
+    if hp < yp + nb and yp < hp + nb or min(up, rp) < max(hp, yp) + nb and min(hp, yp) < max(up + nu, rp + nr):
+        # something may overlap: which
+        reads = (up, nu, "u"), (rp, nr, "residual")
+        _apart_from(hp, nb, "h", (yp, nb, "y"))
+        _apart_or_same(hp, nb, "h", *reads)
+        _apart_or_same(yp, nb, "y", *reads)
     _check("dmoe_sandwich_norm", lib().dmoe_sandwich_norm(
         up, ldu, rp, ldr, w_post.data_ptr(), w_pre.data_ptr(), wf, _ptr(gate), n, scale, eps, T, d, hp, yp, _ptr(rstd_u),
-        _ptr(rstd_h), _stream(stream)))
+        _ptr(rstd_h), _stream_on(stream, dev)))
 
 
 def sandwich_norm_backward_workspace_size(T: int, d: int) -> int:
@@ -881,7 +900,7 @@ def sandwich_norm_backward(dy, u, h, w_post, w_pre, rstd_u, rstd_h, du, dresidua
     _check("dmoe_sandwich_norm_backward", lib().dmoe_sandwich_norm_backward(
         dyp, lddy, up, ldu, hp, w_post.data_ptr(), w_pre.data_ptr(), wf, _ptr(gate), n, scale, rstd_u.data_ptr(),
         rstd_h.data_ptr(), dhp, lddh, T, d, dup, dxp, _ptr(dw_post), _ptr(dw_pre), _ptr(d_gate), _ptr(ws), nws,
-        _stream(stream)))
+        _stream_on(stream, dev)))
 
 
 def linear_workspace_size(M: int, K: int, N: int) -> int:
@@ -918,7 +937,7 @@ def linear(x, w, y, ws, bias=None, act: str = "none", deriv=None, residual=None,
     _apart_from(yp, nb, "y", *reads)
     _apart_or_same(yp, nb, "y", added)
     _check("dmoe_linear", lib().dmoe_linear(
-        xp, ldx, wp, _ptr(bias), b32, a, rp, ldr, M, K, N, yp, fp, ws.data_ptr(), nws, _stream(stream)))
+        xp, ldx, wp, _ptr(bias), b32, a, rp, ldr, M, K, N, yp, fp, ws.data_ptr(), nws, _stream_on(stream, dev)))
 
 
 def linear_backward_workspace_size(M: int, K: int, N: int) -> int:
@@ -964,7 +983,7 @@ def linear_backward(dy, x, w, dx, dw, ws, deriv=None, dbias=None, factor=None, s
     if dbias is not None:
         _is(dbias, dev, torch.float32, "dbias", (N,))
     _check("dmoe_linear_backward", lib().dmoe_linear_backward(
-        dyp, lddy, fp, xp, ldx, wp, kp, M, K, N, dxp, dwp, f32, _ptr(dbias), ws.data_ptr(), nws, _stream(stream)))
+        dyp, lddy, fp, xp, ldx, wp, kp, M, K, N, dxp, dwp, f32, _ptr(dbias), ws.data_ptr(), nws, _stream_on(stream, dev)))
 
 
 # ----------------------------------------------------------------- whole layer

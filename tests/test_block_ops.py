@@ -802,3 +802,139 @@ def test_binding_refusals(dm):
         dm.linear_backward(o, x, wm, x, None, ws)
     with pytest.raises(ValueError, match="factor"):
         dm.linear_backward(o, x, wm, None, None, ws, factor=x)
+
+
+# ------------------------------------------- what a caller may do besides
+
+@pytest.mark.gpu
+def test_rows_behind_the_last_stay_as_they_were(dm):
+    def tail(*shape, dtype=BF):
+        whole = empty(shape[0] + 9, *shape[1:], dtype=dtype)
+        return whole, whole[:shape[0]]
+
+    kept = []
+    for M, K, N in ((7, 264, 520), (130, 264, 520), (1000, 4096, 136)):
+        x, w = randn(1, M, K), randn(2, K, N, scale=K ** -0.5)
+        ws, _ = workspace(max(dm.linear_workspace_size(M, K, N), dm.linear_backward_workspace_size(M, K, N)))
+        (a, y), (b, f), (c, dx) = tail(M, N), tail(M, N), tail(M, K)
+        dm.linear(x, w, y, ws, act="gelu", deriv=f)
+        dm.linear_backward(y, x, w, dx, None, ws, deriv=f)
+        kept += [(a, M), (b, M), (c, M)]
+    for T, d in ((5, 64), (130, 4104)):
+        u, x, w = randn(1, T, d), randn(2, T, d), randn(3, d)
+        (a, h), (b, y), (c, du), (e, dx) = tail(T, d), tail(T, d), tail(T, d), tail(T, d)
+        (f, ru), (g, rh) = tail(T, dtype=F32), tail(T, dtype=F32)
+        dm.sandwich_norm(u, x, w, w, 1e-5, h, y, rstd_u=ru, rstd_h=rh)
+        dm.sandwich_norm_backward(y, u, h, w, w, ru, rh, du, dx, None, None, None)
+        kept += [(t, T) for t in (a, b, c, e, f, g)]
+    for T, E, k in ((5, 64, 1), (8193, 64, 8), (77, 40, 3)):
+        (a, idx), (b, gw), (c, dl) = tail(T, k, dtype=I32), tail(T, k, dtype=F32), tail(T, E, dtype=F32)
+        lg = randn(1, T, E, dtype=F32)
+        dm.route_balanced(lg, k, idx, gw)
+        dm.route_balanced_backward(lg, idx, gw, dl)
+        kept += [(a, T), (b, T), (c, T)]
+    for t, n in kept:
+        rest = t[n:]
+        assert torch.equal(rest, torch.full_like(rest, 77 if t.dtype is I32 else 777.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_route_of_rows_at_odd_places(dm, shift):
+    T, E, k = 8200, 64, 4
+    flat = randn(1, T * E + 4, dtype=F32)
+    bias = randn(2, E + 4, scale=0.02, dtype=F32)[shift:shift + E]
+    logits = flat[shift:shift + T * E].view(T, E)
+    idx, w = route(dm, logits, k, bias=bias, scores="sigmoid")
+    idx2, w2 = route(dm, logits.clone(), k, bias=bias.clone(), scores="sigmoid")
+    assert torch.equal(idx, idx2) and torch.equal(w, w2)
+    d = randn(3, T, k, dtype=F32)
+    out = empty(T * E + 4, dtype=F32)
+    dl, dl2 = out[shift:shift + T * E].view(T, E), empty(T, E, dtype=F32)
+    dm.route_balanced_backward(logits, idx, d, dl, scores="sigmoid")
+    dm.route_balanced_backward(logits, idx, d, dl2, scores="sigmoid")
+    assert torch.equal(dl, dl2)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(dm):
+    """Calls on two streams with workspaces of their own, and two graphs replayed side by side."""
+    M, K, N = 600, 1032, 2056
+    w = randn(2, K, N, scale=K ** -0.5)
+    sets = []
+    for i in range(2):
+        x, dy = randn(10 + i, M, K), randn(20 + i, M, N)
+        ws, _ = workspace(max(dm.linear_workspace_size(M, K, N), dm.linear_backward_workspace_size(M, K, N)))
+        sets.append((x, dy, ws, empty(M, N), empty(M, N), empty(M, K), empty(K, N), empty(N, dtype=F32)))
+
+    def run(s):
+        x, dy, ws, y, f, dx, dw, db = s
+        dm.linear(x, w, y, ws, act="silu", deriv=f)
+        dm.linear_backward(dy, x, w, dx, dw, ws, deriv=f, dbias=db)
+
+    want = []
+    for s in sets:
+        run(s)
+        want.append([t.clone() for t in s[3:]])
+        for t in s[3:]:
+            t.fill_(1.0)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                run(s)
+    torch.cuda.synchronize()
+    for s, ref in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(s[3:], ref))
+    graphs = []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(s)
+        graphs.append(g)
+        for t in s[3:]:
+            t.fill_(1.0)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, ref in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(s[3:], ref))
+
+
+@pytest.mark.gpu
+def test_long_rows_of_many_tokens(dm):
+    """Offsets beyond 32 bits: [70000, 32768] outputs hold 2.3e9 elements."""
+    M, K, N = 70000, 64, 32768
+    free, _ = torch.cuda.mem_get_info()
+    if free < 30 << 30:
+        pytest.skip("needs 30 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda").to(BF)
+    w = (torch.randn(K, N, generator=g, device="cuda") * K ** -0.5).to(BF)
+    r = torch.empty(M, N, device="cuda", dtype=BF)
+    r.zero_()
+    y = torch.empty(M, N, device="cuda", dtype=BF)
+    ws, _ = workspace(dm.linear_workspace_size(M, K, N))
+    dm.linear(x, w, y, ws, act="gelu", deriv=r)
+    for rows in (slice(0, 3), slice(65534, 65539), slice(M - 3, M)):
+        z = x[rows].double() @ w.double()
+        ref, df = ref_act(z, "gelu")
+        S = x[rows].double().abs() @ w.double().abs()
+        tol = 2 * (K + 8) * U32 * S + 4e-7 * (1 + z.abs())
+        close(y[rows], ref, U16 * ref.abs() + 1.2 * tol, "y")
+        close(r[rows], df, U16 * df.abs() + tol, "deriv")
+    del y
+    # the norms over the same elements: 140000 rows of 16384
+    u = r.view(140000, 16384)
+    h, o = torch.empty_like(u), torch.empty_like(u)
+    ones = torch.ones(16384, device="cuda", dtype=BF)
+    dm.sandwich_norm(u, u, ones, ones, 1e-5, h, o)
+    for i in (0, 131072, 139999):
+        ref = u[i].double() * (1 + 1 / torch.sqrt(u[i].double().square().mean() + 1e-5))
+        close(h[i], ref, (U16 + 200 * U32) * ref.abs(), "h")
