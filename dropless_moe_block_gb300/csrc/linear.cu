@@ -451,25 +451,29 @@ __global__ void __launch_bounds__(kThreadsL, 1) linear_kernel(const __grid_const
   }
 }
 
-// ------------------------------------------------------------- few rows
-// For so few rows W's bytes are all there is to do, and a tile of 256 rows of
-// x is nearly empty: its product takes as long as its loads.  So W takes the
-// place of the first operand, 128 of its columns the rows of a tile, and the
-// rows of x, 16, 32 or 64 of them, are the columns: y^T = W^T x^T, and the
-// product is a tenth of the loads.  One CTA a tile and part of K, a deep ring of
-// 16 KB slices of W; the parts of a tile are a cluster, whose CTAs meet in each
-// other's shared memory, in a fixed order.  One CTA draws some 60 GB/s, so some
-// 110 of them draw all that HBM has.
-// 1 x 14336 x 4096: 26.5 us in tiles of rows of x, with their join; 21.5 here.
-constexpr int kFewRows = 64;
-constexpr int kFewTile = 128;  // columns of W
+// ------------------------------------------------------- the product turned
+// For few rows W's bytes are all there is to do, and a tile of 256 rows of x is
+// nearly empty: its product takes as long as its loads.  So W takes the place
+// of the first operand, 128 of its columns the rows of a tile, and the rows of
+// x, 16 to 128 of them, are the columns: y^T = W^T x^T, and the product is a
+// tenth of the loads.  One CTA a tile and part of K, a deep ring of 16 KB slices
+// of W; the parts of a tile are a cluster, whose CTAs meet in each other's
+// shared memory, in a fixed order.  More rows take blocks of 128: small
+// products, too, are done sooner in 5 us of launch, first loads and epilogue
+// than in the 8 of the pairs below.  (us, those and these: 1 x 14336 x 4096
+// 26.5 and 22, 64 x 1024 x 1024 12.2 and 6.1, 128 x 4096 x 4096 18.5 and 13.2,
+// 512 x 1024 x 1024 12.8 and 8.0.)
+constexpr int kTurnedRows = 128;  // of a block
+constexpr int kFewTile = 128;     // columns of W
 constexpr int kFewStages = 11;
-constexpr int kFewThreads = 192;  // TMA producer, MMA issuer, four epilogue warps
+constexpr int kFewEpiWarps = 8;
+constexpr int kFewThreads = 64 + 32 * kFewEpiWarps;  // with the TMA producer and the MMA issuer
 
 struct ParamsF {
   CUtensorMap map_w, map_x;
   int box;  // rows of x that are loaded
-  int tiles, parts, slices;
+  int cols;  // tiles over the columns
+  int tiles, parts, slices;  // tiles: over the columns, then over the blocks of rows
   Out o;
   int32_t* err;
 };
@@ -502,28 +506,30 @@ __device__ __forceinline__ void tmem_load16(uint32_t ta, float* v) {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-__device__ __forceinline__ float float_of_bf16(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ uint32_t bf16_pair(float2 v) {
+  const __nv_bfloat162 h = __float22bfloat162_rn(v);
+  return reinterpret_cast<const uint32_t&>(h);
+}
 
-// One sum on its way out.
+__device__ __forceinline__ float2 pair_of(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
 template <int ACT>
-__device__ __forceinline__ void finish(const Out& o, int row, int c, float v) {
-  if (o.bias)
-    v += o.bias_f32 ? __ldg(static_cast<const float*>(o.bias) + c)
-                    : float_of_bf16(__ldg(static_cast<const uint16_t*>(o.bias) + c));
-  const int64_t at = static_cast<int64_t>(row) * o.cols + c;
-  if (ACT != DMOE_ACT_NONE) {
-    float2 y, g;
-    if (ACT == DMOE_ACT_GELU) gelu_pair(make_float2(v, v), y, g);
-    else silu_pair(make_float2(v, v), y, g);
-    v = y.x;
-    if (o.deriv) o.deriv[at] = bf16_bits(g.x);
-  }
-  if (o.residual) v += float_of_bf16(o.residual[row * o.ld_res + c]);
-  static_cast<uint16_t*>(o.out)[at] = bf16_bits(v);
+__device__ __forceinline__ void act_pair(float2 z, float2& y, float2& g) {
+  if (ACT == DMOE_ACT_GELU) gelu_pair(z, y, g);
+  else if (ACT == DMOE_ACT_SILU) silu_pair(z, y, g);
+  else y = z, g = make_float2(1.f, 1.f);
+}
+
+__device__ __forceinline__ float2 dsmem_ld_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
 template <int ACT, int ROWS>
-__global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_constant__ ParamsF p) {
+__global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_constant__ ParamsF p) {
   using PL = PlanF<ROWS>;
   constexpr int STAGES = PL::STAGES;
   constexpr uint32_t TMEM_COLS = 2 * ROWS;
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_c
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull + a, 1);
-      mbar_init(tempty + a, 4);
+      mbar_init(tempty + a, kFewEpiWarps);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -572,14 +578,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_c
       int stage = 0;
       uint32_t phase = 0;
       for (int tile = first; ok && tile < p.tiles; tile += next) {
+        const int block = tile / p.cols, c0 = (tile - block * p.cols) * kFewTile;
         for (int i = k0; i < k1; ++i) {
           ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
           if (!ok) break;
           uint8_t* sw = smem + stage * PL::STAGE;
           mbar_arrive_expect_tx(full + stage, PL::W_BYTES + p.box * BK * 2);
-          tma_load_2d(sw, &p.map_w, full + stage, tile * kFewTile, i * BK);
-          tma_load_2d(sw + ATOM, &p.map_w, full + stage, tile * kFewTile + 64, i * BK);
-          tma_load_2d(sw + PL::W_BYTES, &p.map_x, full + stage, i * BK, 0);
+          tma_load_2d(sw, &p.map_w, full + stage, c0, i * BK);
+          tma_load_2d(sw + ATOM, &p.map_w, full + stage, c0 + 64, i * BK);
+          tma_load_2d(sw + PL::W_BYTES, &p.map_x, full + stage, i * BK, block * ROWS);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -632,25 +639,46 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_c
   } else {
     uint32_t acc = 0, acc_phase = 0;
     for (int tile = first; ok && tile < p.tiles; tile += next) {
-      const int c = tile * kFewTile + quad * 32 + lane;
+      const int block = tile / p.cols, c = (tile - block * p.cols) * kFewTile + quad * 32 + lane;
+      const int row0 = block * ROWS, rows = min(ROWS, p.o.rows - row0);
+      float bias = 0.f;
+      if (p.parts == 1 && p.o.bias && c < p.o.cols)
+        bias = p.o.bias_f32 ? __ldg(static_cast<const float*>(p.o.bias) + c)
+                            : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.o.bias) + c)) << 16);
       ok = mbar_wait(tfull + acc, acc_phase, abort_flag);
       if (!ok) break;
       __syncwarp();
       fence_after_sync();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * ROWS;
 #pragma unroll 1
-      for (int r = 0; r < ROWS && r < p.o.rows; r += 16) {
+      for (int r = (warp - 2) / 4 * 16; r < rows; r += kFewEpiWarps / 4 * 16) {
         float v[16];
         __syncwarp();
         tmem_load16(tb + r, v);
         if (p.parts > 1) {
 #pragma unroll
           for (int q = 0; q < 16; ++q)
-            if (r + q < p.o.rows) sums[(r + q) * kFewTile + quad * 32 + lane] = v[q];
+            if (r + q < rows) sums[(r + q) * kFewTile + quad * 32 + lane] = v[q];
         } else if (c < p.o.cols) {
+          // what is added is fetched for all rows at once: y may be where it lies
+          uint16_t add[16];
+          if (p.o.residual) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (r + q < p.o.rows) finish<ACT>(p.o, r + q, c, v[q]);
+            for (int q = 0; q < 16; ++q) add[q] = r + q < rows ? p.o.residual[(row0 + r + q) * p.o.ld_res + c] : 0;
+          }
+          const int64_t at = static_cast<int64_t>(row0 + r) * p.o.cols + c;
+#pragma unroll
+          for (int q = 0; q < 16; q += 2) {
+            float2 y, g;
+            act_pair<ACT>(make_float2(v[q] + bias, v[q + 1] + bias), y, g);
+            if (p.o.residual) y = dmoe::f2_add(y, make_float2(__uint_as_float(add[q] << 16), __uint_as_float(add[q + 1] << 16)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (r + q + j >= rows) continue;
+              if (ACT != DMOE_ACT_NONE && p.o.deriv) p.o.deriv[at + static_cast<int64_t>(q + j) * p.o.cols] = bf16_bits(j ? g.y : g.x);
+              static_cast<uint16_t*>(p.o.out)[at + static_cast<int64_t>(q + j) * p.o.cols] = bf16_bits(j ? y.y : y.x);
+            }
+          }
         }
       }
       fence_before_sync();
@@ -674,30 +702,43 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_rows_kernel(const __grid_c
   if (p.parts > 1) {
     __syncwarp();
     cluster_sync();  // every part's sums are there
-    // this CTA's share of the columns, of all rows
-    const int share = kFewTile / p.parts, log_share = __ffs(share) - 1;  // parts is a power of two
-    const int from = rank * share;
-    // four sums at a time, for the way to the other CTAs
-    for (int i0 = threadIdx.x; i0 < p.o.rows * share; i0 += 4 * kFewThreads) {
-      float v[4][8];
+    // this CTA's share of the columns, of all rows, two columns at a time; four of
+    // those pairs together, for the way to the other CTAs and to what is added
+    const int share = kFewTile / p.parts, log_pairs = __ffs(share) - 2;  // parts is a power of two
+    const int block = first / p.cols, c0 = (first - block * p.cols) * kFewTile;
+    const int row0 = block * ROWS, rows = min(ROWS, p.o.rows - row0);
+    const int from = rank * share, pairs = rows << log_pairs;
+    for (int i0 = threadIdx.x; i0 < pairs; i0 += 4 * kFewThreads) {
+      float2 v[4][8], bias[4];
+      uint32_t add[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * kFewThreads;
-        const int r = i >> log_share, col = from + (i & (share - 1));
-        if (i >= p.o.rows * share) continue;
+        const int r = i >> log_pairs, col = from + 2 * (i & (share / 2 - 1)), c = c0 + col;
+        bias[j] = make_float2(0.f, 0.f);
+        add[j] = 0;
+        if (i >= pairs || c >= p.o.cols) continue;
         const uint32_t at = smem_u32(sums + r * kFewTile + col);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[j][q] = q < p.parts ? dsmem_ld_f32(dsmem_addr(at, q)) : 0.f;
+        for (int q = 0; q < 8; ++q) v[j][q] = q < p.parts ? dsmem_ld_f32x2(dsmem_addr(at, q)) : make_float2(0.f, 0.f);
+        if (p.o.bias)
+          bias[j] = p.o.bias_f32 ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p.o.bias) + c))
+                                 : pair_of(__ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.o.bias) + c)));
+        if (p.o.residual) add[j] = *reinterpret_cast<const uint32_t*>(p.o.residual + (row0 + r) * p.o.ld_res + c);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * kFewThreads;
-        const int r = i >> log_share, c = first * kFewTile + from + (i & (share - 1));
-        if (i >= p.o.rows * share || c >= p.o.cols) continue;
-        float sum = v[j][0];
+        const int r = i >> log_pairs, c = c0 + from + 2 * (i & (share / 2 - 1));
+        if (i >= pairs || c >= p.o.cols) continue;
+        float2 sum = v[j][0], y, g;
 #pragma unroll
-        for (int q = 1; q < 8; ++q) sum += v[j][q];
-        finish<ACT>(p.o, r, c, sum);
+        for (int q = 1; q < 8; ++q) sum = dmoe::f2_add(sum, v[j][q]);
+        act_pair<ACT>(dmoe::f2_add(sum, bias[j]), y, g);
+        const int64_t to = static_cast<int64_t>(row0 + r) * p.o.cols + c;
+        if (ACT != DMOE_ACT_NONE && p.o.deriv) *reinterpret_cast<uint32_t*>(p.o.deriv + to) = bf16_pair(g);
+        if (p.o.residual) y = dmoe::f2_add(y, pair_of(add[j]));
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o.out) + to) = bf16_pair(y);
       }
     }
     __syncwarp();
@@ -839,24 +880,28 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ su
 constexpr int kMaxParts = 64;
 constexpr int kMinSlices = 4;  // of a part
 
-// What the times below leave out: launch, first loads, last epilogue.
-constexpr int64_t kTilesNs = 8000, kFewNs = 4500;
+// What the items' times leave out: launch and first loads, and the last
+// epilogue (with an activation more).  Single tiles of 264 columns of K, none
+// and gelu: 7.0 and 9.1 us.
+constexpr int64_t kTilesNs = 5000, kTurnedNs = 4000;
+int64_t last_epilogue_ns(bool act) { return act ? 2700 : 1000; }
 
 // Nanoseconds of an item: `busy` pairs at work, each with this many K slices
 // of a tile.  A slice costs what its product or its loads from L2 take or,
 // where no other pair reads the same columns (alone), what its bytes take from
 // HBM at 6.5 TB/s.  A 512-wide tile, which fills the TMEM, also waits for part of
 // its epilogue; of a narrower one the next product hides it, unless it is
-// longer, as with an activation and its derivative over a short sum.
+// longer (several: pairs have more than one), as with an activation and its
+// derivative over a short sum.
 // Measured: 1024 x 2048 x 2048 in tiles of 128, 256 and 512 20, 24 and 41 us, in
 // two parts 22, 19 and -; 8192 x 512 x 2048, gelu 44, 37 and 40; 8192 x 2048 x
 // 512 28, 22 and 33; 8192 x 14336 x 4096 -, 610 and 572.
-int64_t item_ns(int slices, int tile, bool alone, int busy, bool act) {
+int64_t item_ns(int slices, int tile, bool alone, int busy, bool act, bool several) {
   const int64_t product = tile == 2 * BN ? 630 : tile == BN ? 400 : 310;
   const int64_t bytes = alone ? static_cast<int64_t>(tile) * BK * 2 * busy / 6500 : 0;
   const int64_t sums = slices * std::max(product, bytes);
   if (tile == 2 * BN) return sums + (act ? 11000 : 5500);
-  return std::max<int64_t>(sums, tile == BN ? (act ? 7000 : 4000) : (act ? 5000 : 2500)) + 500;
+  return several ? std::max<int64_t>(sums, tile == BN ? (act ? 7000 : 4000) : (act ? 5000 : 2500)) : sums;
 }
 
 // A product [rows, cols] over K slices, and how it is cut.
@@ -866,7 +911,7 @@ struct Want {
   int tile, parts;
   int items() const { return ceil_div(rows, 2 * BM) * ceil_div(cols, tile) * parts; }
   int64_t ns(int busy) const {
-    return item_ns(ceil_div(slices, parts), tile, rows <= 2 * BM, std::min(busy, kUnits), act && parts == 1);
+    return item_ns(ceil_div(slices, parts), tile, rows <= 2 * BM, std::min(busy, kUnits), act && parts == 1, busy > kUnits);
   }
   // the join: a launch, and the sums' way to memory and back
   int64_t join_ns() const {
@@ -914,7 +959,7 @@ int64_t choose(Want& a, Want& b) {
       }
     }
   a = best_a, b = best_b;
-  return least + kTilesNs;
+  return least + kTilesNs + last_epilogue_ns(a.act);
 }
 
 // Bytes that the parts of a [rows, cols] product's sums need at most: 2 kUnits
@@ -988,25 +1033,66 @@ dmoe_status join(const Out* o, int parts_a, int parts_b, cudaStream_t st) {
   return DMOE_OK;
 }
 
-// The parts of few rows' product (a cluster's CTAs: 1, 2, 4 or 8, as many as
-// leave one CTA an SM), and its nanoseconds: slices of 16 KB of W, at what one
-// CTA draws or at its share of 6.5 TB/s.
-struct FewCut {
-  int parts;
+// Clusters of so many CTAs of a turned product that are resident together, as
+// the device answers once (of 8 there are fewer than 16, however many SMs are
+// free: 256 x 1024 x 1024 in 16 of them 14.2 us, in two waves; 0: it does not say).
+int resident_clusters(int parts, const dmoe::DeviceInfo& di) {
+  static std::atomic<int> kept[64][4];
+  const int at = parts == 8 ? 3 : parts == 4 ? 2 : parts == 2 ? 1 : 0;
+  int n = kept[di.device][at].load(std::memory_order_acquire);
+  if (n == 0) {
+    auto kern = turned_kernel<DMOE_ACT_NONE, kTurnedRows>;
+    constexpr size_t smem = PlanF<kTurnedRows>::SMEM;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(parts));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    kept[di.device][at].store(n, std::memory_order_release);
+  }
+  return n;
+}
+
+// The parts of a turned product (a cluster's CTAs: 1, 2, 4 or 8, as many as are
+// resident together), and its nanoseconds.  A slice takes a CTA 0.27 us, or its
+// share of HBM's 6.5 TB/s; the epilogue, four pairs of columns a thread in 1 us,
+// or of a whole tile 32 rows in 0.8.
+struct TurnedCut {
+  int rows, parts;
   int64_t ns;
 };
-FewCut cut_few(int K, int N) {
-  const int tiles = ceil_div(N, kFewTile), slices = ceil_div(K, BK);
+TurnedCut cut_turned(int M, int K, int N, const dmoe::DeviceInfo& di) {
+  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : kTurnedRows;
+  const int cols = ceil_div(N, kFewTile), blocks = ceil_div(M, rows), slices = ceil_div(K, BK);
+  const int64_t tiles = static_cast<int64_t>(cols) * blocks;
   int parts = 8;
-  while (parts > 1 && (tiles * parts > 2 * kUnits || slices < 2 * parts)) parts /= 2;
-  const int busy = std::min(tiles * parts, 2 * kUnits);
-  const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / 6500);
-  return FewCut{parts, static_cast<int64_t>(ceil_div(tiles * parts, 2 * kUnits)) * ceil_div(slices, parts) * slice + kFewNs};
+  while (parts > 1 && (slices < 2 * parts || tiles > resident_clusters(parts, di))) parts /= 2;
+  const int64_t busy = std::min<int64_t>(tiles * parts, 2 * kUnits);
+  const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / std::min<int64_t>(blocks, busy) / 6500);
+  const int64_t live = std::min(M, rows);
+  const int64_t epilogue =
+      parts > 1 ? ceil_div(live * (kFewTile / 2 / parts), 4 * kFewThreads) * 1000 : ceil_div(live, 4 * kFewEpiWarps) * 800;
+  const int64_t waves = (tiles * parts + 2 * kUnits - 1) / (2 * kUnits);
+  return TurnedCut{rows, parts, waves * (ceil_div(slices, parts) * slice + epilogue) + 10 * live + kTurnedNs};
 }
 
 template <int ACT, int ROWS>
-cudaError_t launch_few(const ParamsF& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
-  auto kern = few_rows_kernel<ACT, ROWS>;
+cudaError_t launch_turned(const ParamsF& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
+  auto kern = turned_kernel<ACT, ROWS>;
   constexpr size_t smem = PlanF<ROWS>::SMEM;
   static std::atomic<uint64_t> opted{0};
   const uint64_t bit = uint64_t(1) << di.device;
@@ -1022,19 +1108,21 @@ cudaError_t launch_few(const ParamsF& p, const dmoe::DeviceInfo& di, cudaStream_
 }
 
 template <int ACT>
-dmoe_status run_few(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const Out& o, int parts,
-                    const dmoe::DeviceInfo& di, cudaStream_t st) {
+dmoe_status run_turned(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const Out& o, const TurnedCut& cut,
+                       const dmoe::DeviceInfo& di, cudaStream_t st) {
   ParamsF p{};
-  p.box = o.rows;
-  p.tiles = ceil_div(o.cols, kFewTile);
-  p.parts = parts;
+  p.box = std::min(o.rows, cut.rows);
+  p.cols = ceil_div(o.cols, kFewTile);
+  p.tiles = p.cols * ceil_div(o.rows, cut.rows);
+  p.parts = cut.parts;
   p.slices = ceil_div(K, BK);
   p.o = o;
   p.err = di.err_word;
   if (!map_pitched(&p.map_w, w, K, o.cols, o.cols, 64, BK) || !map_pitched(&p.map_x, x, o.rows, K, ldx, BK, p.box))
     return DMOE_ERR_CUDA;
-  const cudaError_t e = o.rows <= 16 ? launch_few<ACT, 16>(p, di, st)
-                        : o.rows <= 32 ? launch_few<ACT, 32>(p, di, st) : launch_few<ACT, 64>(p, di, st);
+  const cudaError_t e = cut.rows == 16   ? launch_turned<ACT, 16>(p, di, st)
+                        : cut.rows == 32 ? launch_turned<ACT, 32>(p, di, st)
+                        : cut.rows == 64 ? launch_turned<ACT, 64>(p, di, st) : launch_turned<ACT, kTurnedRows>(p, di, st);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
@@ -1116,16 +1204,16 @@ DMOE_API dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t*
   if (s != DMOE_OK) return s;
   Want a{M, N, ceil_div(K, BK), act != DMOE_ACT_NONE}, none{};
   const int64_t ns = choose(a, none);
-  const FewCut few = cut_few(K, N);
-  const bool is_few = M <= kFewRows && few.ns < ns;
-  if (!is_few && a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
+  const TurnedCut cut = cut_turned(M, K, N, di);
+  const bool turned = cut.ns < ns;
+  if (!turned && a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
   const Out o{M, N, bias, bias_f32, deriv, residual, ldr, nullptr, y, 0, nullptr};
   float* part = static_cast<float*>(ws);
   cudaStream_t st = dmoe::as_stream(stream);
-  if (is_few) {
-    if (act == DMOE_ACT_GELU) return run_few<DMOE_ACT_GELU>(x, ldx, w, K, o, few.parts, di, st);
-    if (act == DMOE_ACT_SILU) return run_few<DMOE_ACT_SILU>(x, ldx, w, K, o, few.parts, di, st);
-    return run_few<DMOE_ACT_NONE>(x, ldx, w, K, o, few.parts, di, st);
+  if (turned) {
+    if (act == DMOE_ACT_GELU) return run_turned<DMOE_ACT_GELU>(x, ldx, w, K, o, cut, di, st);
+    if (act == DMOE_ACT_SILU) return run_turned<DMOE_ACT_SILU>(x, ldx, w, K, o, cut, di, st);
+    return run_turned<DMOE_ACT_NONE>(x, ldx, w, K, o, cut, di, st);
   }
   ParamsL p{};
   if (!map_pitched(&p.map_a[0], x, M, K, ldx, BK, box_rows(M)) || !map_pitched(&p.map_b[0], w, K, N, N, 64, BK))
