@@ -823,24 +823,27 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Join 
   }
 }
 
-// dz = bf16(dy deriv) (dz NULL: dy is dz), and the sums over every gridDim.y-th
-// stripe of rows of the unrounded products, one fp32 row each (sums NULL: none).
-// 256 columns a block, eight rows at a time.  dz is in 16 bits because both
+// dz = bf16(dy deriv) (dz NULL: dy is dz), and the sums over every gridDim.x-th
+// stripe of rows of the unrounded products: one fp32 row of `sums` each, or,
+// where the stripes are a cluster (JOINED), their sum in `sums` itself (sums NULL:
+// none).  256 columns a block, eight rows at a time.  dz is in 16 bits because both
 // products take it so: half a step of bf16 on each of a sum's terms.  HBM-bound:
 // 4093 x 10240 37 us, 6.8 TB/s (in one wave: with eight rows in flight and three
 // blocks an SM, in two, 70).
+template <bool JOINED>
 __global__ void __launch_bounds__(256) dz_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                                  const uint16_t* __restrict__ deriv, int M, int N,
                                                  uint16_t* __restrict__ dz, float* __restrict__ sums) {
   __shared__ float sh[8][256];
+  __shared__ float total[256];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
+  const int c = blockIdx.y * 256 + lane * 8;
   float s[8] = {};
   if (c < N) {
 #pragma unroll 4
-    for (int64_t r = blockIdx.y * 8 + warp; r < M; r += gridDim.y * 8) {
+    for (int64_t r = blockIdx.x * 8 + warp; r < M; r += gridDim.x * 8) {
       float f[8];
       unpack8x(__ldg(reinterpret_cast<const uint4*>(dy + r * lddy + c)), f);
       if (deriv) {
@@ -858,12 +861,21 @@ __global__ void __launch_bounds__(256) dz_kernel(const uint16_t* __restrict__ dy
 #pragma unroll
   for (int q = 0; q < 8; ++q) sh[warp][lane * 8 + q] = s[q];
   __syncthreads();
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < N) {
-    float t = 0.f;
+  const int col = blockIdx.y * 256 + threadIdx.x;
+  float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sh[w][threadIdx.x];
-    sums[static_cast<int64_t>(blockIdx.y) * N + col] = t;
+  for (int w = 0; w < 8; ++w) t += sh[w][threadIdx.x];
+  if (JOINED) {
+    total[threadIdx.x] = t;
+    cluster_sync();
+    if (cluster_ctarank() == 0 && col < N) {
+      t = 0.f;
+      for (unsigned q = 0; q < gridDim.x; ++q) t += dsmem_ld_f32(dsmem_addr(smem_u32(total + threadIdx.x), q));
+      sums[col] = t;
+    }
+    cluster_sync();  // the others' sums have been read
+  } else if (col < N) {
+    sums[static_cast<int64_t>(blockIdx.x) * N + col] = t;
   }
 }
 
@@ -955,8 +967,10 @@ int64_t choose(Want& a, Want& b) {
       if (!b.rows && tb != BN) continue;
       for (const int pa : kParts) {
         if (!tries(a, ta, pa)) break;
+        if (b.rows && (pa & (pa - 1))) continue;  // of two products powers of two alone: each try takes the host 50 ns
         for (const int pb : kParts) {
           if (pb > 1 && (!b.rows || !tries(b, tb, pb))) break;
+          if (pb & (pb - 1)) continue;
           a.tile = ta, a.parts = pa, b.tile = tb, b.parts = pb;
           weigh(a, b);
         }
@@ -1161,6 +1175,10 @@ bool off16(const void* a) { return !dmoe::aligned16(a); }
 // (it only reaches rows past it).
 int box_rows(int rows) { return std::min(rows, BM); }
 
+// Stripes of rows, a cluster, of a dz_kernel that joins its sums itself: up to
+// 128 rows each, 16 a warp (0: more rows, whose sums a launch of their own joins).
+int joined_stripes(int M) { return M > 1024 ? 0 : M > 128 ? 8 : M > 64 ? 4 : M > 32 ? 2 : 1; }
+
 // Stripes of rows whose sums dz_kernel leaves: some four blocks an SM.
 int stripes(int M, int N) {
   const int cols = ceil_div(N, 256);
@@ -1265,13 +1283,15 @@ DMOE_API dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, cons
   uint8_t* base = static_cast<uint8_t*>(ws);
   const uint16_t* dz = dy;
   int64_t lddz = lddy;
-  const int n = stripes(M, N);
+  const int joined = joined_stripes(M), n = joined ? joined : stripes(M, N);
   const bool products = dx || dw;
   if ((deriv && products) || dbias) {
     uint16_t* out = deriv && products ? reinterpret_cast<uint16_t*>(base + l.dz) : nullptr;
-    float* sums = dbias ? reinterpret_cast<float*>(base + l.sums) : nullptr;
-    const cudaError_t e = dmoe::launch_pdl(dz_kernel, dim3(ceil_div(N, 256), n), dim3(256), 0, st, dy, lddy, deriv, M, N,
-                                           out, sums);
+    float* sums = !dbias ? nullptr : joined ? dbias : reinterpret_cast<float*>(base + l.sums);
+    const dim3 grid(n, ceil_div(N, 256));
+    const cudaError_t e =
+        joined ? dmoe::launch_pdl_cluster(dz_kernel<true>, grid, dim3(256), 0, st, n, dy, lddy, deriv, M, N, out, sums)
+               : dmoe::launch_pdl(dz_kernel<false>, grid, dim3(256), 0, st, dy, lddy, deriv, M, N, out, sums);
     if (e != cudaSuccess) return dmoe::cuda_status(e);
     dmoe::count_launches(1);
     if (out) dz = out, lddz = N;
@@ -1299,7 +1319,7 @@ DMOE_API dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, cons
                                     reinterpret_cast<float*>(base + l.part_w), di, st);
     if (s != DMOE_OK) return s;
   }
-  if (dbias) {
+  if (dbias && !joined) {
     const cudaError_t e = dmoe::launch_pdl(dbias_kernel, dim3(ceil_div(N, 256)), dim3(256), 0, st,
                                            reinterpret_cast<const float*>(base + l.sums), n, N, dbias);
     if (e != cudaSuccess) return dmoe::cuda_status(e);
