@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads,
     unpack8(b[i], g);
     if (v < nvec) load_w<WF32>(w_post, v, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = fmaf(scale, g[j], f[j] * k * w[j]);
+    for (int j = 0; j < 8; ++j) f[j] = fmaf(f[j] * w[j], k, scale * g[j]);  // two bf16 values' product is exact
     b[i] = pack8(f);  // the kept stream: bf16, what the backward will read
     if (live && v < nvec) *(reinterpret_cast<uint4*>(h + t * d) + v) = b[i];
     else b[i] = make_uint4(0, 0, 0, 0);
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads,
     unpack8(b[i], f);
     load_w<WF32>(w_pre, v, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = f[j] * rh * w[j];
+    for (int j = 0; j < 8; ++j) f[j] = f[j] * w[j] * rh;
     *(reinterpret_cast<uint4*>(y + t * d) + v) = pack8(f);
   }
 }
