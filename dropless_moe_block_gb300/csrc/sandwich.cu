@@ -29,23 +29,28 @@ namespace {
 using namespace dmoe::rows;
 
 constexpr int kMaxD = 16384;
-constexpr int kMinThreads = 128;           // forward: of a block, while a row takes fewer
 constexpr int kMaxStages = 4;              // backward: rows in flight per group of threads
 constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
 constexpr int kBackThreads = 512;          // backward: threads per SM, 128 registers each
 
-// Five blocks of 256 threads an SM (48 registers) where a row takes that many:
-// 8192 x 4096 42.2 us, 45.4 with four, 48.2 with six; narrower rows are
-// better off with registers (8192 x 512: 7.8 us with 1024 threads an SM, 8.7 with
-// 1280).
+// Forward: threads of a block, whole rows of TPR threads, and blocks an SM.
+// Five blocks of 256 threads (48 registers): 8192 x 4096 42.2 us, 45.4 with
+// four, 48.2 with six; 320 threads, 4093 x 5120, likewise (29.6 us, 31.5 with
+// three).  Narrower rows are better off with registers (8192 x 512: 7.8 us with
+// 1024 threads an SM, 8.7 with 1280; 192 threads, 8192 x 3000, 33.2 with 1152,
+// 39.3 with 1344).
+__host__ __device__ constexpr int forward_block(int tpr) { return tpr == 96 ? 192 : tpr > 128 ? tpr : 128; }
+__host__ __device__ constexpr int forward_blocks(int tpr) {
+  return (tpr == 256 || tpr == 320 ? 1280 : tpr % 96 == 0 ? 1152 : 1024) / forward_block(tpr);
+}
+
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(TPR > kMinThreads ? TPR : kMinThreads,
-                                  TPR == 256 ? 5 : 1024 / (TPR > kMinThreads ? TPR : kMinThreads))
+__global__ void __launch_bounds__(forward_block(TPR), forward_blocks(TPR))
     sandwich_norm_kernel(const uint16_t* u, int64_t ldu, const uint16_t* x, int64_t ldx,
                          const void* __restrict__ w_post, const void* __restrict__ w_pre,
                          const float* __restrict__ gate, int gate_step, float scale, float eps, int T, int d,
                          uint16_t* h, uint16_t* y, float* __restrict__ rstd_u, float* __restrict__ rstd_h) {
-  constexpr int BLOCK = TPR > kMinThreads ? TPR : kMinThreads;
+  constexpr int BLOCK = forward_block(TPR);
   constexpr int RPB = BLOCK / TPR;
   __shared__ float red[2][BLOCK / 32];
   dmoe::pdl_wait();
@@ -422,8 +427,28 @@ __global__ void __launch_bounds__(1024) sandwich_sums_kernel(const float* __rest
   }
 }
 
-// Threads per row: the smallest power of two from 32 on that holds it at two
-// vectors a thread; above 8192 columns at four.
+// Forward: the fewest threads of these that hold a row at two vectors each; above
+// 8192 columns four.  (Where powers of two alone would leave up to half of
+// them without a second vector: 8192 x 2560 34 us in 256 threads, 28 in 160;
+// 8192 x 6144 87 in 512, 64 in 384.)
+template <typename F>
+cudaError_t forward_by_width(int d, const F& f) {
+  const int nvec = d >> 3;
+  if (nvec <= 2 * 32) return f.template operator()<32, 2>();
+  if (nvec <= 2 * 64) return f.template operator()<64, 2>();
+  if (nvec <= 2 * 96) return f.template operator()<96, 2>();
+  if (nvec <= 2 * 128) return f.template operator()<128, 2>();
+  if (nvec <= 2 * 160) return f.template operator()<160, 2>();
+  if (nvec <= 2 * 192) return f.template operator()<192, 2>();
+  if (nvec <= 2 * 256) return f.template operator()<256, 2>();
+  if (nvec <= 2 * 320) return f.template operator()<320, 2>();
+  if (nvec <= 2 * 384) return f.template operator()<384, 2>();
+  if (nvec <= 2 * 512) return f.template operator()<512, 2>();
+  return f.template operator()<512, 4>();
+}
+
+// Backward: threads per row: the smallest power of two from 32 on that holds it
+// at two vectors a thread; above 8192 columns at four.
 int threads_per_row(int d) {
   int tpr = 32;
   while (tpr < 512 && 2 * tpr < (d >> 3)) tpr *= 2;
@@ -464,8 +489,7 @@ struct Forward {
 
   template <int TPR, int VPT>
   cudaError_t operator()() const {
-    constexpr int block = TPR > kMinThreads ? TPR : kMinThreads;
-    const int rpb = block / TPR;
+    constexpr int block = forward_block(TPR), rpb = block / TPR;
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + rpb - 1) / rpb));
     auto kern = wf32 ? sandwich_norm_kernel<TPR, VPT, true> : sandwich_norm_kernel<TPR, VPT, false>;
     return dmoe::launch_pdl(kern, grid, dim3(block), 0, st, u, ldu, x, ldx, w_post, w_pre, gate, gate_step, scale, eps,
@@ -525,7 +549,7 @@ DMOE_API dmoe_status dmoe_sandwich_norm(const uint16_t* u, int64_t ldu, const ui
   if (s != DMOE_OK) return s;
   const Forward f{u, ldu, residual, ldr, w_post, w_pre, weight_f32, gate, gate_rows == 1 ? 0 : 1, scale, eps, T, d,
                   h, y, rstd_u, rstd_h, dmoe::as_stream(stream)};
-  const cudaError_t e = by_width(d, f);
+  const cudaError_t e = forward_by_width(d, f);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;

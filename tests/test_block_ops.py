@@ -389,6 +389,16 @@ def check_backward(got, ref, size, T):
             close(got[n], ref[n], (e + T * U32) * size[n], n)
 
 
+WIDTHS = [512, 520, 1024, 1032, 1536, 1544, 2048, 2056, 2560, 2568, 3064, 3080, 4096, 4104, 5120, 5128, 6144, 6152, 8192]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", WIDTHS)
+def test_sandwich_norm_on_both_sides_of_every_width(dm, d):
+    for T, kind, wf32, scale in ((9, "row", False, 0.7), (160, "one", True, 1.0)):
+        test_sandwich_norm(dm, T, d, kind, wf32, scale)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,d", SIZES + [(3001, 72)])
 @pytest.mark.parametrize("kind,wf32,scale,stream", [("none", False, 1.0, True), ("row", True, 0.7, False),
