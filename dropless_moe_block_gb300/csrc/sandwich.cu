@@ -31,7 +31,6 @@ using namespace dmoe::rows;
 constexpr int kMaxD = 16384;
 constexpr int kMaxStages = 4;              // backward: rows in flight per group of threads
 constexpr size_t kRingBytes = 200 * 1024;  // of shared memory for them per SM
-constexpr int kBackThreads = 512;          // backward: threads per SM, 128 registers each
 
 // Forward: threads of a block, whole rows of TPR threads, and blocks an SM.
 // Five blocks of 256 threads (48 registers): 8192 x 4096 42.2 us, 45.4 with
@@ -183,15 +182,19 @@ __device__ __forceinline__ float three_sums(const float* s, int lane) {
 // (8192 x 4096: 99 us with one vector and value by value, 71 so; 8191 x 512,
 // with blocks of four rows that wait for one another and leave 608 partial
 // rows, 19 us, 17.7 with groups).
+// Its threads, one block an SM: whole groups of a row's threads, 128 registers each.
+__host__ __device__ constexpr int back_threads(int tpr) { return 512 / tpr * tpr; }
+
 template <int TPR, int VPT, bool WF32>
-__global__ void __launch_bounds__(kBackThreads, 1) sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
+__global__ void __launch_bounds__(back_threads(TPR), 1) sandwich_norm_backward_kernel(const __grid_constant__ Back p) {
   using namespace dmoe::tc;
   using dmoe::f2_fma;
   using dmoe::f2_mul;
-  constexpr int GROUPS = kBackThreads / TPR;
+  constexpr int THREADS = back_threads(TPR);
+  constexpr int GROUPS = THREADS / TPR;
   constexpr int WPR = TPR / 32;
   constexpr bool KEEP = VPT <= 2;  // the weights in registers
-  __shared__ float red[2][kBackThreads / 32 * 4];
+  __shared__ float red[2][THREADS / 32 * 4];
   __shared__ uint64_t full[GROUPS][kMaxStages];
   __shared__ int gave_up[GROUPS];
   extern __shared__ __align__(16) uint8_t ring[];  // [GROUPS][stages][dy, u, h, dh][d], then the weights' sums
@@ -292,13 +295,10 @@ __global__ void __launch_bounds__(kBackThreads, 1) sandwich_norm_backward_kernel
       if ((lane & 7) == 0) red[flip][(threadIdx.x >> 5) * 4 + (lane >> 3)] = sum;
       meet();
       const float* r = red[flip] + rg * WPR * 4;
-      if (WPR >= 8) {
-        sum = r[lane];
+      sum = lane < 4 * WPR ? r[lane] : 0.f;
 #pragma unroll
-        for (int k = 1; k < WPR / 8; ++k) sum += r[lane + 32 * k];
-      } else {
-        sum = lane < 4 * WPR ? r[lane] : 0.f;
-      }
+      for (int k = 32; k < 4 * WPR; k += 32)
+        if (lane + k < 4 * WPR) sum += r[lane + k];
 #pragma unroll
       for (int o = 16; o > 2; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) sandwich_norm_backward_kernel
   }
   __syncthreads();
   float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * d;
-  for (int i = threadIdx.x; i < d / 2; i += kBackThreads) {  // four columns of 2 d
+  for (int i = threadIdx.x; i < d / 2; i += THREADS) {  // four columns of 2 d
     float4 a = reinterpret_cast<const float4*>(sums)[i];
 #pragma unroll
     for (int g = 1; g < GROUPS; ++g) {
@@ -447,12 +447,13 @@ cudaError_t forward_by_width(int d, const F& f) {
   return f.template operator()<512, 4>();
 }
 
-// Backward: threads per row: the smallest power of two from 32 on that holds it
-// at two vectors a thread; above 8192 columns at four.
+// Backward: threads per row, likewise (8192 x 1280 35 us in 128 threads, 29 in 96;
+// 8192 x 2560 56 in 256, 47 in 160; 192 and 384 gain nothing, as fewer than 480
+// threads an SM are left).
 int threads_per_row(int d) {
-  int tpr = 32;
-  while (tpr < 512 && 2 * tpr < (d >> 3)) tpr *= 2;
-  return tpr;
+  for (const int tpr : {32, 64, 96, 128, 160, 256})
+    if ((d >> 3) <= 2 * tpr) return tpr;
+  return 512;
 }
 
 template <typename F>
@@ -460,13 +461,15 @@ cudaError_t by_width(int d, const F& f) {
   switch (threads_per_row(d)) {
     case 32: return f.template operator()<32, 2>();
     case 64: return f.template operator()<64, 2>();
+    case 96: return f.template operator()<96, 2>();
     case 128: return f.template operator()<128, 2>();
+    case 160: return f.template operator()<160, 2>();
     case 256: return f.template operator()<256, 2>();
     default: return (d >> 3) <= 1024 ? f.template operator()<512, 2>() : f.template operator()<512, 4>();
   }
 }
 
-size_t back_stage_bytes(int d) { return static_cast<size_t>(kBackThreads / threads_per_row(d)) * d * 2 * 4; }
+size_t back_stage_bytes(int d) { return static_cast<size_t>(back_threads(threads_per_row(d)) / threads_per_row(d)) * d * 2 * 4; }
 int ring_stages(int d) { return static_cast<int>(std::clamp<size_t>(kRingBytes / back_stage_bytes(d), 1, kMaxStages)); }
 
 // Blocks of the backward: one an SM, each leaving one partial row.
@@ -516,7 +519,7 @@ struct Backward {
       if (e != cudaSuccess) return e;
       opted.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return dmoe::launch_pdl(kern, dim3(blocks), dim3(kBackThreads), p.stages * back_stage_bytes(p.d), st, p);
+    return dmoe::launch_pdl(kern, dim3(blocks), dim3(back_threads(TPR)), p.stages * back_stage_bytes(p.d), st, p);
   }
 
   template <int TPR, int VPT>

@@ -427,6 +427,13 @@ def test_sandwich_norm_backward(dm, T, d, kind, wf32, scale, stream):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", WIDTHS)
+def test_sandwich_norm_backward_on_both_sides_of_every_width(dm, d):
+    for T, kind, wf32, scale, stream in ((9, "row", False, 0.7, True), (1600, "one", True, 1.0, False)):
+        test_sandwich_norm_backward(dm, T, d, kind, wf32, scale, stream)
+
+
+@pytest.mark.gpu
 def test_sandwich_norm_against_differences(dm):
     """The backward against differences of the 64-bit forward (its h unrounded)."""
     T, d, eps, scale = 4, 40, 1e-5, 0.8
