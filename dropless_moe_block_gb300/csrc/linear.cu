@@ -17,8 +17,8 @@
 // sub-tiles that share each K slice's rows of the first operand), 256 x 256 or
 // 256 x 128; both gradients' tiles go in one launch.  Where there are fewer
 // tiles than pairs the sum is cut into parts, whose fp32 sums a second launch
-// joins in a fixed order.  Products of few rows, and small ones, run turned
-// round, on clusters (turned_kernel).
+// joins in a fixed order.  The forward product of few rows, and small ones, run
+// turned round, on clusters (turned_kernel).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -463,34 +463,21 @@ __global__ void __launch_bounds__(kThreadsL, 1) linear_kernel(const __grid_const
 // products, too, are done sooner in 5 us of launch, first loads and epilogue
 // than in the 8 of the pairs below.  (us, those and these: 1 x 14336 x 4096
 // 26.5 and 22, 64 x 1024 x 1024 12.2 and 6.1, 128 x 4096 x 4096 18.5 and 13.2,
-// 512 x 1024 x 1024 12.8 and 8.0.)  Small gradients likewise, the tiles of both
-// products in one launch, cut into the same number of parts (M x K x N with dz and
-// dbias: 1024 x 1024 x 1024 24.6 and 16.7, 1000 x 512 x 2048 28.1 and 20.0, 512 x
-// 4096 x 4096 39.0 and 33.0).
+// 512 x 1024 x 1024 12.8 and 8.0.)  The gradients, of which one has a long sum or
+// many tiles, gained nothing turned: with both in one launch of clusters 70 sizes
+// from 8 x 512 x 512 on took the same or up to 19% more.
 constexpr int kTurnedRows = 128;  // of a block
 constexpr int kFewTile = 128;     // columns of W
 constexpr int kFewStages = 11;
 constexpr int kFewEpiWarps = 8;
 constexpr int kFewThreads = 64 + 32 * kFewEpiWarps;  // with the TMA producer and the MMA issuer
 
-// One product D = A B^T, as the tensor cores see it: A's rows (128 a tile) are
-// the columns of the output, B's rows (ROWS a block) its rows.
-//   y   A: W along its columns   B: x along the sum
-//   dx  A: W along the sum       B: dz along the sum
-//   dW  A: dz along its columns  B: x along its columns
-struct Turned {
-  CUtensorMap map_a, map_b;
-  int a_mn, b_mn;   // operands that lie along the output rather than along the sum
-  int box;          // rows of B that are loaded, of one that lies along the sum
-  int cols, tiles;  // tiles over the columns, and over the blocks of rows
-  int slices;
-  Out o;
-};
-
-template <bool BACK>
 struct ParamsF {
-  Turned t[BACK ? 2 : 1];  // the second one's tiles, if it has some, come behind the first one's
-  int tiles, parts, log_parts;
+  CUtensorMap map_w, map_x;
+  int box;  // rows of x that are loaded
+  int cols;  // tiles over the columns
+  int tiles, parts, log_parts, slices;  // tiles: over the columns, then over the blocks of rows
+  Out o;
   int32_t* err;
 };
 
@@ -544,9 +531,8 @@ __device__ __forceinline__ float2 dsmem_ld_f32x2(uint32_t addr) {
   return v;
 }
 
-// BACK: dx, dW or both; else y, of one product and with no part empty.
-template <int ACT, int ROWS, bool BACK>
-__global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_constant__ ParamsF<BACK> p) {
+template <int ACT, int ROWS>
+__global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_constant__ ParamsF p) {
   using PL = PlanF<ROWS>;
   constexpr int STAGES = PL::STAGES;
   constexpr uint32_t TMEM_COLS = 2 * ROWS;
@@ -571,8 +557,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_map(&p.t[0].map_a);
-    tma_prefetch_map(&p.t[0].map_b);
+    tma_prefetch_map(&p.map_w);
+    tma_prefetch_map(&p.map_x);
   }
   if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
   fence_before_sync();
@@ -585,22 +571,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
   const int rank = p.parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = static_cast<int>(blockIdx.x) >> p.log_parts;
   const int next = p.parts > 1 ? p.tiles : static_cast<int>(gridDim.x);
-  // a tile's product, its place there and this part's slices (fewer slices than parts: some have none)
-  struct Place {
-    int which, block, c0, k0, k1;
-  };
-  auto place = [&](int tile) {
-    Place at;
-    at.which = BACK && tile >= p.t[0].tiles;
-    const Turned& t = p.t[at.which];
-    if (at.which) tile -= p.t[0].tiles;
-    at.block = tile / t.cols;
-    at.c0 = (tile - at.block * t.cols) * kFewTile;
-    at.k0 = t.slices * rank >> p.log_parts;  // below 2^31: slices are 64 long
-    at.k1 = t.slices * (rank + 1) >> p.log_parts;
-    return at;
-  };
-  const int quad = warp & 3;  // epilogue: TMEM lanes, and columns, 32 quad .. 32 quad + 31
+  const int k0 = p.slices * rank >> p.log_parts, k1 = p.slices * (rank + 1) >> p.log_parts;  // below 2^31: 64 long
+  const int quad = warp & 3;  // epilogue: TMEM lanes, and columns of W, 32 quad .. 32 quad + 31
   float* sums = reinterpret_cast<float*>(smem);  // parts > 1: [M][kFewTile], once the ring is done with
   bool ok = true;
   if (warp == 0) {
@@ -608,29 +580,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
       int stage = 0;
       uint32_t phase = 0;
       for (int tile = first; ok && tile < p.tiles; tile += next) {
-        const Place at = place(tile);
-        const Turned& t = p.t[at.which];
-        const bool a_mn = BACK ? t.a_mn : true, b_mn = BACK ? t.b_mn : false;
-        const uint32_t bytes = PL::W_BYTES + (b_mn ? ROWS / 64 * ATOM : static_cast<uint32_t>(t.box) * BK * 2);
-        for (int i = at.k0; i < at.k1; ++i) {
+        const int block = tile / p.cols, c0 = (tile - block * p.cols) * kFewTile;
+        for (int i = k0; i < k1; ++i) {
           ok = mbar_wait(empty + stage, phase ^ 1u, abort_flag);
           if (!ok) break;
-          uint8_t* sa = smem + stage * PL::STAGE;
-          uint8_t* sb = sa + PL::W_BYTES;
-          mbar_arrive_expect_tx(full + stage, bytes);
-          if (a_mn) {
-            tma_load_2d(sa, &t.map_a, full + stage, at.c0, i * BK);
-            tma_load_2d(sa + ATOM, &t.map_a, full + stage, at.c0 + 64, i * BK);
-          } else {
-            tma_load_2d(sa, &t.map_a, full + stage, i * BK, at.c0);
-          }
-          if (b_mn) {
-#pragma unroll
-            for (int h = 0; h < ROWS / 64; ++h)
-              tma_load_2d(sb + h * ATOM, &t.map_b, full + stage, at.block * ROWS + 64 * h, i * BK);
-          } else {
-            tma_load_2d(sb, &t.map_b, full + stage, i * BK, at.block * ROWS);
-          }
+          uint8_t* sw = smem + stage * PL::STAGE;
+          mbar_arrive_expect_tx(full + stage, PL::W_BYTES + p.box * BK * 2);
+          tma_load_2d(sw, &p.map_w, full + stage, c0, i * BK);
+          tma_load_2d(sw + ATOM, &p.map_w, full + stage, c0 + 64, i * BK);
+          tma_load_2d(sw + PL::W_BYTES, &p.map_x, full + stage, i * BK, block * ROWS);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -651,24 +609,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
       int stage = 0;
       uint32_t phase = 0, acc = 0, acc_phase = 0;
       constexpr uint32_t MN_STEP = (UMMA_K * 128) >> 4, K_STEP = (UMMA_K * 2) >> 4;
+      const uint64_t a0 = sdesc_sw128(smem_u32(smem), ATOM, 1024);
+      const uint64_t b0 = sdesc_sw128(smem_u32(smem) + PL::W_BYTES, 16, 1024);
+      constexpr uint32_t idesc = idesc_bf16(kFewTile, ROWS, true, false);
       for (int tile = first; ok && tile < p.tiles; tile += next) {
-        const Place at = place(tile);
-        const bool a_mn = BACK ? p.t[at.which].a_mn : true, b_mn = BACK ? p.t[at.which].b_mn : false;
-        const uint64_t a0 = sdesc_sw128(smem_u32(smem), a_mn ? ATOM : 16, 1024);
-        const uint64_t b0 = sdesc_sw128(smem_u32(smem) + PL::W_BYTES, b_mn ? ATOM : 16, 1024);
-        const uint32_t a_step = a_mn ? MN_STEP : K_STEP, b_step = b_mn ? MN_STEP : K_STEP;
-        const uint32_t idesc = idesc_bf16(kFewTile, ROWS, a_mn, b_mn);
         ok = mbar_wait(tempty + acc, acc_phase ^ 1u, abort_flag);
         if (!ok) break;
         fence_after_sync();
-        for (int i = at.k0; i < at.k1; ++i) {
+        for (int i = k0; i < k1; ++i) {
           ok = mbar_wait(full + stage, phase, abort_flag);
           if (!ok) break;
           fence_after_sync();
           const uint64_t off = static_cast<uint64_t>(stage) * (PL::STAGE >> 4);
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk)
-            mma_bf16(tmem_base + acc * ROWS, a0 + off + a_step * kk, b0 + off + b_step * kk, idesc, i > at.k0 || kk > 0);
+            mma_bf16(tmem_base + acc * ROWS, a0 + off + MN_STEP * kk, b0 + off + K_STEP * kk, idesc, i > k0 || kk > 0);
           mma_commit(empty + stage);
           if (++stage == STAGES) {
             stage = 0;
@@ -686,15 +641,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
   } else {
     uint32_t acc = 0, acc_phase = 0;
     for (int tile = first; ok && tile < p.tiles; tile += next) {
-      const Place at = place(tile);
-      const Out& o = p.t[at.which].o;
-      const int c = at.c0 + quad * 32 + lane;
-      const int row0 = at.block * ROWS, rows = min(ROWS, o.rows - row0);
-      const bool empty_part = BACK && at.k0 == at.k1;
+      const int block = tile / p.cols, c = (tile - block * p.cols) * kFewTile + quad * 32 + lane;
+      const int row0 = block * ROWS, rows = min(ROWS, p.o.rows - row0);
       float bias = 0.f;
-      if (!BACK && p.parts == 1 && o.bias && c < o.cols)
-        bias = o.bias_f32 ? __ldg(static_cast<const float*>(o.bias) + c)
-                          : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(o.bias) + c)) << 16);
+      if (p.parts == 1 && p.o.bias && c < p.o.cols)
+        bias = p.o.bias_f32 ? __ldg(static_cast<const float*>(p.o.bias) + c)
+                            : __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.o.bias) + c)) << 16);
       ok = mbar_wait(tfull + acc, acc_phase, abort_flag);
       if (!ok) break;
       __syncwarp();
@@ -704,39 +656,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
       for (int r = (warp - 2) / 4 * 16; r < rows; r += kFewEpiWarps / 4 * 16) {
         float v[16];
         __syncwarp();
-        if (empty_part) {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = 0.f;
-        } else {
-          tmem_load16(tb + r, v);
-        }
+        tmem_load16(tb + r, v);
         if (p.parts > 1) {
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             if (r + q < rows) sums[(r + q) * kFewTile + quad * 32 + lane] = v[q];
-        } else if (c < o.cols) {
-          // what is added or multiplied is fetched for all rows at once: the output may be where it lies
+        } else if (c < p.o.cols) {
+          // what is added is fetched for all rows at once: y may be where it lies
           uint16_t add[16];
-          const uint16_t* from = BACK ? o.factor : o.residual;
-          const int64_t ld = BACK ? o.cols : o.ld_res;
-          if (from) {
+          if (p.o.residual) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) add[q] = r + q < rows ? from[(row0 + r + q) * ld + c] : 0;
+            for (int q = 0; q < 16; ++q) add[q] = r + q < rows ? p.o.residual[(row0 + r + q) * p.o.ld_res + c] : 0;
           }
-          const int64_t to = static_cast<int64_t>(row0 + r) * o.cols + c;
+          const int64_t at = static_cast<int64_t>(row0 + r) * p.o.cols + c;
 #pragma unroll
           for (int q = 0; q < 16; q += 2) {
             float2 y, g;
             act_pair<ACT>(make_float2(v[q] + bias, v[q + 1] + bias), y, g);
-            const float2 w = make_float2(__uint_as_float(add[q] << 16), __uint_as_float(add[q + 1] << 16));
-            if (from) y = BACK ? dmoe::f2_mul(y, w) : dmoe::f2_add(y, w);
+            if (p.o.residual) y = dmoe::f2_add(y, make_float2(__uint_as_float(add[q] << 16), __uint_as_float(add[q + 1] << 16)));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               if (r + q + j >= rows) continue;
-              const int64_t e = to + static_cast<int64_t>(q + j) * o.cols;
-              if (ACT != DMOE_ACT_NONE && o.deriv) o.deriv[e] = bf16_bits(j ? g.y : g.x);
-              if (BACK && o.f32) static_cast<float*>(o.out)[e] = j ? y.y : y.x;
-              else static_cast<uint16_t*>(o.out)[e] = bf16_bits(j ? y.y : y.x);
+              if (ACT != DMOE_ACT_NONE && p.o.deriv) p.o.deriv[at + static_cast<int64_t>(q + j) * p.o.cols] = bf16_bits(j ? g.y : g.x);
+              static_cast<uint16_t*>(p.o.out)[at + static_cast<int64_t>(q + j) * p.o.cols] = bf16_bits(j ? y.y : y.x);
             }
           }
         }
@@ -765,44 +707,40 @@ __global__ void __launch_bounds__(kFewThreads, 1) turned_kernel(const __grid_con
     // this CTA's share of the columns, of all rows, two columns at a time; four of
     // those pairs together, for the way to the other CTAs and to what is added
     const int log_pairs = 6 - p.log_parts, share = 2 << log_pairs;
-    const Place at = place(first);
-    const Out& o = p.t[at.which].o;
-    const int row0 = at.block * ROWS, rows = min(ROWS, o.rows - row0);
+    const int block = first / p.cols, c0 = (first - block * p.cols) * kFewTile;
+    const int row0 = block * ROWS, rows = min(ROWS, p.o.rows - row0);
     const int from = rank * share, pairs = rows << log_pairs;
-    const uint16_t* beside = BACK ? o.factor : o.residual;
-    const int64_t ld = BACK ? o.cols : o.ld_res;
     for (int i0 = threadIdx.x; i0 < pairs; i0 += 4 * kFewThreads) {
       float2 v[4][8], bias[4];
       uint32_t add[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * kFewThreads;
-        const int r = i >> log_pairs, col = from + 2 * (i & (share / 2 - 1)), c = at.c0 + col;
+        const int r = i >> log_pairs, col = from + 2 * (i & (share / 2 - 1)), c = c0 + col;
         bias[j] = make_float2(0.f, 0.f);
         add[j] = 0;
-        if (i >= pairs || c >= o.cols) continue;
-        const uint32_t sum = smem_u32(sums + r * kFewTile + col);
+        if (i >= pairs || c >= p.o.cols) continue;
+        const uint32_t at = smem_u32(sums + r * kFewTile + col);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[j][q] = q < p.parts ? dsmem_ld_f32x2(dsmem_addr(sum, q)) : make_float2(0.f, 0.f);
-        if (!BACK && o.bias)
-          bias[j] = o.bias_f32 ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(o.bias) + c))
-                               : pair_of(__ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(o.bias) + c)));
-        if (beside) add[j] = *reinterpret_cast<const uint32_t*>(beside + (row0 + r) * ld + c);
+        for (int q = 0; q < 8; ++q) v[j][q] = q < p.parts ? dsmem_ld_f32x2(dsmem_addr(at, q)) : make_float2(0.f, 0.f);
+        if (p.o.bias)
+          bias[j] = p.o.bias_f32 ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p.o.bias) + c))
+                                 : pair_of(__ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.o.bias) + c)));
+        if (p.o.residual) add[j] = *reinterpret_cast<const uint32_t*>(p.o.residual + (row0 + r) * p.o.ld_res + c);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * kFewThreads;
-        const int r = i >> log_pairs, c = at.c0 + from + 2 * (i & (share / 2 - 1));
-        if (i >= pairs || c >= o.cols) continue;
+        const int r = i >> log_pairs, c = c0 + from + 2 * (i & (share / 2 - 1));
+        if (i >= pairs || c >= p.o.cols) continue;
         float2 sum = v[j][0], y, g;
 #pragma unroll
         for (int q = 1; q < 8; ++q) sum = dmoe::f2_add(sum, v[j][q]);
         act_pair<ACT>(dmoe::f2_add(sum, bias[j]), y, g);
-        const int64_t to = static_cast<int64_t>(row0 + r) * o.cols + c;
-        if (ACT != DMOE_ACT_NONE && o.deriv) *reinterpret_cast<uint32_t*>(o.deriv + to) = bf16_pair(g);
-        if (beside) y = BACK ? dmoe::f2_mul(y, pair_of(add[j])) : dmoe::f2_add(y, pair_of(add[j]));
-        if (BACK && o.f32) *reinterpret_cast<float2*>(static_cast<float*>(o.out) + to) = y;
-        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o.out) + to) = bf16_pair(y);
+        const int64_t to = static_cast<int64_t>(row0 + r) * p.o.cols + c;
+        if (ACT != DMOE_ACT_NONE && p.o.deriv) *reinterpret_cast<uint32_t*>(p.o.deriv + to) = bf16_pair(g);
+        if (p.o.residual) y = dmoe::f2_add(y, pair_of(add[j]));
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o.out) + to) = bf16_pair(y);
       }
     }
     __syncwarp();
@@ -890,7 +828,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Join 
 // stripe of rows of the unrounded products: one fp32 row of `sums` each, or,
 // where the stripes are a cluster (JOINED), their sum in `sums` itself (sums NULL:
 // none).  256 columns a block, eight rows at a time; JOINED, for fewer rows, 64
-// columns and 32 rows, for more blocks.  dz is in 16 bits because both
+// columns and 32 rows, for more blocks (a whole backward of 1024 x 1024 x 1024
+// takes 16.9 us so, 25 in 256 columns).  dz is in 16 bits because both
 // products take it so: half a step of bf16 on each of a sum's terms.  HBM-bound:
 // 4093 x 10240 37 us, 6.8 TB/s (in one wave: with eight rows in flight and three
 // blocks an SM, in two, 70).
@@ -1126,7 +1065,7 @@ int resident_clusters(int parts, const dmoe::DeviceInfo& di) {
   const int at = parts == 8 ? 3 : parts == 4 ? 2 : parts == 2 ? 1 : 0;
   int n = kept[di.device][at].load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = turned_kernel<DMOE_ACT_NONE, kTurnedRows, false>;
+    auto kern = turned_kernel<DMOE_ACT_NONE, kTurnedRows>;
     constexpr size_t smem = PlanF<kTurnedRows>::SMEM;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
       (void)cudaGetLastError();
@@ -1152,41 +1091,32 @@ int resident_clusters(int parts, const dmoe::DeviceInfo& di) {
   return n;
 }
 
-// The parts of up to two turned products (a cluster's CTAs: 1, 2, 4 or 8, as
-// many as are resident together), and their nanoseconds.  A slice takes a CTA
-// 0.27 us, or its share of HBM's 6.5 TB/s; the epilogue, four pairs of columns a
-// thread in 1 us, or of a whole tile 32 rows in 0.8.
+// The parts of a turned product (a cluster's CTAs: 1, 2, 4 or 8, as many as are
+// resident together), and its nanoseconds.  A slice takes a CTA 0.27 us, or its
+// share of HBM's 6.5 TB/s; the epilogue, four pairs of columns a thread in 1 us,
+// or of a whole tile 32 rows in 0.8.
 struct TurnedCut {
   int rows, parts;
   int64_t ns;
 };
-struct TurnedSize {
-  int rows, cols, sum;  // rows == 0: no such product
-};
-TurnedCut cut_turned(const TurnedSize& x, const TurnedSize& y, const dmoe::DeviceInfo& di) {
-  const int rows = y.rows || x.rows > 64 ? kTurnedRows : x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : 64;
-  auto tiles_of = [&](const TurnedSize& t) { return t.rows ? static_cast<int64_t>(ceil_div(t.cols, kFewTile)) * ceil_div(t.rows, rows) : 0; };
-  auto slices_of = [](const TurnedSize& t) { return t.rows ? ceil_div(t.sum, BK) : 0; };
-  const int64_t tiles = tiles_of(x) + tiles_of(y);
+TurnedCut cut_turned(int M, int K, int N, const dmoe::DeviceInfo& di) {
+  const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : kTurnedRows;
+  const int cols = ceil_div(N, kFewTile), blocks = ceil_div(M, rows), slices = ceil_div(K, BK);
+  const int64_t tiles = static_cast<int64_t>(cols) * blocks;
   int parts = 8;
-  while (parts > 1 && (std::max(slices_of(x), slices_of(y)) < 2 * parts || tiles > resident_clusters(parts, di))) parts /= 2;
+  while (parts > 1 && (slices < 2 * parts || tiles > resident_clusters(parts, di))) parts /= 2;
   const int64_t busy = std::min<int64_t>(tiles * parts, 2 * kUnits);
+  const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / std::min<int64_t>(blocks, busy) / 6500);
+  const int64_t live = std::min(M, rows);
+  const int64_t epilogue =
+      parts > 1 ? ceil_div(live * (kFewTile / 2 / parts), 4 * kFewThreads) * 1000 : ceil_div(live, 4 * kFewEpiWarps) * 800;
   const int64_t waves = (tiles * parts + 2 * kUnits - 1) / (2 * kUnits);
-  int64_t longest = 0;
-  for (const TurnedSize& t : {x, y}) {
-    if (!t.rows) continue;
-    const int64_t blocks = std::min<int64_t>(ceil_div(t.rows, rows), busy), live = std::min(t.rows, rows);
-    const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / blocks / 6500);
-    const int64_t epilogue = parts > 1 ? ceil_div(live * (kFewTile / 2 / parts), 4 * kFewThreads) * 1000
-                                       : ceil_div(live, 4 * kFewEpiWarps) * 800;
-    longest = std::max(longest, ceil_div(slices_of(t), parts) * slice + epilogue + 10 * live);
-  }
-  return TurnedCut{rows, parts, waves * longest + kTurnedNs};
+  return TurnedCut{rows, parts, waves * (ceil_div(slices, parts) * slice + epilogue) + 10 * live + kTurnedNs};
 }
 
-template <int ACT, int ROWS, bool BACK>
-cudaError_t launch_turned(const ParamsF<BACK>& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
-  auto kern = turned_kernel<ACT, ROWS, BACK>;
+template <int ACT, int ROWS>
+cudaError_t launch_turned(const ParamsF& p, const dmoe::DeviceInfo& di, cudaStream_t st) {
+  auto kern = turned_kernel<ACT, ROWS>;
   constexpr size_t smem = PlanF<ROWS>::SMEM;
   static std::atomic<uint64_t> opted{0};
   const uint64_t bit = uint64_t(1) << di.device;
@@ -1201,25 +1131,23 @@ cudaError_t launch_turned(const ParamsF<BACK>& p, const dmoe::DeviceInfo& di, cu
                                   p);
 }
 
-// A turned product's place in the parameters: its tiles and slices.
-void place_turned(Turned& t, const Out& o, int sum, int rows, bool a_mn, bool b_mn) {
-  t.a_mn = a_mn, t.b_mn = b_mn;
-  t.box = std::min(o.rows, rows);
-  t.cols = ceil_div(o.cols, kFewTile);
-  t.tiles = t.cols * ceil_div(o.rows, rows);
-  t.slices = ceil_div(sum, BK);
-  t.o = o;
-}
-
-template <int ACT, bool BACK>
-dmoe_status run_turned(ParamsF<BACK>& p, const TurnedCut& cut, const dmoe::DeviceInfo& di, cudaStream_t st) {
-  p.tiles = p.t[0].tiles + (BACK ? p.t[BACK].tiles : 0);
+template <int ACT>
+dmoe_status run_turned(const uint16_t* x, int64_t ldx, const uint16_t* w, int K, const Out& o, const TurnedCut& cut,
+                       const dmoe::DeviceInfo& di, cudaStream_t st) {
+  ParamsF p{};
+  p.box = std::min(o.rows, cut.rows);
+  p.cols = ceil_div(o.cols, kFewTile);
+  p.tiles = p.cols * ceil_div(o.rows, cut.rows);
   p.parts = cut.parts;
   p.log_parts = cut.parts == 8 ? 3 : cut.parts / 2;
+  p.slices = ceil_div(K, BK);
+  p.o = o;
   p.err = di.err_word;
-  const cudaError_t e = cut.rows == 16   ? launch_turned<ACT, 16, BACK>(p, di, st)
-                        : cut.rows == 32 ? launch_turned<ACT, 32, BACK>(p, di, st)
-                        : cut.rows == 64 ? launch_turned<ACT, 64, BACK>(p, di, st) : launch_turned<ACT, kTurnedRows, BACK>(p, di, st);
+  if (!map_pitched(&p.map_w, w, K, o.cols, o.cols, 64, BK) || !map_pitched(&p.map_x, x, o.rows, K, ldx, BK, p.box))
+    return DMOE_ERR_CUDA;
+  const cudaError_t e = cut.rows == 16   ? launch_turned<ACT, 16>(p, di, st)
+                        : cut.rows == 32 ? launch_turned<ACT, 32>(p, di, st)
+                        : cut.rows == 64 ? launch_turned<ACT, 64>(p, di, st) : launch_turned<ACT, kTurnedRows>(p, di, st);
   if (e != cudaSuccess) return dmoe::cuda_status(e);
   dmoe::count_launches(1);
   return DMOE_OK;
@@ -1305,20 +1233,16 @@ DMOE_API dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t*
   if (s != DMOE_OK) return s;
   Want a{M, N, ceil_div(K, BK), act != DMOE_ACT_NONE}, none{};
   const int64_t ns = choose(a, none);
-  const TurnedCut cut = cut_turned({M, N, K}, {0, 0, 0}, di);
+  const TurnedCut cut = cut_turned(M, K, N, di);
   const bool turned = cut.ns < ns;
   if (!turned && a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
   const Out o{M, N, bias, bias_f32, deriv, residual, ldr, nullptr, y, 0, nullptr};
   float* part = static_cast<float*>(ws);
   cudaStream_t st = dmoe::as_stream(stream);
   if (turned) {
-    ParamsF<false> p{};
-    place_turned(p.t[0], o, K, cut.rows, true, false);
-    if (!map_pitched(&p.t[0].map_a, w, K, N, N, 64, BK) || !map_pitched(&p.t[0].map_b, x, M, K, ldx, BK, p.t[0].box))
-      return DMOE_ERR_CUDA;
-    if (act == DMOE_ACT_GELU) return run_turned<DMOE_ACT_GELU, false>(p, cut, di, st);
-    if (act == DMOE_ACT_SILU) return run_turned<DMOE_ACT_SILU, false>(p, cut, di, st);
-    return run_turned<DMOE_ACT_NONE, false>(p, cut, di, st);
+    if (act == DMOE_ACT_GELU) return run_turned<DMOE_ACT_GELU>(x, ldx, w, K, o, cut, di, st);
+    if (act == DMOE_ACT_SILU) return run_turned<DMOE_ACT_SILU>(x, ldx, w, K, o, cut, di, st);
+    return run_turned<DMOE_ACT_NONE>(x, ldx, w, K, o, cut, di, st);
   }
   ParamsL p{};
   if (!map_pitched(&p.map_a[0], x, M, K, ldx, BK, box_rows(M)) || !map_pitched(&p.map_b[0], w, K, N, N, 64, BK))
@@ -1381,43 +1305,25 @@ DMOE_API dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, cons
   }
   if (products) {
     Want a{dx ? M : 0, K, ceil_div(N, BK), false}, b{dw ? K : 0, N, ceil_div(M, BK), false};
-    const int64_t ns = dx ? choose(a, b) : choose(b, a);
-    const Out ox{dx ? M : 0, K, nullptr, 0, nullptr, nullptr, 0, factor, dx, 0, nullptr};
-    const Out ow{dw ? K : 0, N, nullptr, 0, nullptr, nullptr, 0, nullptr, dw, dw_f32 ? 1 : 0, nullptr};
-    const TurnedSize tx{ox.rows, K, N}, tw{ow.rows, N, M};
-    const TurnedCut cut = cut_turned(tx, tw, di);
-    if (cut.ns < ns) {
-      ParamsF<true> p{};
-      int n_turned = 0;
-      if (dx) {
-        Turned& t = p.t[n_turned++];
-        place_turned(t, ox, N, cut.rows, false, false);
-        if (!map_pitched(&t.map_a, w, K, N, N, BK, kFewTile) || !map_pitched(&t.map_b, dz, M, N, lddz, BK, t.box))
-          return DMOE_ERR_CUDA;
-      }
-      if (dw) {
-        Turned& t = p.t[n_turned++];
-        place_turned(t, ow, M, kTurnedRows, true, true);
-        if (!map_pitched(&t.map_a, dz, M, N, lddz, 64, BK) || !map_pitched(&t.map_b, x, M, K, ldx, 64, BK))
-          return DMOE_ERR_CUDA;
-      }
-      s = run_turned<DMOE_ACT_NONE, true>(p, cut, di, st);
+    if (dx) {
+      choose(a, b);
     } else {
-      ParamsL p{};
-      const int half = std::min(a.tile, BN) / 2;  // of a sub-tile's columns, each CTA's
-      if (dx && (!map_pitched(&p.map_a[0], dz, M, N, lddz, BK, box_rows(M)) || !map_pitched(&p.map_b[0], w, K, N, N, BK, half)))
-        return DMOE_ERR_CUDA;
-      if (dw && (!map_pitched(&p.map_a[1], x, M, K, ldx, 64, BK) || !map_pitched(&p.map_b[1], dz, M, N, lddz, 64, BK)))
-        return DMOE_ERR_CUDA;
-      if (!dx) p.map_a[0] = p.map_a[1], p.map_b[0] = p.map_b[1];
-      if (!dw) p.map_a[1] = p.map_a[0], p.map_b[1] = p.map_b[0];
-      p.a_rows = box_rows(M);
-      if (dx) p.o[0] = ox;
-      if (dw) p.o[1] = ow;
-      p.err = di.err_word;
-      s = run_products<DMOE_ACT_NONE>(p, a, b, reinterpret_cast<float*>(base + l.part_x),
-                                      reinterpret_cast<float*>(base + l.part_w), di, st);
+      choose(b, a);
     }
+    ParamsL p{};
+    const int half = std::min(a.tile, BN) / 2;  // of a sub-tile's columns, each CTA's
+    if (dx && (!map_pitched(&p.map_a[0], dz, M, N, lddz, BK, box_rows(M)) || !map_pitched(&p.map_b[0], w, K, N, N, BK, half)))
+      return DMOE_ERR_CUDA;
+    if (dw && (!map_pitched(&p.map_a[1], x, M, K, ldx, 64, BK) || !map_pitched(&p.map_b[1], dz, M, N, lddz, 64, BK)))
+      return DMOE_ERR_CUDA;
+    if (!dx) p.map_a[0] = p.map_a[1], p.map_b[0] = p.map_b[1];
+    if (!dw) p.map_a[1] = p.map_a[0], p.map_b[1] = p.map_b[0];
+    p.a_rows = box_rows(M);
+    if (dx) p.o[0] = Out{M, K, nullptr, 0, nullptr, nullptr, 0, factor, dx, 0, nullptr};
+    if (dw) p.o[1] = Out{K, N, nullptr, 0, nullptr, nullptr, 0, nullptr, dw, dw_f32 ? 1 : 0, nullptr};
+    p.err = di.err_word;
+    s = run_products<DMOE_ACT_NONE>(p, a, b, reinterpret_cast<float*>(base + l.part_x),
+                                    reinterpret_cast<float*>(base + l.part_w), di, st);
     if (s != DMOE_OK) return s;
   }
   if (dbias && !joined) {
