@@ -1183,8 +1183,14 @@ bool off16(const void* a) { return !dmoe::aligned16(a); }
 int box_rows(int rows) { return std::min(rows, BM); }
 
 // Stripes of rows, a cluster, of a dz_kernel that joins its sums itself: up to
-// 128 rows each (0: more rows, whose sums a launch of their own joins).
-int joined_stripes(int M) { return M > 1024 ? 0 : M > 256 ? 8 : M > 128 ? 4 : M > 64 ? 2 : 1; }
+// 128 rows each (0: more rows, or more than some four blocks an SM, whose sums a
+// launch of their own joins).  Us of a backward, joined and not: 400 x 264 x 264
+// 9.7 and 11.7, 400 x 264 x 4096 (512 blocks) 19.7 and 21.4, 400 x 264 x 8192 27.9
+// and 25.0, 2048 x 1024 x 1024 24.8 and 22.5.
+int joined_stripes(int M, int N) {
+  const int n = M > 256 ? 8 : M > 128 ? 4 : M > 64 ? 2 : 1;
+  return M > 1024 || n * ceil_div(N, 64) > 4 * 2 * kUnits ? 0 : n;
+}
 
 // Stripes of rows whose sums dz_kernel leaves: some four blocks an SM.
 int stripes(int M, int N) {
@@ -1290,7 +1296,7 @@ DMOE_API dmoe_status dmoe_linear_backward(const uint16_t* dy, int64_t lddy, cons
   uint8_t* base = static_cast<uint8_t*>(ws);
   const uint16_t* dz = dy;
   int64_t lddz = lddy;
-  const int joined = joined_stripes(M), n = joined ? joined : stripes(M, N);
+  const int joined = joined_stripes(M, N), n = joined ? joined : stripes(M, N);
   const bool products = dx || dw;
   if ((deriv && products) || dbias) {
     uint16_t* out = deriv && products ? reinterpret_cast<uint16_t*>(base + l.dz) : nullptr;

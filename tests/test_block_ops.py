@@ -610,11 +610,10 @@ def test_linear_backward(dm, M, K, N, kept, f32):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,K,N", [(8, 264, 4104), (64, 512, 2048), (64, 2048, 136), (129, 136, 4096), (300, 1000, 1000),
-                                   (200, 64, 64), (512, 2048, 512), (1023, 72, 520)])
+                                   (200, 64, 64), (512, 2048, 512), (1023, 72, 520), (260, 72, 8200)])
 @pytest.mark.parametrize("kept,f32", [(False, True), (True, False)])
 def test_linear_backward_of_small_products(dm, M, K, N, kept, f32):
-    """One of the two sums much shorter than the other, so that it leaves parts of a tile empty; blocks of
-    rows and of columns that are not whole."""
+    """One of the two sums much shorter than the other, and blocks of rows and of columns that are not whole."""
     test_linear_backward(dm, M, K, N, kept, f32)
 
 
