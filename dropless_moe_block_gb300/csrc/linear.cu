@@ -905,7 +905,7 @@ constexpr int kMinSlices = 4;  // of a part
 // What the items' times leave out: launch and first loads, and the last
 // epilogue (with an activation more).  Single tiles of 264 columns of K, none
 // and gelu: 7.0 and 9.1 us.
-constexpr int64_t kTilesNs = 5000, kTurnedNs = 4000;
+constexpr int64_t kTilesNs = 5000, kTurnedNs = 2500;
 int64_t last_epilogue_ns(bool act) { return act ? 2700 : 1000; }
 
 // Nanoseconds of an item: `busy` pairs at work, each with this many K slices
@@ -1092,26 +1092,30 @@ int resident_clusters(int parts, const dmoe::DeviceInfo& di) {
 }
 
 // The parts of a turned product (a cluster's CTAs: 1, 2, 4 or 8, as many as are
-// resident together), and its nanoseconds.  A slice takes a CTA 0.27 us, or its
-// share of HBM's 6.5 TB/s; the epilogue, four pairs of columns a thread in 1 us,
-// or of a whole tile 32 rows in 0.8.
+// resident together), and its nanoseconds.  A slice takes a CTA 0.27 us (0.30
+// where K is whole), or its share of HBM's 6.5 TB/s; the epilogue, four pairs of
+// columns a thread in 1 us behind the cluster's meeting, or of a whole tile 32
+// rows in 0.2, 0.9 with an activation.  Of 132 sizes from 4 x 256 x 264 to 6000 x
+// 4096 x 4096, which was quicker, this or pairs, is met but for 1% of the time
+// with an activation and 0.4% without.
 struct TurnedCut {
   int rows, parts;
   int64_t ns;
 };
-TurnedCut cut_turned(int M, int K, int N, const dmoe::DeviceInfo& di) {
+TurnedCut cut_turned(int M, int K, int N, bool act, const dmoe::DeviceInfo& di) {
   const int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : kTurnedRows;
   const int cols = ceil_div(N, kFewTile), blocks = ceil_div(M, rows), slices = ceil_div(K, BK);
   const int64_t tiles = static_cast<int64_t>(cols) * blocks;
   int parts = 8;
   while (parts > 1 && (slices < 2 * parts || tiles > resident_clusters(parts, di))) parts /= 2;
   const int64_t busy = std::min<int64_t>(tiles * parts, 2 * kUnits);
-  const int64_t slice = std::max<int64_t>(270, static_cast<int64_t>(2 * ATOM) * busy / std::min<int64_t>(blocks, busy) / 6500);
+  const int64_t bytes = static_cast<int64_t>(2 * ATOM) * busy / std::min<int64_t>(blocks, busy);
+  const int64_t slice = std::max<int64_t>(parts > 1 ? 270 : 300, bytes / 6500);
   const int64_t live = std::min(M, rows);
-  const int64_t epilogue =
-      parts > 1 ? ceil_div(live * (kFewTile / 2 / parts), 4 * kFewThreads) * 1000 : ceil_div(live, 4 * kFewEpiWarps) * 800;
+  const int64_t epilogue = parts > 1 ? 1500 + ceil_div(live * (kFewTile / 2 / parts), 4 * kFewThreads) * 1000 + 10 * live
+                                     : ceil_div(live, 4 * kFewEpiWarps) * (act ? 875 : 225);
   const int64_t waves = (tiles * parts + 2 * kUnits - 1) / (2 * kUnits);
-  return TurnedCut{rows, parts, waves * (ceil_div(slices, parts) * slice + epilogue) + 10 * live + kTurnedNs};
+  return TurnedCut{rows, parts, waves * (ceil_div(slices, parts) * slice + epilogue) + kTurnedNs};
 }
 
 template <int ACT, int ROWS>
@@ -1239,7 +1243,7 @@ DMOE_API dmoe_status dmoe_linear(const uint16_t* x, int64_t ldx, const uint16_t*
   if (s != DMOE_OK) return s;
   Want a{M, N, ceil_div(K, BK), act != DMOE_ACT_NONE}, none{};
   const int64_t ns = choose(a, none);
-  const TurnedCut cut = cut_turned(M, K, N, di);
+  const TurnedCut cut = cut_turned(M, K, N, act != DMOE_ACT_NONE, di);
   const bool turned = cut.ns < ns;
   if (!turned && a.parts > 1 && (!ws || ws_bytes < part_bytes(M, N))) return DMOE_ERR_INVALID_ARG;
   const Out o{M, N, bias, bias_f32, deriv, residual, ldr, nullptr, y, 0, nullptr};

@@ -577,6 +577,13 @@ def test_linear(dm, M, K, N, act, bias, residual):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(200, 264, 8192), (600, 512, 2048), (1000, 520, 2056), (2000, 512, 2048), (5999, 72, 520)])
+@pytest.mark.parametrize("act,bias,residual", [("none", BF, True), ("gelu", F32, True)])
+def test_linear_of_many_small_tiles(dm, M, K, N, act, bias, residual):
+    check_linear(dm, M, K, N, act, bias, residual)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,K,N", LINEAR)
 @pytest.mark.parametrize("kept,f32", [(False, False), (True, True)])
 def test_linear_backward(dm, M, K, N, kept, f32):
