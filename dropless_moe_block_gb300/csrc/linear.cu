@@ -411,20 +411,11 @@ __global__ void __launch_bounds__(kThreadsL, 1) linear_kernel(const __grid_const
             if (o.deriv)
               write_rows32(slab, lane, g, o.deriv + static_cast<int64_t>(row0) * o.cols + ch, o.cols, rows, cols);
           }
+          // y may be residual and dx factor: each value is read by the warp that
+          // overwrites it, before
           if (o.residual && row < o.rows)
-            add_row32(v, o.residual + static_cast<int64_t>(row) * o.ld_res + ch, 1.f, cols);
-          if (o.factor && row < o.rows) {
-            const uint4* a = reinterpret_cast<const uint4*>(o.factor + static_cast<int64_t>(row) * o.cols + ch);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (8 * q < cols) {
-                float f[8];
-                unpack8x(__ldg(a + q), f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[8 * q + i] *= f[i];
-              }
-            }
-          }
+            join_row32<false>(v, o.residual + static_cast<int64_t>(row) * o.ld_res + ch, cols);
+          if (o.factor && row < o.rows) join_row32<true>(v, o.factor + static_cast<int64_t>(row) * o.cols + ch, cols);
           const int64_t at = static_cast<int64_t>(row0) * o.cols + ch;
           if (o.f32) write_rows32(slab, lane, v, static_cast<float*>(o.out) + at, o.cols, rows, cols);
           else write_rows32(slab, lane, v, static_cast<uint16_t*>(o.out) + at, o.cols, rows, cols);

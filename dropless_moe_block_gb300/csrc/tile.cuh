@@ -146,7 +146,36 @@ __device__ __forceinline__ void write_rows32(uint32_t slab, int lane, const floa
   __syncwarp();
 }
 
-// v[0..31] += k * 32 bf16 values of a row of which `cols` exist.
+// A plain load, of memory that the kernel itself may write (which __ldg may not
+// read), but one that the compiler may move: held where they stand, the loads
+// of join_row32 wait behind the accumulator's and the last stores (8192 x 512 x
+// 2048 onto a residual 54 us, 26 with these).  So it is for values that the
+// reader alone overwrites, by stores that hang on what it read.
+__device__ __forceinline__ uint4 ld_own(const uint4* a) {
+  uint4 q;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+      : "l"(reinterpret_cast<uint64_t>(a)));
+  return q;
+}
+
+// 32 bf16 values of a row of which `cols` exist, added to v[0..31] or multiplied
+// into them; the row may be the one the caller overwrites.
+template <bool MUL>
+__device__ __forceinline__ void join_row32(float* v, const uint16_t* a, int cols) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (8 * j < cols) {
+      float f[8];
+      unpack8x(ld_own(reinterpret_cast<const uint4*>(a) + j), f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[8 * j + q] = MUL ? v[8 * j + q] * f[q] : v[8 * j + q] + f[q];
+    }
+  }
+}
+
+// v[0..31] += k * 32 bf16 values of a row of which `cols` exist (which nothing
+// writes meanwhile).
 __device__ __forceinline__ void add_row32(float* v, const uint16_t* a, float k, int cols) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

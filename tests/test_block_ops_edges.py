@@ -1,0 +1,87 @@
+"""The block's operators where test_block_ops.py does not take them: outputs that lie over what their call reads, and the edges
+of what the operators allow.
+
+Sums of products are made exact, where that helps: whole numbers times a power of two, whose sums fp32 holds however they are
+ordered or cut, so that what follows them is compared without a sum's error.
+"""
+
+import pytest
+import torch
+
+from test_block_ops import BF, F32, U16, U32, close, dm, empty, ref_act, workspace  # noqa: F401
+
+
+def whole(seed, *shape, most=2, unit=1.0, dtype=BF):
+    """Whole numbers from -most to most, times unit (a power of two)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randint(-most, most + 1, shape, generator=g, device="cuda").double() * unit).to(dtype)
+
+
+def launches(dm, f):
+    n = dm.launch_count()
+    f()
+    return dm.launch_count() - n
+
+
+# --------------------------------------------------------------- dense linear
+
+# Forward products of whole sums in pairs of CTAs: tiles 256 and 512 columns wide.
+WHOLE = [(2560, 512, 4096), (1031, 1000, 5128), (2100, 2048, 2056)]
+
+
+def exact_case(M, K, N, act, bias, residual):
+    x, w = whole(1, M, K), whole(2, K, N, unit=2.0 ** -6)
+    b = None if bias is None else whole(3, N, unit=0.25, dtype=bias)
+    r = whole(4, M, N, most=9, unit=0.125) if residual else None
+    z = x.double() @ w.double()  # exact: |z| 2^6 < 4 K < 2^24
+    if b is not None:
+        z = z + b.double()
+    return x, w, b, r, z
+
+
+def check_exact(got, z, act, r, what, deriv=None):
+    y, f = ref_act(z, act)
+    if r is not None:
+        y = y + r.double()
+    if act == "none":
+        assert torch.equal(got, y.to(F32).to(BF)), what  # (y is exact in fp32: one rounding)
+        return
+    # Phi is known to 1.5e-7, sigmoid to a few ulp, and what is added rounds once more
+    ea = 4e-7 * (1 + z.abs())
+    close(got, y, U16 * y.abs() + ea + 4 * U32 * (y.abs() + 4), what)
+    if deriv is not None:
+        close(deriv, f, U16 * f.abs() + ea, what + ": deriv")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", WHOLE)
+@pytest.mark.parametrize("act,bias", [("none", BF), ("gelu", F32), ("silu", None)])
+def test_linear_of_pairs_onto_its_residual(dm, M, K, N, act, bias):
+    """y over the residual, which the same tiles read: the result of the call that keeps them apart."""
+    x, w, b, r, z = exact_case(M, K, N, act, bias, True)
+    y = empty(M, N)
+    ws, _ = workspace(dm.linear_workspace_size(M, K, N))
+    assert launches(dm, lambda: dm.linear(x, w, y, ws, bias=b, act=act, residual=r)) == 1
+    check_exact(y, z, act, r, "y")
+    for _ in range(3):  # not once by chance
+        onto = r.clone()
+        dm.linear(x, w, onto, ws, bias=b, act=act, residual=onto)
+        assert torch.equal(onto, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(2560, 4096, 512), (1031, 5128, 1000), (130, 1032, 12296), (1, 8, 26960), (2051, 264, 8200)])
+def test_linear_backward_onto_its_factor(dm, M, K, N):
+    """dx over factor, in whole tiles and behind sums that were cut."""
+    dy, w, f = whole(1, M, N), whole(2, K, N, unit=2.0 ** -6), whole(3, M, K, most=9, unit=0.125)
+    ws, guard = workspace(dm.linear_backward_workspace_size(M, K, N))
+    want = ((dy.double() @ w.double().t()) * f.double()).to(F32).to(BF)  # below 2^24 units of 2^-9: exact before its rounding
+    dx = empty(M, K)
+    dm.linear_backward(dy, None, w, dx, None, ws, factor=f)
+    assert torch.equal(dx, want)
+    for _ in range(3):
+        onto = f.clone()
+        dm.linear_backward(dy, None, w, onto, None, ws, factor=onto)
+        assert torch.equal(onto, want)
+    assert bool((guard == 0x5a).all())
