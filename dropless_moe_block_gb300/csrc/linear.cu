@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const uint16_t* __restrict__ dy
                                                  const uint16_t* __restrict__ deriv, int M, int N,
                                                  uint16_t* __restrict__ dz, float* __restrict__ sums) {
   constexpr int COLS = JOINED ? 64 : 256, ROWS = 2048 / COLS;  // of a block at a time
-  __shared__ float sh[ROWS][COLS + 4];
+  __shared__ __align__(16) float sh[ROWS][COLS + 4];  // filled four columns at a time
   __shared__ float total[COLS];
   dmoe::pdl_wait();
   dmoe::pdl_launch_dependents();
