@@ -1,5 +1,5 @@
-"""The block's operators where test_block_ops.py does not take them: outputs that lie over what their call reads, and the edges
-of what the operators allow.
+"""The block's operators where test_block_ops.py does not take them: products cut along K with all that
+follows the sums, outputs that lie over what their call reads, and the edges of what the operators allow.
 
 Sums of products are made exact, where that helps: whole numbers times a power of two, whose sums fp32 holds however they are
 ordered or cut, so that what follows them is compared without a sum's error.
@@ -26,8 +26,10 @@ def launches(dm, f):
 
 # --------------------------------------------------------------- dense linear
 
+# Forward products that a pair of CTAs sums in parts, one part a range of K, and a second launch joins.
+CUT = [(1, 26960, 8), (7, 16392, 72), (130, 12296, 1032), (509, 15168, 1208), (2051, 8200, 264), (4300, 8200, 264)]
 # Forward products of whole sums in pairs of CTAs: tiles 256 and 512 columns wide.
-WHOLE = [(2560, 512, 4096), (1031, 1000, 5128), (2100, 2048, 2056)]
+WHOLE = [(2560, 512, 4096), (1031, 1000, 5128), (2303, 6152, 4096)]
 
 
 def exact_case(M, K, N, act, bias, residual):
@@ -52,6 +54,49 @@ def check_exact(got, z, act, r, what, deriv=None):
     close(got, y, U16 * y.abs() + ea + 4 * U32 * (y.abs() + 4), what)
     if deriv is not None:
         close(deriv, f, U16 * f.abs() + ea, what + ": deriv")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", CUT)
+@pytest.mark.parametrize("act,bias,residual", [("none", None, False), ("none", BF, True), ("gelu", F32, True),
+                                               ("silu", BF, False), ("silu", F32, True)])
+def test_linear_cut_along_its_sum(dm, M, K, N, act, bias, residual):
+    x, w, b, r, z = exact_case(M, K, N, act, bias, residual)
+    y, f = empty(M, N), None if act == "none" else empty(M, N)
+    ws, guard = workspace(dm.linear_workspace_size(M, K, N))
+    # a later rule of the cuts that takes these sizes elsewhere has to name others here
+    assert launches(dm, lambda: dm.linear(x, w, y, ws, bias=b, act=act, deriv=f, residual=r)) == 2
+    check_exact(y, z, act, r, "y", f)
+    assert bool((guard == 0x5a).all())
+    if r is not None:  # onto the residual, and rows of wider tensors
+        kept = r.clone()
+        dm.linear(x, w, r, ws, bias=b, act=act, residual=r)
+        assert torch.equal(r, y)
+        wide = empty(M, K + N + 16)
+        wide[:, 8:8 + K], wide[:, 16 + K:] = x, kept
+        y.fill_(777.0)
+        dm.linear(wide[:, 8:8 + K], w, y, ws, bias=b, act=act, residual=wide[:, 16 + K:])
+        assert torch.equal(r, y)
+
+
+@pytest.mark.gpu
+def test_linear_workspace_of_cut_products_serves_fewer_rows(dm):
+    K, N = 15168, 1208
+    n = dm.linear_workspace_size(509, K, N)
+    ws, guard = workspace(n)
+    w = whole(2, K, N, unit=2.0 ** -6)
+    cut = 0
+    for M in (509, 400, 300, 257, 200, 130, 65, 3):
+        assert dm.linear_workspace_size(M, K, N) <= n
+        x, y = whole(M, M, K), empty(M, N)
+        cut += launches(dm, lambda: dm.linear(x, w, y, ws)) == 2
+        assert torch.equal(y, (x.double() @ w.double()).to(F32).to(BF)), M
+    assert cut >= 3
+    assert bool((guard == 0x5a).all())
+    with pytest.raises(dm.DmoeError):  # too small for the parts' sums, which are not written then
+        x, y = whole(1, 509, K), empty(509, N)
+        dm.linear(x, w, y, ws[:1 << 16])
+    assert bool((y == 777.0).all())
 
 
 @pytest.mark.gpu
