@@ -552,14 +552,13 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_eighths_kernel(const __g
       const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        most = fmaxf(most, fabsf(bb[r]));
+        most = fmaxf(most, fabsf(bb[r]) < INFINITY ? fabsf(bb[r]) : 0.f);  // (an infinite one's place is the range's end)
         const float z = s[i][r];
         const float v = sig ? rcp_approx(1.f + ex2_approx(z * -kLog2e)) : ex2_approx((z - m) * kLog2e) * inv;
         s[i][r] = z == -INFINITY ? -INFINITY : fmaxf(v + bb[r], -INFINITY);  // the choice; NaN is minus infinity
       }
     }
     most = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
-    near = most == INFINITY;  // experts that a bias rules out, or forces
     const float range = most + inv;
     open = (sig ? 5.f : 12.f) * 4.7683716e-7f * range;
     quarter = 0.24999f / range;  // all numbers' places lie above 1

@@ -5,10 +5,13 @@ Sums of products are made exact, where that helps: whole numbers times a power o
 ordered or cut, so that what follows them is compared without a sum's error.
 """
 
+import math
+
 import pytest
 import torch
 
-from test_block_ops import BF, F32, U16, U32, close, dm, empty, ref_act, workspace  # noqa: F401
+from test_block_ops import (BF, F32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_scores,  # noqa: F401
+                            route, workspace)
 
 
 def whole(seed, *shape, most=2, unit=1.0, dtype=BF):
@@ -130,3 +133,27 @@ def test_linear_backward_onto_its_factor(dm, M, K, N):
         dm.linear_backward(dy, None, w, onto, None, ws, factor=onto)
         assert torch.equal(onto, want)
     assert bool((guard == 0x5a).all())
+
+
+# -------------------------------------------------------------------- routing
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [(8300, 64, 4, 1, 1), (8193, 64, 8, 2, 1), (8200, 128, 3, 4, 2), (8195, 256, 8, 8, 4),
+                                                     (8192, 256, 8, 1, 1), (50, 64, 1, 1, 1), (70, 256, 1, 8, 2), (3000, 96, 5, 4, 2)])
+def test_route_with_experts_ruled_out_and_forced(dm, T, E, k, groups, top_groups, scores):
+    """A bias of minus infinity or NaN rules an expert out, one of plus infinity forces it: alone, together, and where they leave fewer
+    experts than are chosen."""
+    size = E // groups
+    logits = randn(1, T, E, dtype=F32)
+    logits[3::50, size - 1:] = -math.inf  # few experts left
+    logits[7::60] = -math.inf             # none
+    for out, forced in (([2], []), ([0, 1, E - 1], []), ([5], [3]), ([], [1, E - 2]), (list(range(4, E)), [0])):
+        bias = randn(2, E, scale=0.02, dtype=F32)
+        bias[out] = -math.inf
+        bias[out[1:2]] = math.nan
+        bias[forced] = math.inf
+        idx, w = route(dm, logits, k, bias=bias, scores=scores, groups=groups, top_groups=top_groups)
+        ri, rw = ref_route(logits, bias, k, scores, groups, top_groups, True, 1.0)
+        assert torch.equal(idx.long(), ri), (out, forced)
+        close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
