@@ -110,7 +110,14 @@ __device__ __forceinline__ void top_two(F a, F& first, F& second) {
   first = upper(first, a);
 }
 
-// Of the lanes that share a group, `lanes` neighbours (a power of two).
+// Half a group's worth, which passes no type's end where its two terms do not.
+template <class F>
+__device__ __forceinline__ F half_worth(F first, F second) {
+  const F half = static_cast<F>(0.5);
+  return second == -INFINITY ? half * first : half * first + half * second;
+}
+
+// That of the lanes that share a group, `lanes` neighbours (a power of two).
 template <class F>
 __device__ __forceinline__ F group_worth(F first, F second, int lanes) {
   for (int o = 1; o < lanes; o <<= 1) {
@@ -118,7 +125,7 @@ __device__ __forceinline__ F group_worth(F first, F second, int lanes) {
     top_two(f, first, second);
     top_two(s, first, second);
   }
-  return second == -INFINITY ? first : first + second;
+  return half_worth(first, second);
 }
 
 // How many of the groups (one every `lanes` lanes, a power of two) are better
@@ -324,8 +331,8 @@ __device__ __forceinline__ void route_by_warp(const Choice& p, int64_t t, const 
     // the worst that stays against the best that goes
     const float low = float_of(__reduce_min_sync(kFull, stays ? key_of(worth) : kFull));
     const float high = float_of(__reduce_max_sync(kFull, g < p.groups && !stays ? key_of(worth) : 0u));
-    const float open = open_steps * step;  // as far as two choices may be off
-    if (low - high <= 2.f * open && !rows_alike()) {
+    const float open = open_steps * step;  // as far as two choices may be off, and two halves of two choices
+    if (low - high <= open && !rows_alike()) {
       // the groups' two best in 64 bits: of those that may be among them
       need_total();
       const float least = second - open;
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_eighths_kernel(const __g
         g[0] = fmaxf(fminf(f1, f2), fmaxf(g[0], g2));
       }
     }
-    const float worth = g[0] == -INFINITY ? f[0] : f[0] + g[0];
+    const float worth = half_worth(f[0], g[0]);
     const int mine = q / (8 / G);
     int rank = 0;
 #pragma unroll
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_eighths_kernel(const __g
     }
     const bool stays = rank < p.top_groups;
     const float low = -max8(stays ? -worth : -INFINITY), high = max8(stays ? -INFINITY : worth);
-    near |= low - high <= 2.f * open;
+    near |= low - high <= open;
     in = __ballot_sync(kFull, stays) >> (lane & 24);
   }
   uint32_t key[NI][4];

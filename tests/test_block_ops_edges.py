@@ -157,3 +157,19 @@ def test_route_with_experts_ruled_out_and_forced(dm, T, E, k, groups, top_groups
         ri, rw = ref_route(logits, bias, k, scores, groups, top_groups, True, 1.0)
         assert torch.equal(idx.long(), ri), (out, forced)
         close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups", [(5, 8, 1, 4), (300, 96, 3, 4), (40, 64, 1, 2), (9000, 256, 8, 8), (9000, 64, 8, 2)])
+def test_route_by_groups_whose_worth_passes_fp32(dm, T, E, k, groups, scores):
+    """Two biases near fp32's end: their sums are infinite in fp32, and different in 64 bits."""
+    size = E // groups
+    logits = randn(1, T, E, dtype=F32)
+    for sums in ((2e38, 3e38), (3e38, 2e38), (-2e38, -1.9e38), (-3e38, 3e38)):
+        bias = torch.full((E,), sums[0], device="cuda")
+        bias[size:2 * size] = sums[1]
+        idx, w = route(dm, logits, k, bias=bias, scores=scores, groups=groups, top_groups=1)
+        ri, rw = ref_route(logits, bias, k, scores, groups, 1, True, 1.0)
+        assert torch.equal(idx.long(), ri), sums
+        close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
