@@ -888,7 +888,7 @@ def sandwich_norm_backward(dy, u, h, w_post, w_pre, rstd_u, rstd_h, du, dresidua
             raise ValueError("d_gate needs a gate")
         _is(d_gate, dev, f32, "d_gate", (n,))
     nws = 0
-    if dw_post is not None or dw_pre is not None or (d_gate is not None and n == 1):
+    if dw_post is not None or dw_pre is not None or (d_gate is not None and n != T):
         nws = _workspace(ws, dev)
     dyp, up, hp, dhp, dup, dxp = dy.data_ptr(), u.data_ptr(), h.data_ptr(), _ptr(dh), du.data_ptr(), dresidual.data_ptr()
     nb = 2 * T * d

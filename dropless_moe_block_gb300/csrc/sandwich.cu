@@ -589,17 +589,17 @@ DMOE_API dmoe_status dmoe_sandwich_norm_backward(const uint16_t* dy, int64_t ldd
   dmoe_status s = dmoe::device_info(&di);
   if (s != DMOE_OK) return s;
   cudaStream_t st = dmoe::as_stream(stream);
-  const bool shared = d_gate && gate_rows == 1;  // one gate for all rows: its gradient is their sum
   if (T == 0) {  // no rows: the sums over them are zero
     cudaError_t e = cudaSuccess;
     if (dw_post) e = cudaMemsetAsync(dw_post, 0, static_cast<size_t>(d) * sizeof(float), st);
     if (e == cudaSuccess && dw_pre) e = cudaMemsetAsync(dw_pre, 0, static_cast<size_t>(d) * sizeof(float), st);
-    if (e == cudaSuccess && shared) e = cudaMemsetAsync(d_gate, 0, sizeof(float), st);
+    if (e == cudaSuccess && d_gate && gate_rows == 1) e = cudaMemsetAsync(d_gate, 0, sizeof(float), st);
     return dmoe::cuda_status(e);
   }
   const int blocks = backward_blocks(T, di.sm_count);
   const size_t part = static_cast<size_t>(blocks) * 2 * d;
   const bool sums = dw_post || dw_pre;
+  const bool shared = d_gate && gate_rows != T;  // one gate for all rows: its gradient is their sum
   if ((sums || shared) && (!ws || ws_bytes < (part + T) * sizeof(float))) return DMOE_ERR_INVALID_ARG;
   float* row_gate = static_cast<float*>(ws) + part;
   Back p{dy, u, h, dh, lddy, ldu, lddh, w_post, w_pre, rstd_u, rstd_h, gate, gate_rows == 1 ? 0 : 1, scale, T, d,

@@ -10,8 +10,8 @@ import math
 import pytest
 import torch
 
-from test_block_ops import (BF, F32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_scores,  # noqa: F401
-                            route, workspace)
+from test_block_ops import (BF, F32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_sandwich_backward,  # noqa: F401
+                            ref_scores, check_backward, route, weights, workspace)
 
 
 def whole(seed, *shape, most=2, unit=1.0, dtype=BF):
@@ -173,3 +173,21 @@ def test_route_by_groups_whose_worth_passes_fp32(dm, T, E, k, groups, scores):
         ri, rw = ref_route(logits, bias, k, scores, groups, 1, True, 1.0)
         assert torch.equal(idx.long(), ri), sums
         close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
+
+
+# ----------------------------------------------------- norms around the block
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 2])
+def test_gradient_of_a_gate_a_row_needs_no_workspace(dm, T):
+    """One row's gate is a gate of T rows, too: its gradient is written by the row, with no sums to bring together."""
+    d = 264
+    dy, u, h = randn(1, T, d), randn(2, T, d), randn(3, T, d, scale=3.0)
+    a, b = weights(False, d)
+    gate = torch.sigmoid(randn(9, T, dtype=F32))
+    ru = torch.rsqrt(u.float().square().mean(1) + 1e-5)
+    rh = torch.rsqrt(h.float().square().mean(1) + 1e-5)
+    got = {"du": empty(T, d), "dx": empty(T, d), "gate": empty(T, dtype=F32)}
+    dm.sandwich_norm_backward(dy, u, h, a, b, ru, rh, got["du"], got["dx"], None, None, None, gate=gate, d_gate=got["gate"])
+    ref, size = ref_sandwich_backward(dy, u, h, a, b, ru, rh, None, gate, 1.0)
+    check_backward(got, ref, size, T)
