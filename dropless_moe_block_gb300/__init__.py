@@ -765,9 +765,12 @@ def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = 
         _is(bias, dev, torch.float32, "bias", (E,))
     _is(expert_idx, dev, torch.int32, "expert_idx", (T, k))
     _is(gate_w, dev, torch.float32, "gate_w", (T, k))
+    lp, wp = logits.data_ptr(), gate_w.data_ptr()
+    if wp < lp + 4 * T * E and lp < wp + 4 * T * k:
+        raise ValueError("gate_w must not overlap logits")
     _check("dmoe_route_balanced", lib().dmoe_route_balanced(
-        logits.data_ptr(), _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
-        int(bool(renormalize)), scale, expert_idx.data_ptr(), gate_w.data_ptr(), _stream_on(stream, dev)))
+        lp, _ptr(bias), T, E, k, _name(_SCORES, scores, "scores"), groups, top_groups,
+        int(bool(renormalize)), scale, expert_idx.data_ptr(), wp, _stream_on(stream, dev)))
 
 
 def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = "softmax", renormalize: bool = True,
@@ -781,10 +784,10 @@ def route_balanced_backward(logits, expert_idx, d_gate, d_logits, scores: str = 
     _is(expert_idx, dev, torch.int32, "expert_idx", (T, k))
     _is(d_gate, dev, torch.float32, "d_gate", (T, k))
     _is(d_logits, dev, torch.float32, "d_logits", (T, E))
-    lp, op, n = logits.data_ptr(), d_logits.data_ptr(), 4 * T * E
-    _apart_from(op, n, "d_logits", (lp, n, "logits"))
+    lp, gp, op, n = logits.data_ptr(), d_gate.data_ptr(), d_logits.data_ptr(), 4 * T * E
+    _apart_from(op, n, "d_logits", (lp, n, "logits"), (gp, 4 * T * k, "d_gate"))
     _check("dmoe_route_balanced_backward", lib().dmoe_route_balanced_backward(
-        lp, expert_idx.data_ptr(), d_gate.data_ptr(), T, E, k, _name(_SCORES, scores, "scores"), int(bool(renormalize)),
+        lp, expert_idx.data_ptr(), gp, T, E, k, _name(_SCORES, scores, "scores"), int(bool(renormalize)),
         scale, op, _stream_on(stream, dev)))
 
 

@@ -867,7 +867,7 @@ DMOE_API dmoe_status dmoe_route_balanced(const float* logits, const float* bias,
       top_groups < 1 || top_groups > groups || k > top_groups * (E / groups) || !isfinite(scale))
     return DMOE_ERR_INVALID_ARG;
   if (T == 0) return DMOE_OK;
-  if (!logits || !expert_idx || !gate_w) return DMOE_ERR_INVALID_ARG;
+  if (!logits || !expert_idx || !gate_w || gate_w == logits) return DMOE_ERR_INVALID_ARG;
   if (misaligned4(logits) || misaligned4(bias) || misaligned4(expert_idx) || misaligned4(gate_w))
     return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;
@@ -893,7 +893,7 @@ DMOE_API dmoe_status dmoe_route_balanced_backward(const float* logits, const int
                                                   float* d_logits, dmoe_stream_t stream) {
   if (T < 0 || E < 1 || E > 1024 || k < 1 || k > E || bad_scores(scores) || !isfinite(scale)) return DMOE_ERR_INVALID_ARG;
   if (T == 0) return DMOE_OK;
-  if (!logits || !expert_idx || !d_gate || !d_logits) return DMOE_ERR_INVALID_ARG;
+  if (!logits || !expert_idx || !d_gate || !d_logits || d_logits == logits || d_logits == d_gate) return DMOE_ERR_INVALID_ARG;
   if (misaligned4(logits) || misaligned4(expert_idx) || misaligned4(d_gate) || misaligned4(d_logits))
     return DMOE_ERR_INVALID_ARG;
   dmoe::DeviceInfo di;

@@ -629,7 +629,7 @@ typedef enum dmoe_scores { DMOE_SCORES_SOFTMAX = 0, DMOE_SCORES_SIGMOID = 1 } dm
  * nothing to its group's worth, comes after all others and, by its logit, has
  * the weight 0.  Where every chosen logit is minus infinity the weights are 0.
  *   logits [T, E] fp32, bias [E] fp32 or NULL (read)
- *   expert_idx [T, k] int32, gate_w [T, k] fp32 (written)
+ *   expert_idx [T, k] int32, gate_w [T, k] fp32 (written; they overlap nothing)
  * 1 <= E <= 1024, 1 <= groups <= 32 a divisor of E, 1 <= top_groups <= groups,
  * 1 <= k <= top_groups * E / groups. */
 dmoe_status dmoe_route_balanced(const float* logits, const float* bias, int T, int E, int k, int scores, int groups,
@@ -640,7 +640,8 @@ dmoe_status dmoe_route_balanced(const float* logits, const float* bias, int T, i
  * chosen set is locally constant, and the bias has no gradient).  expert_idx
  * [T, k] holds distinct experts; an entry outside [0, E) is left out and sets
  * DMOE_SITE_ROUTE_INDEX | DMOE_ERR_DEVICE.  scores, renormalize and scale as
- * in the forward call.  d_gate [T, k], d_logits [T, E] fp32 (written). */
+ * in the forward call.  d_gate [T, k], d_logits [T, E] fp32 (written; it
+ * overlaps nothing, d_gate of k = E experts neither). */
 dmoe_status dmoe_route_balanced_backward(const float* logits, const int32_t* expert_idx, const float* d_gate, int T,
                                          int E, int k, int scores, int renormalize, float scale, float* d_logits,
                                          dmoe_stream_t stream);

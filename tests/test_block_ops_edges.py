@@ -5,12 +5,13 @@ Sums of products are made exact, where that helps: whole numbers times a power o
 ordered or cut, so that what follows them is compared without a sum's error.
 """
 
+import ctypes
 import math
 
 import pytest
 import torch
 
-from test_block_ops import (BF, F32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_sandwich_backward,  # noqa: F401
+from test_block_ops import (BF, F32, I32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_sandwich_backward,  # noqa: F401
                             ref_scores, check_backward, route, weights, workspace)
 
 
@@ -173,6 +174,38 @@ def test_route_by_groups_whose_worth_passes_fp32(dm, T, E, k, groups, scores):
         ri, rw = ref_route(logits, bias, k, scores, groups, 1, True, 1.0)
         assert torch.equal(idx.long(), ri), sums
         close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
+
+
+def test_route_refuses_outputs_over_its_inputs_without_gpu():
+    from dropless_moe_block_gb300 import build
+    build.build()
+    import dropless_moe_block_gb300 as m
+    L = m.lib()
+    p = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(5)]
+    # logits, bias, T, E, k, scores, groups, top_groups, renormalize, scale, expert_idx, gate_w
+    assert L.dmoe_route_balanced(p[0], p[1], 4, 8, 8, 1, 1, 1, 1, 1.0, p[2], p[0], None) == 1
+    # logits, expert_idx, d_gate, T, E, k, scores, renormalize, scale, d_logits
+    assert L.dmoe_route_balanced_backward(p[0], p[1], p[2], 4, 8, 8, 1, 1, 1.0, p[0], None) == 1
+    assert L.dmoe_route_balanced_backward(p[0], p[1], p[2], 4, 8, 8, 1, 1, 1.0, p[2], None) == 1
+
+
+@pytest.mark.gpu
+def test_route_refuses_outputs_over_its_inputs(dm):
+    """With as many choices as experts the weights have the logits' shape, and the gradients one another's."""
+    T, E = 64, 8
+    logits, idx, w = randn(1, T, E, dtype=F32), empty(T, E, dtype=I32), empty(T, E, dtype=F32)
+    kept = logits.clone()
+    with pytest.raises(ValueError, match="gate_w must not overlap logits"):
+        dm.route_balanced(logits, E, idx, logits)
+    both = empty(T * E + T * 2 - 4, dtype=F32)
+    with pytest.raises(ValueError, match="gate_w must not overlap logits"):
+        dm.route_balanced(both[:T * E].view(T, E), 2, idx.view(-1)[:2 * T].view(T, 2), both[T * E - 4:].view(T, 2))
+    dm.route_balanced(logits, E, idx, w)
+    d = randn(2, T, E, dtype=F32)
+    for over in (d, logits):
+        with pytest.raises(ValueError, match="d_logits must not overlap"):
+            dm.route_balanced_backward(logits, idx, d, over)
+    assert torch.equal(logits, kept)
 
 
 # ----------------------------------------------------- norms around the block
