@@ -1314,7 +1314,9 @@ class SharedExpert:
     """Buffers and calls of a dense two-layer MLP that every token passes beside
     its routed experts: y = act(x . w1 + b1) . w2 + b2 + residual, the residual
     being what the routed experts gave.  w1 [d, F], w2 [F, d] bf16; b1 [F], b2
-    [d] bf16 or fp32, or None; act: "gelu" or "silu"."""
+    [d] bf16 or fp32, or None; act: "gelu" or "silu".  Gradients of biases that
+    the forward pass had none of are not computed: db1 and db2 (zeros at first)
+    stay as they were."""
 
     def __init__(self, T: int, d: int, F: int, act: str = "gelu", device="cuda"):
         if act not in ("gelu", "silu"):
@@ -1326,12 +1328,14 @@ class SharedExpert:
         self.dz = torch.empty(T, F, **bf)
         self.y, self.dx = torch.empty(T, d, **bf), torch.empty(T, d, **bf)
         self.dW1, self.dW2 = torch.empty(d, F, **bf), torch.empty(F, d, **bf)
-        self.db1, self.db2 = torch.empty(F, **f32), torch.empty(d, **f32)
+        self.db1, self.db2 = torch.zeros(F, **f32), torch.zeros(d, **f32)
+        self.biased = False, False  # whether the last forward pass had b1, and b2
         n = max(linear_workspace_size(T, d, F), linear_workspace_size(T, F, d),
                 linear_backward_workspace_size(T, d, F), linear_backward_workspace_size(T, F, d))
         self.ws = torch.empty(n, dtype=torch.uint8, device=device)
 
     def forward(self, x, w1, w2, b1=None, b2=None, residual=None):
+        self.biased = b1 is not None, b2 is not None
         linear(x, w1, self.a, self.ws, bias=b1, act=self.act, deriv=self.deriv)
         linear(self.a, w2, self.y, self.ws, bias=b2, residual=residual)
         return self.y
@@ -1339,8 +1343,9 @@ class SharedExpert:
     def backward(self, dy, x, w1, w2):
         """dx and, in dW1, dW2, db1 and db2, the weights' gradients (the
         residual's is dy)."""
-        linear_backward(dy, self.a, w2, self.dz, self.dW2, self.ws, dbias=self.db2, factor=self.deriv)
-        linear_backward(self.dz, x, w1, self.dx, self.dW1, self.ws, dbias=self.db1)
+        b1, b2 = self.biased
+        linear_backward(dy, self.a, w2, self.dz, self.dW2, self.ws, dbias=self.db2 if b2 else None, factor=self.deriv)
+        linear_backward(self.dz, x, w1, self.dx, self.dW1, self.ws, dbias=self.db1 if b1 else None)
         return self.dx
 
 

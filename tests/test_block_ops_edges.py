@@ -224,3 +224,27 @@ def test_gradient_of_a_gate_a_row_needs_no_workspace(dm, T):
     dm.sandwich_norm_backward(dy, u, h, a, b, ru, rh, got["du"], got["dx"], None, None, None, gate=gate, d_gate=got["gate"])
     ref, size = ref_sandwich_backward(dy, u, h, a, b, ru, rh, None, gate, 1.0)
     check_backward(got, ref, size, T)
+
+
+# ------------------------------------------------------ a block's other parts
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("has1,has2", [(False, False), (True, False), (False, True), (True, True)])
+def test_shared_expert_makes_the_gradients_of_biases_it_has(dm, has1, has2):
+    """One launch less for every bias that is not there, the other gradients bit for bit the same, and what was in db1 and db2 left
+    there."""
+    T, d, F = 70, 128, 520
+    x, dy = randn(1, T, d), randn(2, T, d)
+    w1, w2 = randn(3, d, F, scale=d ** -0.5), randn(4, F, d, scale=F ** -0.5)
+    full, s = dm.SharedExpert(T, d, F), dm.SharedExpert(T, d, F)
+    zero1, zero2 = torch.zeros(F, device="cuda"), torch.zeros(d, device="cuda")
+    y = full.forward(x, w1, w2, zero1, zero2)
+    n = launches(dm, lambda: full.backward(dy, x, w1, w2))
+    assert float(s.db1.abs().sum() + s.db2.abs().sum()) == 0.0
+    s.db1.fill_(7.0), s.db2.fill_(7.0)
+    assert torch.equal(s.forward(x, w1, w2, zero1 if has1 else None, zero2 if has2 else None), y)
+    assert launches(dm, lambda: s.backward(dy, x, w1, w2)) == n - (not has1) - (not has2)
+    for name in ("dx", "dW1", "dW2"):
+        assert torch.equal(getattr(s, name), getattr(full, name)), name
+    assert torch.equal(s.db1, full.db1) if has1 else bool((s.db1 == 7.0).all())
+    assert torch.equal(s.db2, full.db2) if has2 else bool((s.db2 == 7.0).all())
