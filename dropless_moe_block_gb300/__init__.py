@@ -1089,12 +1089,16 @@ class DMoELayer:
         """With ``w_gate`` ([E, d] bf16) the layer computes the router logits
         itself (``gate_route_topk``, into ``self.gate_logits``) and ``logits``
         is not read; the gradient of the gate's own GEMM is the caller's
-        (``self.d_logits`` . w_gate into dx, d_logits^T . x for w_gate)."""
+        (``self.d_logits`` . w_gate into dx, d_logits^T . x for w_gate).  The
+        layer's own gate serves up to 256 experts; logits of more are the
+        caller's to make."""
         T, d, E, F, k = self.T, self.d, self.E, self.F, self.k
         swi = self.act == "swiglu"
         if w_gate is not None:
             if self.front != "separate":
                 raise ValueError("a layer with its own gate runs the separate front")
+            if E > 256:
+                raise ValueError(f"a layer's own gate serves up to 256 experts, not {E}: give it logits")
             logits = self.gate_logits
         self._logits = logits  # the router backward reads them
         if self.front != "separate":
@@ -1108,10 +1112,13 @@ class DMoELayer:
                                                                        self.tokens_per_expert)))
         else:
             front = []
-            if w_gate is not None:  # (of a balanced layer it makes the logits alone; its choice is written over)
-                front.append(("gate_route_topk", lambda: gate_route_topk(x, w_gate, k, self.renormalize,
-                                                                         self.gate_logits, self.expert_idx,
-                                                                         self.gate_w)))
+            if w_gate is not None:
+                # of a balanced layer it makes the logits alone: one choice a
+                # token, the fewest there are, is written over by the router's
+                n = k if self.balanced is None else 1
+                idx, gate = self.expert_idx.view(-1)[:T * n].view(T, n), self.gate_w.view(-1)[:T * n].view(T, n)
+                front.append(("gate_route_topk", lambda: gate_route_topk(x, w_gate, n, self.renormalize,
+                                                                         self.gate_logits, idx, gate)))
             if self.balanced is not None:
                 front.append(("route_balanced", lambda: route_balanced(logits, k, self.expert_idx, self.gate_w,
                                                                        bias=self.route_bias,

@@ -248,3 +248,38 @@ def test_shared_expert_makes_the_gradients_of_biases_it_has(dm, has1, has2):
         assert torch.equal(getattr(s, name), getattr(full, name)), name
     assert torch.equal(s.db1, full.db1) if has1 else bool((s.db1 == 7.0).all())
     assert torch.equal(s.db2, full.db2) if has2 else bool((s.db2 == 7.0).all())
+
+
+def test_layers_own_gate_and_its_limit(monkeypatch):
+    from dropless_moe_block_gb300 import build
+    build.build()
+    import dropless_moe_block_gb300 as m
+    big = m.DMoELayer(64, 128, 320, 128, 2, device="cpu", balanced={})
+    with pytest.raises(ValueError, match="256 experts, not 320"):
+        big.forward_calls(None, None, None, None, w_gate=object())
+    assert [n for n, _ in big.forward_calls(None, None, None, None)][:2] == ["route_balanced", "permute_pad"]
+    # a balanced layer's gate makes logits: it chooses no more than it has to
+    seen = []
+    monkeypatch.setattr(m, "gate_route_topk", lambda x, w, k, renorm, logits, idx, gate: seen.append((k, idx.shape, gate.shape)))
+    for balanced, k in (({}, 1), (None, 6)):
+        layer = m.DMoELayer(64, 128, 16, 128, 6, device="cpu", balanced=balanced)
+        dict(layer.forward_calls(None, None, None, None, w_gate=object()))["gate_route_topk"]()
+        assert seen.pop() == (k, (64, k), (64, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(8, 3), (64, 8)])
+def test_balanced_layer_with_its_own_gate(dm, E, k):
+    """The choice, weights and output of the same layer given the logits that the gate made."""
+    T, d, F = 300, 128, 128
+    x, wg = randn(1, T, d), randn(2, E, d, scale=d ** -0.5)
+    w1, w2 = randn(3, d, E * F, scale=d ** -0.5), randn(4, E * F, d, scale=F ** -0.5)
+    own, given = (dm.DMoELayer(T, d, E, F, k, "gelu", True, balanced={"scores": "sigmoid", "groups": 4, "top_groups": 2}) for _ in "ab")
+    for layer in (own, given):
+        layer.route_bias.copy_(torch.linspace(-0.2, 0.2, E, device="cuda"))
+    own.forward(x, None, w1, w2, w_gate=wg)
+    z = x.double() @ wg.double().t()
+    close(own.gate_logits, z, 2 * d * U32 * (x.double().abs() @ wg.double().abs().t()), "logits")
+    given.forward(x, own.gate_logits.clone(), w1, w2)
+    for name in ("expert_idx", "gate_w", "tokens_per_expert", "y"):
+        assert torch.equal(getattr(own, name), getattr(given, name)), name
