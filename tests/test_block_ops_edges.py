@@ -11,6 +11,7 @@ import math
 import pytest
 import torch
 
+import test_block_ops as ops
 from test_block_ops import (BF, F32, I32, U16, U32, clean, close, dm, empty, randn, ref_act, ref_route, ref_sandwich_backward,  # noqa: F401
                             ref_scores, check_backward, route, weights, workspace)
 
@@ -160,6 +161,60 @@ def test_route_with_experts_ruled_out_and_forced(dm, T, E, k, groups, top_groups
         close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
 
 
+def c_of(logits, bias, scores):
+    """What experts are chosen by, in 64 bits."""
+    z = clean(logits)
+    c = ref_scores(z, scores) + bias.double()
+    return torch.where((z == -math.inf) | torch.isnan(c), torch.full_like(c, -math.inf), c)
+
+
+def check_choice(logits, bias, idx, w, k, scores, groups, top_groups):
+    """A choice whose candidates lie as close as 64-bit roundings: not the reference's order, but its values, and the weights of the
+    very choice.  A 64-bit score is off by some 1e-16 of values below 1, a softmax's by 1e-15."""
+    T, E = logits.shape
+    i, c = idx.long(), c_of(logits, bias, scores)
+    assert int(i.min()) >= 0 and int(i.max()) < E
+    assert bool((i.sort(1).values.diff(dim=1) > 0).all())  # distinct
+    got = c.gather(1, i)
+    assert float(got.diff(dim=1).max()) < 1e-14  # descending
+    settled = torch.ones(T, dtype=torch.bool, device="cuda")
+    if top_groups < groups:
+        worth = c.view(T, groups, -1).topk(2, 2).values.sum(2)
+        order = worth.sort(dim=1, descending=True).values
+        least = order[:, top_groups - 1:top_groups]
+        assert bool((worth.gather(1, i // (E // groups)) >= least - 4e-14).all())  # of groups that may stay
+        settled = (least - order[:, top_groups:top_groups + 1])[:, 0] > 4e-14
+    ri, _ = ref_route(logits, bias, k, scores, groups, top_groups, True, 1.0)
+    assert float((got - c.gather(1, ri)).abs()[settled].max()) < 1e-14
+    s = ref_scores(clean(logits), scores).gather(1, i)
+    close(w, s / s.sum(1, keepdim=True), 400 * U32 * s / s.sum(1, keepdim=True), "gate_w")
+    return int(settled.sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,groups,top_groups", [(300, 1, 1), (300, 8, 3), (8300, 1, 1), (8300, 8, 3)])
+def test_route_of_rows_that_the_bias_levels(dm, scores, T, groups, top_groups):
+    """Choices within fp32's step of one another in every row: all of them are the 64 bits' to make."""
+    E, k = 256, 8
+    row = randn(1, 1, E, dtype=F32)
+    bias = (0.5 - ref_scores(row.double(), scores)[0]).to(F32)
+    logits = row + randn(2, T, E, scale=1e-7, dtype=F32)
+    c = c_of(logits, bias, scores)
+    assert float((c.amax(1) - c.amin(1)).max()) < 1e-6
+    idx, w = route(dm, logits, k, bias=bias, scores=scores, groups=groups, top_groups=top_groups)
+    assert check_choice(logits, bias, idx, w, k, scores, groups, top_groups) > T // 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [(9000, 96, 6, 4, 2), (9000, 160, 8, 5, 3), (6000, 512, 8, 16, 4), (6000, 512, 8, 1, 1),
+                                                     (4000, 1024, 33, 32, 5)])
+def test_route_of_several_tokens_a_warp(dm, T, E, k, groups, top_groups, scores):
+    """Warps that walk from token to token, with the groups' scores of one where the last one's were."""
+    ops.test_route(dm, T, E, k, groups, top_groups, scores, True, True)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k,groups", [(5, 8, 1, 4), (300, 96, 3, 4), (40, 64, 1, 2), (9000, 256, 8, 8), (9000, 64, 8, 2)])
@@ -224,6 +279,15 @@ def test_gradient_of_a_gate_a_row_needs_no_workspace(dm, T):
     dm.sandwich_norm_backward(dy, u, h, a, b, ru, rh, got["du"], got["dx"], None, None, None, gate=gate, d_gate=got["gate"])
     ref, size = ref_sandwich_backward(dy, u, h, a, b, ru, rh, None, gate, 1.0)
     check_backward(got, ref, size, T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(1000, 8200), (500, 12808), (700, 16384)])
+@pytest.mark.parametrize("kind,wf32,scale,stream", [("row", True, 0.7, True), ("one", False, 1.0, False)])
+def test_sandwich_norm_of_many_wide_rows(dm, T, d, kind, wf32, scale, stream):
+    """Four vectors a thread, several rows a block: its ring filled again and again, of one stage at 16384 columns."""
+    ops.test_sandwich_norm(dm, T, d, kind, wf32, scale)
+    ops.test_sandwich_norm_backward(dm, T, d, kind, wf32, scale, stream)
 
 
 # ------------------------------------------------------ a block's other parts
