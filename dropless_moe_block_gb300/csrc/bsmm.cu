@@ -55,6 +55,8 @@ namespace {
 
 using dmoe::tc::smem_u32;
 using namespace dmoe::act;
+using dmoe::f2_fma;
+using dmoe::f2_mul;
 
 enum Op : int { OP_SDD = 0, OP_DSD = 1, OP_DSDT = 2, OP_DSTD = 3, OP_DSTDT = 4 };
 
@@ -466,24 +468,6 @@ __device__ __forceinline__ void load_slice(const Params& p, const Tile& tl, int 
       for (int j = 0; j < ATOMS; ++j) ld(sb + j * ATOM_BYTES, &p.map_b, scol(j0 + j), srow(j0 + j));
     }
   }
-}
-
-// Packed two-lane fp32 arithmetic of the sm_100 family: one instruction
-// yields two independent results, each rounded as the scalar operation.
-__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-
-__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
