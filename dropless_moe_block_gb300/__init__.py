@@ -757,7 +757,8 @@ def route_balanced(logits, k: int, expert_idx, gate_w, bias=None, scores: str = 
     groups of neighbouring experts whose two best choices sum to most.
     ``gate_w``: the scores of the chosen without the bias, divided by their sum
     (``renormalize``), times ``scale``.  Ties go to the lower expert; candidates
-    that fp32 cannot tell apart are compared in 64 bits."""
+    that fp32 cannot tell apart are compared in 64 bits, which are more the larger
+    a finite bias is: minus infinity rules an expert out at no cost."""
     T, E = logits.shape
     dev = _device(logits, "logits")
     _is(logits, dev, torch.float32, "logits", (T, E))
@@ -912,7 +913,7 @@ def linear_workspace_size(M: int, K: int, N: int) -> int:
 
 def linear(x, w, y, ws, bias=None, act: str = "none", deriv=None, residual=None, stream=None):
     """y = act(x . w + bias) + residual with w [K, N] as an expert's weights lie;
-    act: "none", "gelu" (exact) or "silu".  ``deriv`` (bf16 [M, N]) receives the
+    act: "none", "gelu" (erf) or "silu".  ``deriv`` (bf16 [M, N]) receives the
     activation's derivative, all that the backward needs of the sums.  ``x`` and
     ``residual`` may be row slices of wider tensors; ``y`` may be ``residual``.
     ``ws``: uint8, linear_workspace_size() bytes."""

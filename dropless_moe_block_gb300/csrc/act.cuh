@@ -23,7 +23,8 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // The exact (erf) GELU, gelu(x) = x Phi(x), and its derivative
 // gelu'(x) = Phi(x) + x phi(x), of two accumulator values with packed
 // arithmetic.  Phi comes from the erfc approximation of Abramowitz & Stegun,
-// Handbook of Mathematical Functions, formula 7.1.26 (|error| <= 1.5e-7):
+// Handbook of Mathematical Functions, formula 7.1.26 (|error| <= 1.5e-7; of
+// Phi(x) itself 0.05% at x = -4, 0.36% at -6, 1% at -8):
 //   erfc(z) ~= t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-z^2),
 //   t = 1 / (1 + p z),  z = |x| / sqrt(2) >= 0,
 // with the coefficients halved so that the product is Phi(-|x|) directly.

@@ -137,6 +137,22 @@ def test_linear_backward_onto_its_factor(dm, M, K, N):
     assert bool((guard == 0x5a).all())
 
 
+def test_linear_widths_end_at_2_to_the_20_without_gpu():
+    from dropless_moe_block_gb300 import build
+    build.build()
+    import dropless_moe_block_gb300 as m
+    L, most = m.lib(), 1 << 20
+    p = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(9)]
+    for K, N in ((most + 8, 64), (64, most + 8)):
+        assert m.linear_workspace_size(4, K, N) == 0 and m.linear_backward_workspace_size(4, K, N) == 0
+        # x, ldx, w, bias, f32, act, residual, ldr, M, K, N, y, deriv, ws, ws_bytes
+        assert L.dmoe_linear(p[0], K, p[1], None, 0, 0, None, 0, 4, K, N, p[2], None, p[3], 1 << 30, None) == 1
+        # dy, lddy, deriv, x, ldx, w, factor, M, K, N, dx, dw, f32, dbias, ws, ws_bytes
+        assert L.dmoe_linear_backward(p[0], N, None, p[1], K, p[2], None, 4, K, N, p[3], p[4], 0, None, p[5], 1 << 30, None) == 1
+    for K, N in ((most, 64), (64, most)):
+        assert m.linear_workspace_size(4, K, N) > 0 and m.linear_backward_workspace_size(4, K, N) > 0
+
+
 # -------------------------------------------------------------------- routing
 
 @pytest.mark.gpu
