@@ -6,13 +6,15 @@
 //   a group's worth: its two largest c summed; the best groups stay
 //   of their experts the k largest c;  w = s (/ their sum) * scale
 //
-// One warp per token, lane l with experts l, l + 32, ....  16381 tokens of 256
-// experts are 17 MB, 3 us of HBM, and take 25: what bounds it are some 1080
-// instructions a token (70% of the issue slots while an SM is busy; 21 us), and
-// behind them the last of the tokens decided twice.  So the choice works on
-// 31-bit keys, a choice's place in its range and under it the
-// expert's register, such that one integer reduction over the warp finds the
-// best and where it lies.
+// A warp per token, lane l with experts l, l + 32, ..., for any number of
+// experts; of 64, 128 or 256, and where there are tokens enough, four tokens a
+// warp (route_eighths_kernel).  16381 tokens of 256 experts in groups are 17 MB,
+// 3 us of HBM, and take four a warp 19 to 24: 450 instructions a token, whose
+// latency bounds it, and behind them the last of the tokens decided twice.  A
+// warp a token takes some 1080, and is bound by them (70% of the issue slots
+// while an SM is busy, 25 to 27 us).  So the choice works on 31-bit keys, a
+// choice's place in its range and under it the expert's register, or number,
+// such that one integer reduction finds the best and where it lies.
 //
 // Which experts are chosen must not hang on how the keys, or fp32, round: a
 // key is known to `tol` steps, and a token where two neighbours of the
