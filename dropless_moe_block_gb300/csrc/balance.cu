@@ -80,10 +80,16 @@ __device__ __forceinline__ float clean(float z) { return fminf(fmaxf(z, -INFINIT
 __device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
 // What the chosen scores are proportional to, `top` being the largest chosen
-// logit: scores that would vanish in fp32 (all chosen sigmoids below e^-30,
-// where they are exponentials to 13 digits) keep their ratios.
+// logit: scores that would vanish in fp32 keep their ratios.  Where all chosen
+// sigmoids lie below e^-30 they are exponentials to 13 digits; above it they are
+// taken 2^48 times, which their quotients do not show, and those that fp32 holds
+// no longer in full (below e^-80) from the square of their root.
 __device__ __forceinline__ float proportion(float z, float top, bool sig) {
-  return sig && top >= -30.f ? sigmoid(z) : expf(z - top);
+  if (!sig || top < -30.f) return expf(z - top);
+  constexpr float up = 281474976710656.f;  // 2^48
+  if (z >= -80.f) return sigmoid(z) * up;
+  const float root = expf(0.5f * z);
+  return root * up * root;
 }
 
 struct Choice {

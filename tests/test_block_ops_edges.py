@@ -247,6 +247,27 @@ def test_route_by_groups_whose_worth_passes_fp32(dm, T, E, k, groups, scores):
         close(w, rw, 400 * U32 * rw + 2.0 ** -126, "gate_w")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(600, 64), (600, 40), (8200, 64)])
+def test_renormalised_sigmoids_far_from_one_another(dm, T, E):
+    """Chosen sigmoids whose quotients fp32 holds while the smaller ones themselves are below what it holds in full."""
+    k = 6
+    logits = torch.full((T, E), -500.0, device="cuda")
+    top = torch.linspace(-29.9, 3.0, T, device="cuda")
+    logits[:, :k] = top[:, None] - torch.tensor([0.0, 30.0, 55.0, 62.0, 70.0, 80.0], device="cuda")
+    idx, w = route(dm, logits, k, scores="sigmoid")
+    ri, rw = ref_route(logits, None, k, "sigmoid", 1, 1, True, 1.0)
+    assert torch.equal(idx.long(), ri)
+    # exponentials of arguments without a rounding (2 ulp; twice the root's), a sum and a quotient
+    close(w, rw, 40 * U32 * rw + 2.0 ** -126, "gate_w")
+    d = randn(1, T, k, dtype=F32)
+    dl = empty(T, E, dtype=F32)
+    dm.route_balanced_backward(logits, idx, d, dl, scores="sigmoid")
+    ref = ops.ref_route_backward(logits, ri, d, "sigmoid", True, 1.0)
+    size = torch.zeros(T, E, device="cuda", dtype=torch.float64).scatter_(1, ri, rw * 2 * d.double().abs().amax(1, keepdim=True))
+    close(dl, ref, 100 * U32 * size + 2.0 ** -126, "d_logits")
+
+
 def test_route_refuses_outputs_over_its_inputs_without_gpu():
     from dropless_moe_block_gb300 import build
     build.build()
