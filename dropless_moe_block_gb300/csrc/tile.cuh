@@ -150,7 +150,8 @@ __device__ __forceinline__ void write_rows32(uint32_t slab, int lane, const floa
 // read), but one that the compiler may move: held where they stand, the loads
 // of join_row32 wait behind the accumulator's and the last stores (8192 x 512 x
 // 2048 onto a residual 54 us, 26 with these).  So it is for values that the
-// reader alone overwrites, by stores that hang on what it read.
+// reader alone overwrites, by stores that hang on what it read, and behind a
+// branch on the wait for what came before, which it does not pass.
 __device__ __forceinline__ uint4 ld_own(const uint4* a) {
   uint4 q;
   asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
